@@ -47,8 +47,20 @@ class DbfMbokLayerC(ctypes.Structure):
                 ("w_packed", ctypes.c_void_p), ("s_in", ctypes.c_void_p), ("s_out", ctypes.c_void_p)]
 
 
+class DbfMx4LayerC(ctypes.Structure):
+    """dbf_mx4_layer of dbf.h."""
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class DbfAct8C(ctypes.Structure):
+    """dbf_act8 of dbf.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _LP = ctypes.POINTER(DbfLayerC)
+_MP = ctypes.POINTER(DbfMx4LayerC)
+_AP = ctypes.POINTER(DbfAct8C)
 _SIGS = {
     "dbf_packed_bytes": (_sz, [_i64, _i64]),
     "dbf_pack_signs": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _sz, _vp, _vp]),
@@ -85,6 +97,19 @@ _SIGS = {
     "dbf_debug_noalloc_header": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_int32)]),
     "dbf_debug_fused_schedule": (ctypes.c_int, [_LP, _i64, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
                                                 ctypes.POINTER(ctypes.c_double)]),
+    "dbf_mx4_code_bytes": (_sz, [_i64, _i64]),
+    "dbf_mx4_scale_bytes": (_sz, [_i64, _i64]),
+    "dbf_mx4_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _sz, _vp, _sz, _vp, _vp]),
+    "dbf_mx4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, ctypes.c_int, _vp]),
+    "dbf_mx4_workspace_bytes": (_sz, [_MP, _i64]),
+    "dbf_mx4_forward": (ctypes.c_int, [_MP, _vp, ctypes.c_int, _vp, ctypes.c_int, _i64, ctypes.c_int, _vp, _sz, _vp]),
+    "dbf_act8_code_bytes": (_sz, [_i64, _i64]),
+    "dbf_act8_scale_bytes": (_sz, [_i64, _i64]),
+    "dbf_act8_save": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _AP, _vp, _vp]),
+    "dbf_act8_load": (ctypes.c_int, [_AP, _i64, _i64, _vp, ctypes.c_int, _vp]),
+    "dbf_mx4_gated_workspace_bytes": (_sz, [_MP, _MP, _i64]),
+    "dbf_mx4_gated_forward": (ctypes.c_int, [_MP, _MP, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp,
+                                             ctypes.c_int, _AP, _AP, _i64, ctypes.c_int, _vp, _sz, _vp]),
     "dbf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dbf_version": (ctypes.c_char_p, []),
 }
@@ -541,3 +566,228 @@ def forward_segmented(table: AdapterTable, seg_offsets: torch.Tensor, seg_adapte
                                       _flags(accumulate, False), _ptr(ws), ws.numel(), _ptr(status),
                                       _stream(stream)), "dbf_forward_segmented")
     return y
+
+
+# ---- 4-bit base layer, gated block, 8-bit activations -------------------------
+# These take the device from their tensors: the call runs with that device
+# current and, without an explicit stream, on its current stream.
+
+_GATES = {"silu": 0, "gelu": 1}
+
+
+class _On:
+    """Makes the tensors' device current for a call and gives its stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        self.dev, self.stream, self.old = t.device.index, stream, None
+
+    def __enter__(self) -> int:
+        cur = torch.cuda.current_device()
+        if cur != self.dev:
+            self.old = cur
+            torch.cuda.set_device(self.dev)
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.old is not None:
+            torch.cuda.set_device(self.old)
+
+
+def _need(t: Optional[torch.Tensor], name: str, shape, dtypes, like: torch.Tensor) -> None:
+    """A tensor argument as the C ABI reads it: contiguous, of this shape and
+    type, on the same device."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} tensor of {[str(d) for d in dtypes]} on "
+                         f"{like.device}, got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+
+
+_ACT = (torch.float32, torch.bfloat16)
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_U8 = (torch.uint8,)
+
+
+def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
+    """A workspace of one call: only its header has to be zero."""
+    ws = torch.empty(max(int(nbytes), WS_HEADER_BYTES), dtype=torch.uint8, device=like.device)
+    ws[:WS_HEADER_BYTES].zero_()
+    return ws
+
+
+def _mx4_shapes(rows: int, k: int):
+    nb = -(-k // 32)
+    return (rows, nb * 16), (-(-rows // 128), -(-nb // 4), 32, 4, 4)
+
+
+def mx4_quantize(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Microscaled 4-bit form of a rows x k float tensor (dbf_mx4_quantize).
+
+    Returns (codes [rows, ceil(k/32) * 16], scales [row tiles, block tiles, 32, 4, 4]), uint8."""
+    rows, k = src.shape
+    src = src.contiguous()
+    _need(src, "src", (rows, k), _FLOATS, src)
+    cs, ss = _mx4_shapes(rows, k)
+    with _On(src, stream) as s:
+        codes = torch.empty(cs, dtype=torch.uint8, device=src.device) if codes is None else codes
+        scales = torch.empty(ss, dtype=torch.uint8, device=src.device) if scales is None else scales
+        _need(codes, "codes", cs, _U8, src)
+        _need(scales, "scales", ss, _U8, src)
+        _check(_lib.dbf_mx4_quantize(_ptr(src), _DT[src.dtype], rows, k, _ptr(codes), codes.numel(), _ptr(scales),
+                                     scales.numel(), _ptr(status), s), "dbf_mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, out: Optional[torch.Tensor] = None,
+                   dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The rows x k values that 4-bit codes and scales stand for (dbf_mx4_dequantize)."""
+    cs, ss = _mx4_shapes(rows, k)
+    _need(codes, "codes", cs, _U8, codes)
+    _need(scales, "scales", ss, _U8, codes)
+    with _On(codes, stream) as s:
+        out = torch.empty((rows, k), dtype=dtype, device=codes.device) if out is None else out
+        _need(out, "out", (rows, k), _FLOATS, codes)
+        _check(_lib.dbf_mx4_dequantize(_ptr(codes), _ptr(scales), rows, k, _ptr(out), _DT[out.dtype], s),
+               "dbf_mx4_dequantize")
+    return out
+
+
+@dataclass
+class Mx4Layer:
+    """Device-resident 4-bit layer W [N, M]: codes [N, ceil(M/32) * 16] and
+    tiled scales [ceil(N/128), ceil(M/128), 32, 4, 4], uint8."""
+    M: int
+    N: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def quantize(W: torch.Tensor, stream=None) -> "Mx4Layer":
+        """The 4-bit layer of a dense weight W [N, M]."""
+        return Mx4Layer(W.shape[1], W.shape[0], *mx4_quantize(W, stream=stream))
+
+    def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        return mx4_dequantize(self.codes, self.scales, self.N, self.M, dtype=dtype, stream=stream)
+
+    def descriptor(self) -> DbfMx4LayerC:
+        cs, ss = _mx4_shapes(self.N, self.M)
+        _need(self.codes, "codes", cs, _U8, self.codes)
+        _need(self.scales, "scales", ss, _U8, self.codes)
+        return DbfMx4LayerC(self.M, self.N, _ptr(self.codes), _ptr(self.scales))
+
+
+def mx4_workspace_bytes(layer: Mx4Layer, T: int) -> int:
+    d = layer.descriptor()
+    return int(_lib.dbf_mx4_workspace_bytes(ctypes.byref(d), T))
+
+
+def mx4_forward(layer: Mx4Layer, x: torch.Tensor, y: Optional[torch.Tensor] = None, accumulate: bool = False,
+                ws: Optional[torch.Tensor] = None, y_dtype: Optional[torch.dtype] = None, static_weights: bool = False,
+                stream=None) -> torch.Tensor:
+    """y = [acc] y + W q(x) (dbf_mx4_forward). x: [T, M] float32/bfloat16."""
+    T = x.shape[0]
+    _need(x, "x", (T, layer.M), _ACT, layer.codes)
+    d = layer.descriptor()
+    with _On(x, stream) as s:
+        if y is None:
+            if accumulate:
+                raise ValueError("accumulate needs y")
+            y = torch.empty((T, layer.N), dtype=y_dtype or x.dtype, device=x.device)
+        _need(y, "y", (T, layer.N), _ACT, x)
+        if ws is None:
+            ws = _scratch(_lib.dbf_mx4_workspace_bytes(ctypes.byref(d), T), x)
+        _check(_lib.dbf_mx4_forward(ctypes.byref(d), _ptr(x), _DT[x.dtype], _ptr(y), _DT[y.dtype], T,
+                                    _flags(accumulate, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_forward")
+    return y
+
+
+@dataclass
+class Act8:
+    """An activation kept in 8 bits: codes [rows, ceil(cols/32) * 32] and
+    scales [ceil(cols/32), rows], uint8."""
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "Act8":
+        nb = -(-cols // 32)
+        return Act8(rows, cols, torch.empty((rows, nb * 32), dtype=torch.uint8, device=device),
+                    torch.empty((nb, rows), dtype=torch.uint8, device=device))
+
+    def descriptor(self) -> DbfAct8C:
+        nb = -(-self.cols // 32)
+        _need(self.codes, "codes", (self.rows, nb * 32), _U8, self.codes)
+        _need(self.scales, "scales", (nb, self.rows), _U8, self.codes)
+        return DbfAct8C(_ptr(self.codes), _ptr(self.scales))
+
+
+def act8_save(src: torch.Tensor, out: Optional[Act8] = None, status: Optional[torch.Tensor] = None, stream=None) -> Act8:
+    """Keep a rows x cols float tensor in 8 bits (dbf_act8_save)."""
+    rows, cols = src.shape
+    src = src.contiguous()
+    _need(src, "src", (rows, cols), _FLOATS, src)
+    with _On(src, stream) as s:
+        out = Act8.empty(rows, cols, src.device) if out is None else out
+        if (out.rows, out.cols) != (rows, cols) or out.codes.device != src.device:
+            raise ValueError("out: another shape or device than src")
+        d = out.descriptor()
+        _check(_lib.dbf_act8_save(_ptr(src), _DT[src.dtype], rows, cols, ctypes.byref(d), _ptr(status), s), "dbf_act8_save")
+    return out
+
+
+def act8_load(a: Act8, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values an Act8 stands for (dbf_act8_load)."""
+    with _On(a.codes, stream) as s:
+        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.codes.device) if out is None else out
+        _need(out, "out", (a.rows, a.cols), _FLOATS, a.codes)
+        d = a.descriptor()
+        _check(_lib.dbf_act8_load(ctypes.byref(d), a.rows, a.cols, _ptr(out), _DT[out.dtype], s), "dbf_act8_load")
+    return out
+
+
+def _saved(a: Optional[Act8], T: int, N: int, like: torch.Tensor):
+    if a is None:
+        return None
+    if (a.rows, a.cols) != (T, N) or a.codes.device != like.device:
+        raise ValueError(f"saved activation: expected {(T, N)} on {like.device}, got {(a.rows, a.cols)} on {a.codes.device}")
+    return a.descriptor()
+
+
+def mx4_gated_workspace_bytes(gate: Mx4Layer, up: Mx4Layer, T: int) -> int:
+    dg, du = gate.descriptor(), up.descriptor()
+    return int(_lib.dbf_mx4_gated_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T))
+
+
+def mx4_gated_forward(gate: Mx4Layer, up: Mx4Layer, x: torch.Tensor, h: Optional[torch.Tensor] = None, act: str = "silu",
+                      g_add: Optional[torch.Tensor] = None, u_add: Optional[torch.Tensor] = None,
+                      save: Optional[Tuple[Act8, Act8]] = None, ws: Optional[torch.Tensor] = None,
+                      h_dtype: Optional[torch.dtype] = None, static_weights: bool = False, stream=None) -> torch.Tensor:
+    """h = act(Wg q(x) [+ g_add]) . (Wu q(x) [+ u_add]) (dbf_mx4_gated_forward).
+
+    act: "silu" or "gelu" (tanh form). g_add, u_add: [T, N] of one type, e.g. an
+    adapter's branches. save: (Act8, Act8) [T, N] that receive g and u for
+    mx4_gated_backward."""
+    T, N = x.shape[0], gate.N
+    _need(x, "x", (T, gate.M), _ACT, gate.codes)
+    _need(up.codes, "up.codes", gate.codes.shape, _U8, x)
+    _need(g_add, "g_add", (T, N), _ACT, x)
+    _need(u_add, "u_add", (T, N), _ACT if g_add is None else (g_add.dtype,), x)
+    dg, du = gate.descriptor(), up.descriptor()
+    sg, su = (_saved(a, T, N, x) for a in (save or (None, None)))
+    add = g_add if g_add is not None else u_add
+    with _On(x, stream) as s:
+        h = torch.empty((T, N), dtype=h_dtype or x.dtype, device=x.device) if h is None else h
+        _need(h, "h", (T, N), _ACT, x)
+        if ws is None:
+            ws = _scratch(_lib.dbf_mx4_gated_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T), x)
+        _check(_lib.dbf_mx4_gated_forward(ctypes.byref(dg), ctypes.byref(du), _GATES[act], _ptr(x), _DT[x.dtype], _ptr(g_add),
+                                          _ptr(u_add), F32 if add is None else _DT[add.dtype], _ptr(h), _DT[h.dtype],
+                                          sg and ctypes.byref(sg), su and ctypes.byref(su), T, _flags(False, static_weights),
+                                          _ptr(ws), ws.numel(), s), "dbf_mx4_gated_forward")
+    return h

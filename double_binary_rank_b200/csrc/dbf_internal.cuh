@@ -145,6 +145,25 @@ cudaError_t gemm_backward(const dbf_layer &L, const uint32_t *b1t, const uint32_
                           float *dalpha, float *dbeta, float *dgamma, float *db1, float *db2,
                           int flags, void *ws, cudaStream_t s);
 
+// ---- 4-bit base layer and 8-bit activations (dbf_mx_*.cu)
+namespace mx {
+struct Product;
+}
+bool mx_size_ok(int64_t rows, int64_t k);
+cudaError_t launch_quantize4(const void *src, dbf_dtype dt, int64_t rows, int64_t k, uint8_t *codes, uint8_t *scales,
+                             int32_t *status, cudaStream_t s);
+cudaError_t launch_dequantize4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
+                               dbf_dtype dt, cudaStream_t s);
+cudaError_t launch_act8_save(const void *src, dbf_dtype dt, int64_t rows, int64_t k, uint8_t *codes, uint8_t *scales,
+                             int32_t *status, cudaStream_t s);
+cudaError_t launch_act8_load(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
+                             dbf_dtype dt, cudaStream_t s);
+// products: mats 1 (y = W q(x)) or 2 (the gated block)
+bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats);
+cudaError_t mx_decode(const mx::Product &c, cudaStream_t s);
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats);
+cudaError_t mx_gemm(const mx::Product &c, cudaStream_t s);
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace dbf

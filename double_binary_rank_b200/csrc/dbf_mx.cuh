@@ -1,0 +1,201 @@
+// Microscaled formats shared by the 4-bit base layer and the 8-bit
+// activations: block scales, conversions, layouts.
+//
+// A row is cut into blocks of 32 columns. Each block holds one scale 2^s,
+// stored as the byte s + 127 (E8M0; 255 is NaN and marks a block that held a
+// NaN or an infinity), and 32 codes of the block's values divided by 2^s:
+//   4 bits, E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+//       s = floor(log2 amax) - 2, so amax / 2^s lies in [4, 8) and what is
+//       above 6 saturates;
+//   8 bits, E4M3: up to 448; s the smallest with amax <= 448 * 2^s, so
+//       nothing saturates.
+// Both s are clamped to [-127, 127]. Dividing by a power of two is exact, so
+// the one rounding is that to the code (nearest, ties to even).
+#pragma once
+
+#include "dbf_internal.cuh"
+
+namespace dbf {
+namespace mx {
+
+constexpr int kBlock = 32;
+
+__host__ __device__ inline int64_t blocks(int64_t k) { return (k + kBlock - 1) / kBlock; }
+// bytes of one row of 4-bit codes: whole blocks, 16 bytes each
+__host__ __device__ inline int64_t code_pitch(int64_t k) { return blocks(k) * 16; }
+// 4-bit scales lie in tiles of 128 rows x 4 blocks (512 bytes), tiles of one
+// row tile side by side: the order in which tcgen05.cp brings them into
+// tensor memory, so a tile of them is one contiguous copy.
+__host__ __device__ inline int64_t scale_tiles(int64_t k) { return (blocks(k) + 3) / 4; }
+__host__ __device__ inline int64_t scale_at(int64_t row, int64_t block, int64_t tiles)
+{
+    return ((row >> 7) * tiles + (block >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (block & 3);
+}
+
+// Largest finite magnitude's bits in, scale byte out; NaN and infinity give 255.
+__device__ __forceinline__ uint32_t scale_byte4(uint32_t amax_bits)
+{
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+__device__ __forceinline__ uint32_t scale_byte8(uint32_t amax_bits)
+{
+    const uint32_t e = amax_bits >> 23;
+    if (e == 255u) return 255u;
+    const uint32_t up = (amax_bits & 0x7FFFFFu) > 0x600000u ? 1u : 0u;   // above 1.75 * 2^e = 448 * 2^(e - 8)
+    return e + up > 8u ? e + up - 8u : 0u;
+}
+// 2^-s of a scale byte below 254, exact (255 gives 0: the block's codes are 0)
+__device__ __forceinline__ float inv_scale(uint32_t b) { return b == 255u ? 0.0f : __uint_as_float((254u - b) << 23); }
+// 2^s; NaN for 255
+__device__ __forceinline__ float scale_value(uint32_t b)
+{
+    return __uint_as_float(b == 255u ? 0x7FC00000u : (b ? b << 23 : 0x00400000u));
+}
+
+// Eight values to eight E2M1 codes, v[0] in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight E2M1 codes to their values (exact in fp16, then fp32).
+__device__ __forceinline__ void from_e2m1x8(uint32_t w, float (&v)[8])
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(lo) : "f"(a), "f"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(hi) : "f"(c), "f"(d));
+    return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+}
+
+__device__ __forceinline__ void from_e4m3x4(uint32_t w, float (&v)[4])
+{
+    uint32_t h[2];
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"(static_cast<uint16_t>(w >> 16)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// Eight consecutive values of row p[0 .. k) from column c (a multiple of 8);
+// columns at or past k read as zero. vec: every row starts 16-byte aligned
+// and k is a multiple of 8, so the eight are one or two aligned vectors.
+__device__ __forceinline__ void load8(const void *src, dbf_dtype dt, int64_t row_start, int64_t c, int64_t k, bool vec,
+                                      float (&v)[8])
+{
+    if (c >= k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        return;
+    }
+    const int64_t at = row_start + c;
+    if (vec) {
+        if (dt == DBF_F32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at);
+            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (dt == DBF_BF16) {
+                    v[2 * i] = __uint_as_float(q[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&q[i]));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (c + i >= k)
+            v[i] = 0.0f;
+        else if (dt == DBF_F16)
+            v[i] = h2f(static_cast<const uint16_t *>(src)[at + i]);
+        else
+            v[i] = load_act(src, dt, at + i);
+    }
+}
+
+__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;   // as integers, NaN > infinity > finite
+        m = b > m ? b : m;
+    }
+    return m;
+}
+
+// The four lanes that hold one block agree on its largest magnitude.
+__device__ __forceinline__ uint32_t block_amax(uint32_t m)
+{
+    const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, m, 1);
+    m = a > m ? a : m;
+    const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, m, 2);
+    return b > m ? b : m;
+}
+
+// A lane's eight values to codes; four neighbouring lanes hold one block.
+// Returns the code word and the block's scale byte.
+__device__ __forceinline__ uint32_t quantize8_e2m1(float (&v)[8], uint32_t &byte)
+{
+    byte = scale_byte4(block_amax(amax_bits8(v)));
+    const float inv = inv_scale(byte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    const uint32_t w = e2m1x8(v);
+    return byte == 255u ? 0u : w;
+}
+
+// The scale bytes of the four blocks that a half-warp holds, as one word
+// (the same in every lane of the half).
+__device__ __forceinline__ uint32_t half_warp_scales(uint32_t byte, int lane)
+{
+    const int base = lane & 16;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= __shfl_sync(0xFFFFFFFFu, byte, base + 4 * i) << (8 * i);
+    return w;
+}
+
+}  // namespace mx
+}  // namespace dbf

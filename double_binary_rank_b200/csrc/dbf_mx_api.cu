@@ -1,0 +1,185 @@
+// Host entry points of the 4-bit base layer, its gated block and the 8-bit
+// activations: argument checks (no launch on a failed check) and path choice.
+#include "dbf_mx_layer.cuh"
+
+namespace {
+
+using namespace dbf;
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+dbf_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DBF_OK : DBF_ERR_CUDA; }
+bool act_dtype_ok(dbf_dtype d) { return d == DBF_F32 || d == DBF_BF16; }
+bool float_dtype_ok(dbf_dtype d) { return d == DBF_F32 || d == DBF_BF16 || d == DBF_F16; }
+uintptr_t size_of(dbf_dtype d) { return d == DBF_F32 ? 4 : 2; }
+
+dbf_status check_matrix(const void *values, dbf_dtype d, const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k,
+                        const int32_t *status)
+{
+    if (rows <= 0 || k <= 0 || !values || !codes || !scales || !float_dtype_ok(d)) return DBF_ERR_INVALID_ARG;
+    if (!mx_size_ok(rows, k)) return DBF_ERR_UNSUPPORTED;
+    if (!aligned(values, size_of(d)) || !aligned(codes, 16) || !aligned(scales, 16) || (status && !aligned(status, 4)))
+        return DBF_ERR_ALIGNMENT;
+    return DBF_OK;
+}
+
+bool layer_shape_ok(const dbf_mx4_layer *L) { return L && L->M > 0 && L->N > 0; }
+// tiles of at least 16 tokens and 256 rows are counted in 32 bits
+bool tokens_ok(const dbf_mx4_layer *L, int64_t T)
+{
+    return T >= 0 && T < (int64_t{1} << 31) - 4096 && ((L->N + 255) / 256) * ((T + 15) / 16) < (int64_t{1} << 31) &&
+           mx_size_ok(L->N, L->M);
+}
+
+dbf_status check_layer(const dbf_mx4_layer *L)
+{
+    if (!L->codes || !L->scales) return DBF_ERR_INVALID_ARG;
+    return aligned(L->codes, 16) && aligned(L->scales, 16) ? DBF_OK : DBF_ERR_ALIGNMENT;
+}
+
+size_t product_workspace(const dbf_mx4_layer *L, int64_t T, int mats)
+{
+    if (!layer_shape_ok(L) || !tokens_ok(L, T)) return 0;
+    if (T == 0 || mx_decode_fits(L->M, L->N, T, mats)) return kWsHeaderBytes;
+    return mx_gemm_workspace_bytes(L->M, L->N, T, mats);
+}
+
+dbf_status run(const mx::Product &c, size_t need, size_t ws_bytes, cudaStream_t s)
+{
+    if (!c.ws || ws_bytes < need) return DBF_ERR_WORKSPACE;
+    if (!aligned(c.ws, 256)) return DBF_ERR_ALIGNMENT;
+    return from_cuda(mx_decode_fits(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
+}
+
+bool same_shape(const dbf_mx4_layer *a, const dbf_mx4_layer *b)
+{
+    return layer_shape_ok(a) && layer_shape_ok(b) && a->M == b->M && a->N == b->N;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dbf_mx4_code_bytes(int64_t rows, int64_t k)
+{
+    return rows > 0 && k > 0 ? static_cast<size_t>(rows * mx::code_pitch(k)) : 0;
+}
+
+size_t dbf_mx4_scale_bytes(int64_t rows, int64_t k)
+{
+    return rows > 0 && k > 0 ? static_cast<size_t>((rows + 127) / 128 * mx::scale_tiles(k) * 512) : 0;
+}
+
+dbf_status dbf_mx4_quantize(const void *src, dbf_dtype src_dtype, int64_t rows, int64_t k, uint8_t *codes, size_t codes_bytes,
+                            uint8_t *scales, size_t scales_bytes, int32_t *status_dev, void *stream)
+{
+    const dbf_status st = check_matrix(src, src_dtype, codes, scales, rows, k, status_dev);
+    if (st != DBF_OK) return st;
+    if (codes_bytes < dbf_mx4_code_bytes(rows, k) || scales_bytes < dbf_mx4_scale_bytes(rows, k)) return DBF_ERR_INVALID_ARG;
+    return from_cuda(launch_quantize4(src, src_dtype, rows, k, codes, scales, status_dev, static_cast<cudaStream_t>(stream)));
+}
+
+dbf_status dbf_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
+                              dbf_dtype dst_dtype, void *stream)
+{
+    const dbf_status st = check_matrix(dst, dst_dtype, codes, scales, rows, k, nullptr);
+    if (st != DBF_OK) return st;
+    return from_cuda(launch_dequantize4(codes, scales, rows, k, dst, dst_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dbf_act8_code_bytes(int64_t rows, int64_t cols)
+{
+    return rows > 0 && cols > 0 ? static_cast<size_t>(rows * mx::blocks(cols) * mx::kBlock) : 0;
+}
+
+size_t dbf_act8_scale_bytes(int64_t rows, int64_t cols)
+{
+    return rows > 0 && cols > 0 ? static_cast<size_t>(rows * mx::blocks(cols)) : 0;
+}
+
+dbf_status dbf_act8_save(const void *src, dbf_dtype src_dtype, int64_t rows, int64_t cols, const dbf_act8 *dst,
+                         int32_t *status_dev, void *stream)
+{
+    if (!dst) return DBF_ERR_INVALID_ARG;
+    if (rows == 0 && cols > 0) return DBF_OK;
+    const dbf_status st = check_matrix(src, src_dtype, dst->codes, dst->scales, rows, cols, status_dev);
+    if (st != DBF_OK) return st;
+    return from_cuda(
+        launch_act8_save(src, src_dtype, rows, cols, dst->codes, dst->scales, status_dev, static_cast<cudaStream_t>(stream)));
+}
+
+dbf_status dbf_act8_load(const dbf_act8 *src, int64_t rows, int64_t cols, void *dst, dbf_dtype dst_dtype, void *stream)
+{
+    if (!src) return DBF_ERR_INVALID_ARG;
+    if (rows == 0 && cols > 0) return DBF_OK;
+    const dbf_status st = check_matrix(dst, dst_dtype, src->codes, src->scales, rows, cols, nullptr);
+    if (st != DBF_OK) return st;
+    return from_cuda(launch_act8_load(src->codes, src->scales, rows, cols, dst, dst_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T) { return product_workspace(L, T, 1); }
+
+dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dtype, void *y, dbf_dtype y_dtype, int64_t T,
+                           int flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!layer_shape_ok(L) || T < 0 || !act_dtype_ok(x_dtype) || !act_dtype_ok(y_dtype) ||
+        (flags & ~(DBF_ACCUMULATE | DBF_WEIGHTS_STATIC)))
+        return DBF_ERR_INVALID_ARG;
+    if (!tokens_ok(L, T)) return DBF_ERR_UNSUPPORTED;
+    if (T == 0) return DBF_OK;
+    if (!x || !y) return DBF_ERR_INVALID_ARG;
+    const dbf_status st = check_layer(L);
+    if (st != DBF_OK) return st;
+    if (!aligned(x, 16) || !aligned(y, 16)) return DBF_ERR_ALIGNMENT;
+    mx::Product c = {};
+    c.M = L->M, c.N = L->N, c.T = T, c.mats = 1;
+    c.codes[0] = L->codes, c.scales[0] = L->scales;
+    c.x = x, c.xd = x_dtype;
+    c.ep.y = y, c.ep.yd = y_dtype, c.ep.accumulate = flags & DBF_ACCUMULATE ? 1 : 0;
+    c.ep.N = L->N, c.ep.T = T;
+    c.flags = flags, c.ws = ws;
+    return run(c, product_workspace(L, T, 1), ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t dbf_mx4_gated_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T)
+{
+    return same_shape(gate, up) ? product_workspace(gate, T, 2) : 0;
+}
+
+dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const void *x,
+                                 dbf_dtype x_dtype, const void *g_add, const void *u_add, dbf_dtype add_dtype, void *h,
+                                 dbf_dtype h_dtype, const dbf_act8 *save_g, const dbf_act8 *save_u, int64_t T, int flags,
+                                 void *ws, size_t ws_bytes, void *stream)
+{
+    if (!same_shape(gate, up) || T < 0 || (act != DBF_GATE_SILU && act != DBF_GATE_GELU) || !act_dtype_ok(x_dtype) ||
+        !act_dtype_ok(h_dtype) || ((g_add || u_add) && !act_dtype_ok(add_dtype)) || !save_g != !save_u ||
+        (flags & ~DBF_WEIGHTS_STATIC))
+        return DBF_ERR_INVALID_ARG;
+    if (!tokens_ok(gate, T)) return DBF_ERR_UNSUPPORTED;
+    if (T == 0) return DBF_OK;
+    if (!x || !h || (save_g && (!save_g->codes || !save_g->scales || !save_u->codes || !save_u->scales)))
+        return DBF_ERR_INVALID_ARG;
+    dbf_status st = check_layer(gate);
+    if (st == DBF_OK) st = check_layer(up);
+    if (st != DBF_OK) return st;
+    if (!aligned(x, 16) || !aligned(h, 16) || !aligned(g_add, 16) || !aligned(u_add, 16) ||
+        (save_g && (!aligned(save_g->codes, 16) || !aligned(save_g->scales, 16) || !aligned(save_u->codes, 16) ||
+                    !aligned(save_u->scales, 16))))
+        return DBF_ERR_ALIGNMENT;
+    mx::Product c = {};
+    c.M = gate->M, c.N = gate->N, c.T = T, c.mats = 2;
+    c.codes[0] = gate->codes, c.scales[0] = gate->scales;
+    c.codes[1] = up->codes, c.scales[1] = up->scales;
+    c.x = x, c.xd = x_dtype;
+    c.ep.y = h, c.ep.yd = h_dtype, c.ep.act = act;
+    c.ep.g_add = g_add, c.ep.u_add = u_add, c.ep.add_dt = add_dtype;
+    if (save_g) {
+        c.ep.g8 = save_g->codes, c.ep.gs = save_g->scales;
+        c.ep.u8 = save_u->codes, c.ep.us = save_u->scales;
+    }
+    c.ep.pitch8 = mx::blocks(gate->N) * mx::kBlock;
+    c.ep.N = gate->N, c.ep.T = T;
+    c.flags = flags, c.ws = ws;
+    return run(c, product_workspace(gate, T, 2), ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

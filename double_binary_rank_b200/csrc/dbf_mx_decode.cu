@@ -1,0 +1,310 @@
+// y = W q(x) and the gated block for few tokens: one launch, no pre-pass.
+//
+// With few tokens every weight is used a handful of times, so the codes and
+// scales must stream from device memory at its full rate (17 bytes per 32
+// weights); the block-scaled MMA (dbf_mx_gemm.cu has the mathematics) with
+// the weights as its 128 rows and the tokens, padded to 16, as its columns
+// keeps the arithmetic far below that. A cluster of S CTAs shares one block of
+// 128 weight rows (of both weights in the gated block), each taking 1/S of
+// the columns, so that 148 SMs have loads in flight also for small layers:
+//   warp 0      TMA ring of weight stages (256 columns), started before the
+//               kernel in front has ended where the caller allows it;
+//   warps 2..9  meanwhile quantise the CTA's columns of x into shared memory
+//               in the MMA's layout (each cluster does it again: T columns of
+//               a few KB that stay in L2, against one more launch);
+//   warp 1      one thread copies scales and issues the MMAs.
+// The partial sums then meet in shared memory: each CTA adds the S partials of
+// its share of (token, 32 rows) over distributed shared memory in CTA order,
+// so results do not depend on timing, and finishes them.
+#include <algorithm>
+
+#include "dbf_mx_layer.cuh"
+#include "dbf_tc.cuh"
+
+namespace dbf {
+namespace {
+
+using namespace mx;
+using namespace tc;
+
+constexpr int kMaxRing = 8;
+constexpr int kMaxTokens = 64;   // tokens of one tile, and of a call
+constexpr int kWorkers = 8;
+constexpr int kThreads = 32 * (2 + kWorkers);
+constexpr uint32_t kABytes = 128 * 128, kSfBytes = 1024;
+
+struct Smem {
+    uint64_t full[kMaxRing], empty[kMaxRing], x_ready, done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Args {
+    int nk;      // stages of 256 columns, all CTAs of a cluster together
+    int w;       // columns of the MMA: T rounded up to 16
+    int ring;    // weight stages in shared memory
+    int nks;     // most stages of one CTA
+    int T;
+    int64_t M;
+    const void *x;
+    dbf_dtype xd;
+    int vec;
+    int early;   // weights may be read before earlier work is done
+    uint32_t tmem_cols;
+    Epilogue ep;
+    int32_t *status;
+};
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads) mx_decode_kernel(
+    const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1, const __grid_constant__ CUtensorMap mS0,
+    const __grid_constant__ CUtensorMap mS1, const __grid_constant__ Args g)
+{
+    constexpr int kMats = kGated ? 2 : 1;
+    constexpr uint32_t kStage = kMats * (kABytes + kSfBytes);
+    extern __shared__ uint8_t raw[];
+    uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *xq = ring + g.ring * kStage;   // per stage: w rows of 128 bytes, then 1 KB of scales
+    const uint32_t x_stage = g.w * 128 + 1024;
+    Smem *sh = reinterpret_cast<Smem *>(xq + g.nks * x_stage);
+    float *part = reinterpret_cast<float *>(ring);   // [mat][token][128 rows], once the ring is done with
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = gridDim.x, rank = blockIdx.x;
+    const int row0 = blockIdx.y * 128;
+    const int k0 = g.nk * rank / S, nks = g.nk * (rank + 1) / S - k0;
+    volatile int *abort = &sh->abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.ring; ++i) {
+            bar_init(&sh->full[i], 1);
+            bar_init(&sh->empty[i], 1);
+        }
+        bar_init(&sh->x_ready, kWorkers);
+        bar_init(&sh->done, 1);
+        sh->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<1>(&sh->tmem_base, g.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+    const uint32_t sf_col = kMats * g.w;   // scales: 8 columns per weight, then 8 of x
+
+    if (warp == 0) {
+        if (lane == 0) {
+            if (!g.early) griddep_wait();
+            int i = 0;
+            for (; i < nks; ++i) {
+                const int s = i % g.ring;
+                if (!bar_wait(&sh->empty[s], (static_cast<uint32_t>(i / g.ring) & 1u) ^ 1u, abort)) break;
+                uint8_t *st = ring + s * kStage;
+                bar_expect_tx(&sh->full[s], kStage);
+                tma_2d(st, &mA0, (k0 + i) * 128, row0, &sh->full[s]);
+                if (kGated) tma_2d(st + kABytes, &mA1, (k0 + i) * 128, row0, &sh->full[s]);
+                tma_3d(st + kMats * kABytes, &mS0, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
+                if (kGated) tma_3d(st + kMats * kABytes + kSfBytes, &mS1, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
+            }
+            if (*abort)
+                for (int j = i > g.ring ? i - g.ring : 0; j < i; ++j)
+                    drain_wait(&sh->full[j % g.ring], static_cast<uint32_t>(j / g.ring) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t id0 = mxf4_idesc(128, g.w, 0), id2 = mxf4_idesc(128, g.w, 2);
+            bool ok = bar_wait(&sh->x_ready, 0, abort);
+            for (int i = 0; i < nks && ok; ++i) {
+                const int s = i % g.ring;
+                ok = bar_wait(&sh->full[s], static_cast<uint32_t>(i / g.ring) & 1u, abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(ring) + s * kStage, sf = st + kMats * kABytes;
+                const uint32_t xs = smem_u32(xq) + i * x_stage;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    scale_copy<1>(tmem + sf_col + 4 * c, scale_desc(sf + c * 512));
+                    if (kGated) scale_copy<1>(tmem + sf_col + 8 + 4 * c, scale_desc(sf + kSfBytes + c * 512));
+                    scale_copy<1>(tmem + sf_col + 8 * kMats + 4 * c, scale_desc(xs + g.w * 128 + c * 512));
+                }
+                const uint64_t b = sw128_desc(xs);
+#pragma unroll
+                for (int m = 0; m < kMats; ++m) {
+                    const uint64_t a = sw128_desc(st + m * kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mxf4<1>(tmem + m * g.w, a + 2 * kk, b + 2 * kk, kk & 1 ? id2 : id0,
+                                    tmem + sf_col + 8 * m + 4 * (kk >> 1), tmem + sf_col + 8 * kMats + 4 * (kk >> 1),
+                                    i > 0 || kk > 0 ? 1u : 0u);
+                }
+                commit_own(&sh->empty[s]);
+            }
+            commit_own(&sh->done);
+            drain_wait(&sh->done, 0);
+        }
+    } else {
+        const int worker = warp - 2;
+        griddep_wait();     // x, y and the addends belong to earlier work until then
+        griddep_launch();   // what follows may be set up: all earlier work is done
+        for (int u0 = worker; u0 < g.T * nks; u0 += 4 * kWorkers) {
+            float v[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + i * kWorkers;
+                const int t = u / nks, ks = u - t * nks;
+                const int64_t c = static_cast<int64_t>(k0 + ks) * 256 + lane * 8;
+                load8(g.x, g.xd, t * g.M, u < g.T * nks ? c : g.M, g.M, g.vec, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + i * kWorkers;
+                if (u >= g.T * nks) break;
+                const int t = u / nks, ks = u - t * nks;
+                uint32_t byte;
+                const uint32_t q = quantize8_e2m1(v[i], byte);
+                const uint32_t word = half_warp_scales(byte, lane);
+                uint8_t *xs = xq + ks * x_stage;
+                *reinterpret_cast<uint32_t *>(xs + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = q;
+                if ((lane & 15) == 0)
+                    *reinterpret_cast<uint32_t *>(xs + g.w * 128 + (lane >> 4) * 512 + (t & 31) * 16 + (t >> 5) * 4) = word;
+            }
+        }
+        fence_proxy_async();   // the MMA reads what these stores wrote
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh->x_ready);
+        if (bar_wait(&sh->done, 0, abort)) {
+            tc_fence_after();
+            const int quarter = warp & 3, half = worker >> 2;
+            for (int col = half * 16; col < kMats * g.w; col += 32) {
+                float v[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[(col + j) * 128 + quarter * 32 + lane] = v[j];
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2) {
+        const uint32_t base = smem_u32(part);
+        for (int u = rank + S * (warp - 2); u < 4 * g.T; u += S * kWorkers) {
+            const int t = u >> 2, r = (u & 3) * 32 + lane;
+            float sum[kMats];
+#pragma unroll
+            for (int m = 0; m < kMats; ++m) {
+                sum[m] = 0.0f;
+                for (int s = 0; s < S; ++s) sum[m] += ld_cluster_f32(base + ((m * g.w + t) * 128 + r) * 4, s);
+            }
+            if (kGated)
+                finish_gated(g.ep, t, row0 + r, sum[0], sum[kMats - 1]);
+            else
+                finish_plain(g.ep, t, row0 + r, sum[0]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA ends while another still reads its partial sums
+    if (threadIdx.x == 0 && sh->abort && g.status) atomicExch(g.status, static_cast<int32_t>(DBF_ERR_TIMEOUT));
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<1>(tmem, g.tmem_cols);
+    }
+}
+
+struct Shape {
+    int w, split, ring, nks;
+    size_t smem;
+};
+
+// Split of the columns and ring depth; false when the CTA's columns of x do
+// not fit in shared memory.
+bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
+{
+    if (T > kMaxTokens) return false;
+    const int64_t nk = (M + 255) / 256, row_blocks = (N + 127) / 128;
+    const int stage = mats * static_cast<int>(kABytes + kSfBytes);
+    p.w = static_cast<int>((T + 15) / 16 * 16);
+    const int64_t slots = 2 * device_sms();
+    int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, nk, slots / row_blocks}));
+    const int64_t x_stage = p.w * 128 + 1024;
+    const int64_t fixed = 1024 + sizeof(Smem), most = 227 * 1024 - fixed - 3 * stage;
+    while (split < std::min<int64_t>(8, nk) && (nk + split - 1) / split * x_stage > most) ++split;
+    p.split = static_cast<int>(split);
+    p.nks = static_cast<int>((nk + split - 1) / split);
+    const int64_t x_bytes = p.nks * x_stage;
+    if (x_bytes > most || row_blocks > 65535) return false;
+    // two CTAs to an SM where that leaves three stages or all that are needed, else one
+    const int want = std::min(kMaxRing, std::max(2, p.nks));
+    const int64_t two = (113 * 1024 - fixed - x_bytes) / stage, one = (227 * 1024 - fixed - x_bytes) / stage;
+    int64_t ring = two >= std::min(3, want) && row_blocks * split > device_sms() ? two : one;
+    p.ring = static_cast<int>(std::min<int64_t>(ring, want));
+    // at least a third of an SM: with two CTAs to an SM at most, their tensor
+    // memory (256 columns each) is always there, so no CTA waits for it while
+    // another of its cluster waits at the exchange
+    p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + p.ring * stage, 77 * 1024));
+    return p.ring >= 2;
+}
+
+}  // namespace
+
+bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats)
+{
+    Shape p;
+    return shape(M, N, T, mats, p);
+}
+
+cudaError_t mx_decode(const Product &c, cudaStream_t s)
+{
+    Shape p;
+    if (!shape(c.M, c.N, c.T, c.mats, p)) return cudaErrorInvalidValue;
+    const bool gated = c.mats == 2;
+    CUtensorMap a[2], sa[2];
+    for (int m = 0; m < 2; ++m) {
+        const int from = gated ? m : 0;
+        const uint64_t dims[2] = {static_cast<uint64_t>(code_pitch(c.M)), static_cast<uint64_t>(c.N)};
+        const uint64_t strides[1] = {dims[0]};
+        const uint32_t box[2] = {128, 128};
+        const uint64_t tiles = static_cast<uint64_t>(scale_tiles(c.M));
+        const uint64_t sdims[3] = {128, tiles, static_cast<uint64_t>((c.N + 127) / 128)};
+        const uint64_t sstrides[2] = {512, tiles * 512};
+        const uint32_t sbox[3] = {128, 2, 1};
+        if (!tc_map(&a[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes[from], dims, strides, box, true) ||
+            !tc_map(&sa[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, c.scales[from], sdims, sstrides, sbox, false))
+            return cudaErrorInvalidValue;
+    }
+    Args g = {};
+    g.nk = static_cast<int>((c.M + 255) / 256);
+    g.w = p.w;
+    g.ring = p.ring;
+    g.nks = p.nks;
+    g.T = static_cast<int>(c.T);
+    g.M = c.M;
+    g.x = c.x;
+    g.xd = c.xd;
+    g.vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+    g.early = c.flags & DBF_WEIGHTS_STATIC ? 1 : 0;
+    const int cols = c.mats * p.w + 8 * c.mats + 8;
+    g.tmem_cols = 32;
+    while (static_cast<int>(g.tmem_cols) < cols) g.tmem_cols *= 2;
+    g.ep = c.ep;
+    g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
+
+    const auto kernel = gated ? mx_decode_kernel<true> : mx_decode_kernel<false>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), static_cast<int>(p.smem), true);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.split), static_cast<unsigned>((c.N + 127) / 128));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], sa[0], sa[1], g);
+}
+
+}  // namespace dbf

@@ -1,0 +1,427 @@
+// y = W q(x) on the block-scaled tensor cores, and the gated block
+// h = act(Wg q(x) + g_add) (Wu q(x) + u_add), for many tokens.
+//
+// Mathematics: both operands are microscaled (dbf_mx.cuh), so a product of
+// two blocks of 32 is 2^(sa + sb) times a sum of 32 products of E2M1 codes:
+// tcgen05.mma kind::mxf4 computes it with fp32 accumulators from packed codes
+// and scale bytes as they lie in memory. A pre-pass quantises x (one pass
+// over x); one persistent launch does the rest.
+//
+// Tile: a CTA pair (cta_group::2) owns 512 weight rows x w tokens as two
+// accumulators of 256 x w: two row blocks of W, or 256 rows of Wg and the same
+// rows of Wu, so the gated block finds g and u of one element in one place. At
+// four times the bf16 rate the operands' way into the SM bounds the tile, not
+// the MMA: 512 x 240 takes 50 KB per 960 cycles of MMA and SM; a double-buffered
+// 256 x 240 would take 34 KB per 480.
+//   warp 0      TMA: per stage of 256 columns, 2 x 128 rows of codes (128-byte
+//               swizzle), w/2 token rows, and their scale tiles;
+//   warp 1      tensor memory; in CTA 0 one thread copies the stage's scales
+//               into tensor memory (tcgen05.cp) and issues eight MMAs;
+//   warps 2..9  epilogue.
+// The token width w is chosen per call (a multiple of 16 up to 240, what 512
+// tensor-memory columns hold beside 32 of scales) so that the tiles fill whole
+// waves of pairs. Every wait is bounded; on expiry the status word is set.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "dbf_mx_layer.cuh"
+#include "dbf_tc.cuh"
+
+namespace dbf {
+namespace {
+
+using namespace mx;
+using namespace tc;
+
+constexpr int kStages = 4;
+constexpr int kMaxW = 240;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kABytes = 128 * 128;            // 128 rows x 256 codes
+constexpr uint32_t kBBytes = kMaxW / 2 * 128;      // this CTA's half of the tokens
+constexpr uint32_t kSfABytes = 1024, kSfBBytes = 2048;
+constexpr uint32_t kStageBytes = 2 * kABytes + kBBytes + 2 * kSfABytes + kSfBBytes;
+constexpr uint32_t kSfCol = 480;   // tensor-memory columns: 2 w of accumulators, then scales
+constexpr uint32_t kTmemCols = 512;
+
+struct Smem {
+    uint64_t full[kStages], empty[kStages], acc_full, acc_empty, drain, exit_bar;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Args {
+    int nk;         // stages of 256 columns
+    int w;          // tokens per tile
+    int n_p;        // row tiles
+    int tiles;
+    int row_step;   // weight rows of a tile: 512 plain, 256 gated
+    int row_off;    // rows from the first accumulator's to the second's: 256 plain, 0 gated
+    Epilogue ep;
+    int32_t *status;
+};
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
+    const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1, const __grid_constant__ CUtensorMap mS0,
+    const __grid_constant__ CUtensorMap mS1, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mSB,
+    const __grid_constant__ Args g)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Smem *sh = reinterpret_cast<Smem *>(stage0 + kStages * kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+    volatile int *abort = &sh->abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(&sh->full[i], 1);
+            bar_init(&sh->empty[i], 1);
+        }
+        bar_init(&sh->acc_full, 1);
+        bar_init(&sh->acc_empty, 2 * kEpiWarps);
+        bar_init(&sh->drain, 1);
+        bar_init(&sh->exit_bar, 1);
+        sh->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<2>(&sh->tmem_base, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before either is reached from the other
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+    // the pre-pass before this launch has waited for all earlier work, so
+    // weights may be read at once; x's codes, and y, only after it is done
+    griddep_launch();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int half_w = g.w / 2, nrt = g.w > 128 ? 2 : 1;
+            const uint32_t bytes = 2 * (2 * kABytes + half_w * 128 + 2 * kSfABytes + nrt * 1024);
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true, waited = false;
+            for (int tile = unit; tile < g.tiles && ok; tile += units) {
+                const int p = tile % g.n_p, c = tile / g.n_p;
+                const int row0 = p * g.row_step + static_cast<int>(rank) * 128, row1 = row0 + g.row_off;
+                const int tok = c * g.w + static_cast<int>(rank) * half_w;
+                for (int ks = 0; ks < g.nk; ++ks) {
+                    if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = stage0 + s * kStageBytes;
+                    if (rank == 0) bar_expect_tx(&sh->full[s], bytes);
+                    tma_2d_pair(st, &mA0, ks * 128, row0, &sh->full[s]);
+                    tma_2d_pair(st + kABytes, &mA1, ks * 128, row1, &sh->full[s]);
+                    uint8_t *sf = st + 2 * kABytes + kBBytes;
+                    tma_3d_pair(sf, &mS0, 0, ks * 2, row0 >> 7, &sh->full[s]);
+                    tma_3d_pair(sf + kSfABytes, &mS1, 0, ks * 2, row1 >> 7, &sh->full[s]);
+                    if (!waited) {
+                        griddep_wait();
+                        waited = true;
+                    }
+                    tma_2d_pair(st + 2 * kABytes, &mB, ks * 128, tok, &sh->full[s]);
+                    tma_3d_pair(sf + 2 * kSfABytes, &mSB, 0, ks * 2, c * nrt, &sh->full[s]);
+                    ++issued;
+                    if (++s == kStages) s = 0, ph ^= 1u;
+                }
+            }
+            // after a wait gave up, the loads in flight are still waited for
+            // (CTA 0's barriers count both CTAs' bytes)
+            if (*abort && rank == 0)
+                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                    drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, acc_ph = 0;
+            bool ok = true;
+            const int nrt = g.w > 128 ? 2 : 1;
+            const uint32_t id0 = mxf4_idesc(256, g.w, 0), id2 = mxf4_idesc(256, g.w, 2);
+            for (int tile = unit; tile < g.tiles && ok; tile += units) {
+                ok = bar_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
+                if (!ok) break;
+                tc_fence_after();
+                for (int ks = 0; ks < g.nk; ++ks) {
+                    if (!bar_wait(&sh->full[s], ph, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(stage0) + s * kStageBytes;
+                    const uint32_t sf = st + 2 * kABytes + kBBytes;
+                    // scales: columns kSfCol + 8 m + 4 c of accumulator m, K half c; tokens from kSfCol + 16 on
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        scale_copy<2>(tmem + kSfCol + 4 * c, scale_desc(sf + c * 512));
+                        scale_copy<2>(tmem + kSfCol + 8 + 4 * c, scale_desc(sf + kSfABytes + c * 512));
+                        for (int r = 0; r < nrt; ++r)
+                            scale_copy<2>(tmem + kSfCol + 16 + 8 * c + 4 * r, scale_desc(sf + 2 * kSfABytes + r * 1024 + c * 512));
+                    }
+                    const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + 2 * kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t id = kk & 1 ? id2 : id0, acc = ks > 0 || kk > 0 ? 1u : 0u;
+                        const uint32_t sb = tmem + kSfCol + 16 + 8 * (kk >> 1);
+                        mma_mxf4<2>(tmem, a0 + 2 * kk, b + 2 * kk, id, tmem + kSfCol + 4 * (kk >> 1), sb, acc);
+                        mma_mxf4<2>(tmem + g.w, a1 + 2 * kk, b + 2 * kk, id, tmem + kSfCol + 8 + 4 * (kk >> 1), sb, acc);
+                    }
+                    commit_pair_both(&sh->empty[s]);
+                    if (++s == kStages) s = 0, ph ^= 1u;
+                }
+                if (!ok) break;
+                commit_pair_both(&sh->acc_full);
+                acc_ph ^= 1u;
+            }
+            if (*abort) {
+                commit_pair_own(&sh->drain);
+                drain_wait(&sh->drain, 0);
+            }
+        }
+    } else {
+        griddep_wait();   // y (and the addends) belong to earlier work until then
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint32_t acc_ph = 0;
+        for (int tile = unit; tile < g.tiles; tile += units) {
+            const int p = tile % g.n_p, c = tile / g.n_p;
+            if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
+            acc_ph ^= 1u;
+            tc_fence_after();
+            const int64_t t0 = static_cast<int64_t>(c) * g.w;
+            if (kGated) {
+                const int n = p * g.row_step + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+                // the two warps of a lane quarter take turns by 16 tokens
+                for (int j0 = half * 16; j0 < g.w; j0 += 32) {
+                    float vg[16], vu[16];
+                    tmem_ld16(lanes + j0, vg);
+                    tmem_ld16(lanes + g.w + j0, vu);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (t0 + j0 + j < g.ep.T) finish_gated(g.ep, t0 + j0 + j, n, vg[j], vu[j]);
+                }
+            } else {
+                // each of the two warps takes one accumulator
+                const int n = p * g.row_step + half * g.row_off + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+                for (int j0 = 0; j0 < g.w; j0 += 16) {
+                    float v[16];
+                    tmem_ld16(lanes + half * g.w + j0, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (t0 + j0 + j < g.ep.T) finish_plain(g.ep, t0 + j0 + j, n, v[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // neither CTA ends while the other may still reach its shared memory
+    if (threadIdx.x == 0) {
+        bar_arrive_rank(&sh->exit_bar, rank ^ 1u);
+        drain_wait(&sh->exit_bar, 0);
+        if (sh->abort && g.status) atomicExch(g.status, static_cast<int32_t>(DBF_ERR_TIMEOUT));
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<2>(tmem, kTmemCols);
+    }
+}
+
+// Pre-pass: x to codes and scales in the workspace. The scales of the tokens
+// of one tile start a new 128-row scale tile, since a tile of w tokens is no
+// multiple of 128: token t has scale row (t / w) * pad + t % w.
+template <dbf_dtype DT>
+__global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict__ x, int64_t T, int64_t M, bool vec, int w, int pad,
+                                  uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
+{
+    griddep_wait();     // the workspace may still be read by the call before
+    griddep_launch();   // so the product's launch starts with all earlier work done
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+    const int64_t nb = blocks(M), pitch = nb * 16, tiles = scale_tiles(M);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + 8 * i;
+        load8(x, DT, r * M, r < T ? c : M, M, vec, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + 8 * i;
+        uint32_t byte;
+        const uint32_t q = quantize8_e2m1(v[i], byte);
+        const uint32_t word = half_warp_scales(byte, lane);
+        if (r >= T) continue;
+        if (c < nb * kBlock) *reinterpret_cast<uint32_t *>(codes + r * pitch + c / 2) = q;
+        if ((lane & 15) == 0 && (c >> 7) < tiles)
+            *reinterpret_cast<uint32_t *>(scales + scale_at(r / w * pad + r % w, c >> 5, tiles)) = word;
+    }
+}
+
+int resident_pairs(const void *kernel, cudaLaunchConfig_t cfg)
+{
+    static std::mutex lock;
+    static std::map<std::pair<int, const void *>, int> known;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> guard(lock);
+    auto it = known.find({dev, kernel});
+    if (it == known.end()) {
+        const int pairs = std::max(1, device_sms() / 2);
+        cfg.gridDim = dim3(2 * pairs);
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        (void)cudaGetLastError();
+        it = known.emplace(std::make_pair(dev, kernel), e == cudaSuccess && n > 0 ? std::min(n, pairs) : pairs).first;
+    }
+    return it->second;
+}
+
+// Tokens per tile. Cost in cycles of the last pair to finish: waves of tiles,
+// each nk stages and an epilogue. A stage takes its eight MMAs (4 w cycles) or
+// its operands' way into the SM, whichever is longer.
+int tile_width(int64_t N, int64_t M, int64_t T, int mats)
+{
+    const int64_t n_p = (N + (mats == 2 ? 255 : 511)) / (mats == 2 ? 256 : 512);
+    const int64_t nk = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    int best = 16;
+    double least = 0;
+    for (int w = 16; w <= kMaxW; w += 16) {
+        const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
+        const double bytes = 2 * (kABytes + 1024.0) + w / 2 * 128 + (w > 128 ? 2048 : 1024);
+        const double cost = static_cast<double>(waves) * (nk * std::max(4.0 * w, bytes / 45) + 800 + 12.0 * w);
+        if (w == 16 || cost < least) least = cost, best = w;
+        if (w >= T) break;
+    }
+    return best;
+}
+
+struct Plan {
+    int w, pad;
+    size_t codes, scales, total;   // offsets in the workspace, and its size
+};
+
+Plan plan(int64_t M, int64_t N, int64_t T, int mats)
+{
+    Plan p;
+    p.w = tile_width(N, M, T, mats);
+    p.pad = p.w > 128 ? 256 : 128;
+    p.codes = kWsHeaderBytes;
+    p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
+    p.total = align_up(p.scales + static_cast<size_t>((T + p.w - 1) / p.w * (p.pad / 128) * scale_tiles(M) * 512), 256);
+    return p;
+}
+
+bool code_map(CUtensorMap *m, const uint8_t *codes, int64_t k, int64_t rows, int box_rows)
+{
+    const uint64_t dims[2] = {static_cast<uint64_t>(code_pitch(k)), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(code_pitch(k))};
+    const uint32_t box[2] = {128, static_cast<uint32_t>(box_rows)};
+    return tc_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, true);
+}
+
+bool scale_map(CUtensorMap *m, const uint8_t *scales, int64_t k, int64_t row_tiles, int box_tiles)
+{
+    const uint64_t tiles = static_cast<uint64_t>(scale_tiles(k));
+    const uint64_t dims[3] = {128, tiles, static_cast<uint64_t>(row_tiles)};
+    const uint64_t strides[2] = {512, tiles * 512};
+    const uint32_t box[3] = {128, 2, static_cast<uint32_t>(box_tiles)};
+    return tc_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, scales, dims, strides, box, false);
+}
+
+}  // namespace
+
+bool tc_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
+            const uint64_t *strides, const uint32_t *box, bool swizzle128)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    if (!fn) return false;
+    cuuint64_t d[3] = {}, s[2] = {};
+    cuuint32_t b[3] = {}, one[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
+    for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
+    return fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats) { return plan(M, N, T, mats).total; }
+
+cudaError_t mx_gemm(const Product &c, cudaStream_t s)
+{
+    const Plan pl = plan(c.M, c.N, c.T, c.mats);
+    uint8_t *codes = static_cast<uint8_t *>(c.ws) + pl.codes, *scales = static_cast<uint8_t *>(c.ws) + pl.scales;
+
+    CUtensorMap a[2], sa[2], b, sb;
+    const bool gated = c.mats == 2;
+    for (int m = 0; m < 2; ++m)
+        if (!code_map(&a[m], c.codes[gated ? m : 0], c.M, c.N, 128) ||
+            !scale_map(&sa[m], c.scales[gated ? m : 0], c.M, (c.N + 127) / 128, 1))
+            return cudaErrorInvalidValue;
+    if (!code_map(&b, codes, c.M, c.T, pl.w / 2) ||
+        !scale_map(&sb, scales, c.M, (c.T + pl.w - 1) / pl.w * (pl.pad / 128), pl.pad / 128))
+        return cudaErrorInvalidValue;
+
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+
+    cudaLaunchConfig_t pre = {};
+    pre.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + 255) / 256));
+    pre.blockDim = dim3(256);
+    pre.stream = s;
+    pre.attrs = attr;
+    pre.numAttrs = 1;
+    const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+    cudaError_t e = cudaLaunchKernelEx(&pre, c.xd == DBF_F32 ? quantize_x_kernel<DBF_F32> : quantize_x_kernel<DBF_BF16>, c.x, c.T,
+                                       c.M, vec, pl.w, pl.pad, codes, scales);
+    if (e != cudaSuccess) return e;
+
+    const auto kernel = gated ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+    const int smem = 1024 + kStages * kStageBytes + sizeof(Smem);
+    e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    Args g = {};
+    g.nk = static_cast<int>((c.M + 255) / 256);
+    g.w = pl.w;
+    g.row_step = gated ? 256 : 512;
+    g.row_off = gated ? 0 : 256;
+    g.n_p = static_cast<int>((c.N + g.row_step - 1) / g.row_step);
+    g.tiles = static_cast<int>(g.n_p * ((c.T + pl.w - 1) / pl.w));
+    g.ep = c.ep;
+    g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    const int pairs = std::min(resident_pairs(reinterpret_cast<const void *>(kernel), cfg), g.tiles);
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], sa[0], sa[1], b, sb, g);
+}
+
+}  // namespace dbf

@@ -453,6 +453,119 @@ dbf_status dbf_debug_fused_schedule(const dbf_layer *L, int64_t T, int32_t pairs
  * calls in flight on other host threads. */
 void dbf_debug_set_decode_wait_ns(uint64_t ns);
 
+/* ---- 4-bit base layer -------------------------------------------------------
+ * The base that an unmerged adapter is added to is frozen and may be stored in
+ * 4 bits (LoRDBA page, sections 1, 3 and 5). It is kept in microscaled 4-bit
+ * floating point: a row is cut into blocks of 32 columns; a block holds 32
+ * E2M1 codes (sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6) and one scale 2^s, stored
+ * as the byte s + 127 (E8M0).
+ * Quantising a block of largest magnitude amax takes
+ * s = clamp(floor(log2 amax) - 2, -127, 127) (byte 0 for a block of zeros) and
+ * rounds each value / 2^s to the nearest code, ties to the even code, at most
+ * +-6. A block that holds a NaN or an infinity gets the byte 255, and reads
+ * back, and multiplies, as NaN. Bytes 253 and 254 may overflow when read back.
+ * Layout of a rows x k matrix:
+ *   codes: rows of ceil(k/32) * 16 bytes; column 2j in the low nibble of byte
+ *     j, column 2j + 1 in the high one; codes past column k are zero.
+ *   scales: tiles of 128 rows x 4 blocks, 512 bytes each, ceil(rows/128) row
+ *     tiles of ceil(blocks/4) tiles; row r's block b is byte
+ *     (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile (r / 128, b / 4).
+ *     Bytes of blocks past the last one must not be 255 (dbf_mx4_quantize
+ *     writes 0); those of rows past the last one are not used.
+ * Both 16-byte aligned. */
+
+/* Bytes of the codes and of the scales of a rows x k matrix. */
+size_t dbf_mx4_code_bytes(int64_t rows, int64_t k);
+size_t dbf_mx4_scale_bytes(int64_t rows, int64_t k);
+
+/* Quantise src (rows x k, row-major, DBF_F32, DBF_BF16 or DBF_F16).
+ * status_dev: optional device int32; a block with a NaN or an infinity stores
+ *    DBF_ERR_INVALID_ARG there.
+ * Errors: DBF_ERR_INVALID_ARG (null, sizes, dtype, buffers too small),
+ *    DBF_ERR_UNSUPPORTED (k above 65535 * 256), DBF_ERR_ALIGNMENT, DBF_ERR_CUDA. */
+dbf_status dbf_mx4_quantize(const void *src, dbf_dtype src_dtype, int64_t rows, int64_t k, uint8_t *codes, size_t codes_bytes,
+                            uint8_t *scales, size_t scales_bytes, int32_t *status_dev, void *stream);
+
+/* The values that codes and scales stand for, in DBF_F32, DBF_BF16 or DBF_F16
+ * (exact in the first two, subnormals of the type included; fp16 rounds and
+ * overflows). Errors as dbf_mx4_quantize. */
+dbf_status dbf_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
+                              dbf_dtype dst_dtype, void *stream);
+
+/* A 4-bit layer: W is N x M (out x in), codes and scales as above. */
+typedef struct {
+    int32_t M, N;
+    const uint8_t *codes;
+    const uint8_t *scales;
+} dbf_mx4_layer;
+
+/* Workspace bytes of dbf_mx4_forward (0 for invalid input): the header, and
+ * for many tokens the quantised x. */
+size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T);
+
+/* y = [acc] y + W q(x) for T tokens, q(x) being x quantised row by row as
+ * dbf_mx4_quantize does it: both operands are microscaled 4-bit, products are
+ * exact, sums fp32, one rounding to y's type. Any M, N and T: a few tokens run
+ * as one launch that streams the weights, more as a pre-pass and one
+ * tensor-core launch.
+ * x: T x M and y: T x N, DBF_F32 or DBF_BF16, 16-byte aligned, not
+ *    overlapping. flags: DBF_ACCUMULATE | DBF_WEIGHTS_STATIC.
+ * A NaN or an infinity in a block of x makes that token's outputs NaN.
+ * ws: dbf_mx4_workspace_bytes(L, T) bytes, 256-byte aligned, header as in
+ *    dbf_forward. T == 0 is a no-op. Errors: DBF_ERR_INVALID_ARG,
+ *    DBF_ERR_ALIGNMENT, DBF_ERR_WORKSPACE, DBF_ERR_UNSUPPORTED (sizes whose
+ *    tiles 32 bits cannot count), DBF_ERR_CUDA. */
+dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dtype, void *y, dbf_dtype y_dtype, int64_t T,
+                           int flags, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- 8-bit activations ------------------------------------------------------
+ * A T x C activation kept for the backward pass at a little over one byte a
+ * value: blocks of 32 columns as above, E4M3 codes and one E8M0 scale 2^s, s
+ * the smallest (not below -127) with amax <= 448 * 2^s, so that nothing
+ * saturates; values / 2^s to the nearest code, ties to even (fp32 values from
+ * 1.9375 * 2^127 on thus stand for 2^128 and read back as infinity). A block
+ * with a NaN or an infinity reads back as NaN.
+ * codes: rows of ceil(C/32) * 32 bytes, those past column C zero; scales:
+ * [ceil(C/32)][T]. Both 16-byte aligned. */
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+} dbf_act8;
+
+size_t dbf_act8_code_bytes(int64_t rows, int64_t cols);
+size_t dbf_act8_scale_bytes(int64_t rows, int64_t cols);
+
+/* Keep src (rows x cols, DBF_F32, DBF_BF16 or DBF_F16) in 8 bits, and read it
+ * back: e.g. the x of dbf_backward between forward and backward. rows == 0 is a
+ * no-op. status_dev and errors as dbf_mx4_quantize. */
+dbf_status dbf_act8_save(const void *src, dbf_dtype src_dtype, int64_t rows, int64_t cols, const dbf_act8 *dst,
+                         int32_t *status_dev, void *stream);
+dbf_status dbf_act8_load(const dbf_act8 *src, int64_t rows, int64_t cols, void *dst, dbf_dtype dst_dtype, void *stream);
+
+/* ---- gated feed-forward block over two 4-bit layers -------------------------
+ * g = Wg q(x) [+ g_add],  u = Wu q(x) [+ u_add],  h = act(g) . u, with act
+ * SiLU, g / (1 + e^-g), or GELU in its tanh form. Both products, the
+ * activation and the product of the two run in one kernel. */
+typedef enum { DBF_GATE_SILU = 0, DBF_GATE_GELU = 1 } dbf_gate;
+
+/* Workspace bytes of dbf_mx4_gated_forward (0 for invalid input). */
+size_t dbf_mx4_gated_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T);
+
+/* gate, up: layers of one shape (N x M each). x as in dbf_mx4_forward.
+ * g_add, u_add: optional T x N addends (each may be NULL) of type add_dtype,
+ *    DBF_F32 or DBF_BF16: the branches of adapters on the two projections, as
+ *    dbf_forward writes them.
+ * h: T x N, DBF_F32 or DBF_BF16. save_g, save_u: both or neither; g and u
+ *    (addends included, from their fp32 values) are kept there in 8 bits
+ *    (T x N) for dbf_mx4_gated_backward.
+ * flags: DBF_WEIGHTS_STATIC or 0. All pointers 16-byte aligned.
+ * ws: dbf_mx4_gated_workspace_bytes(gate, up, T) bytes, 256-byte aligned,
+ *    header as in dbf_forward. Errors as dbf_mx4_forward. */
+dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const void *x,
+                                 dbf_dtype x_dtype, const void *g_add, const void *u_add, dbf_dtype add_dtype, void *h,
+                                 dbf_dtype h_dtype, const dbf_act8 *save_g, const dbf_act8 *save_u, int64_t T, int flags,
+                                 void *ws, size_t ws_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *dbf_status_string(dbf_status s);
 
