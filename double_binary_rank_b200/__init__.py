@@ -110,6 +110,11 @@ _SIGS = {
     "dbf_mx4_gated_workspace_bytes": (_sz, [_MP, _MP, _i64]),
     "dbf_mx4_gated_forward": (ctypes.c_int, [_MP, _MP, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp,
                                              ctypes.c_int, _AP, _AP, _i64, ctypes.c_int, _vp, _sz, _vp]),
+    "dbf_mx4_backward_workspace_bytes": (_sz, [_MP, _i64, ctypes.c_int]),
+    "dbf_mx4_backward": (ctypes.c_int, [_MP, _vp, ctypes.c_int, _vp, ctypes.c_int, _i64, ctypes.c_int, _vp, _sz, _vp]),
+    "dbf_mx4_gated_backward_workspace_bytes": (_sz, [_MP, _MP, _i64, ctypes.c_int]),
+    "dbf_mx4_gated_backward": (ctypes.c_int, [_MP, _MP, ctypes.c_int, _AP, _AP, _vp, ctypes.c_int, _vp, _vp, _vp,
+                                              ctypes.c_int, _i64, ctypes.c_int, _vp, _sz, _vp]),
     "dbf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dbf_version": (ctypes.c_char_p, []),
 }
@@ -791,3 +796,66 @@ def mx4_gated_forward(gate: Mx4Layer, up: Mx4Layer, x: torch.Tensor, h: Optional
                                           sg and ctypes.byref(sg), su and ctypes.byref(su), T, _flags(False, static_weights),
                                           _ptr(ws), ws.numel(), s), "dbf_mx4_gated_forward")
     return h
+
+
+def mx4_backward_workspace_bytes(layer: Mx4Layer, T: int, dtype: torch.dtype) -> int:
+    d = layer.descriptor()
+    return int(_lib.dbf_mx4_backward_workspace_bytes(ctypes.byref(d), T, _DT[dtype]))
+
+
+def mx4_backward(layer: Mx4Layer, dy: torch.Tensor, dx: Optional[torch.Tensor] = None, accumulate: bool = False,
+                 ws: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None, static_weights: bool = False,
+                 stream=None) -> torch.Tensor:
+    """dx = [acc] dx + dy W (dbf_mx4_backward). dy: [T, N] float32/bfloat16."""
+    T = dy.shape[0]
+    _need(dy, "dy", (T, layer.N), _ACT, layer.codes)
+    d = layer.descriptor()
+    with _On(dy, stream) as s:
+        if dx is None:
+            if accumulate:
+                raise ValueError("accumulate needs dx")
+            dx = torch.empty((T, layer.M), dtype=dx_dtype or dy.dtype, device=dy.device)
+        _need(dx, "dx", (T, layer.M), _ACT, dy)
+        if ws is None:
+            ws = _scratch(_lib.dbf_mx4_backward_workspace_bytes(ctypes.byref(d), T, _DT[dy.dtype]), dy)
+        _check(_lib.dbf_mx4_backward(ctypes.byref(d), _ptr(dy), _DT[dy.dtype], _ptr(dx), _DT[dx.dtype], T,
+                                     _flags(accumulate, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_backward")
+    return dx
+
+
+def mx4_gated_backward_workspace_bytes(gate: Mx4Layer, up: Mx4Layer, T: int, dtype: torch.dtype) -> int:
+    dg, du = gate.descriptor(), up.descriptor()
+    return int(_lib.dbf_mx4_gated_backward_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T, _DT[dtype]))
+
+
+def mx4_gated_backward(gate: Mx4Layer, up: Mx4Layer, dh: torch.Tensor, saved: Tuple[Act8, Act8], act: str = "silu",
+                       dg: Optional[torch.Tensor] = None, du: Optional[torch.Tensor] = None,
+                       dx: Optional[torch.Tensor] = None, want_dx: bool = True, accumulate: bool = False,
+                       ws: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None,
+                       static_weights: bool = False, stream=None):
+    """(dx, dg, du) of the gated block from dh and the 8-bit g and u that
+    mx4_gated_forward kept (dbf_mx4_gated_backward); dx is None without want_dx."""
+    T, N = dh.shape[0], gate.N
+    _need(dh, "dh", (T, N), _ACT, gate.codes)
+    _need(up.codes, "up.codes", gate.codes.shape, _U8, dh)
+    cg, cu = gate.descriptor(), up.descriptor()
+    sg, su = (_saved(a, T, N, dh) for a in saved)
+    with _On(dh, stream) as s:
+        dg = torch.empty_like(dh) if dg is None else dg
+        du = torch.empty_like(dh) if du is None else du
+        _need(dg, "dg", (T, N), (dh.dtype,), dh)
+        _need(du, "du", (T, N), (dh.dtype,), dh)
+        if want_dx and dx is None:
+            if accumulate:
+                raise ValueError("accumulate needs dx")
+            dx = torch.empty((T, gate.M), dtype=dx_dtype or dh.dtype, device=dh.device)
+        if not want_dx:
+            dx = None
+        _need(dx, "dx", (T, gate.M), _ACT, dh)
+        if ws is None and want_dx:
+            ws = _scratch(_lib.dbf_mx4_gated_backward_workspace_bytes(ctypes.byref(cg), ctypes.byref(cu), T, _DT[dh.dtype]), dh)
+        _check(_lib.dbf_mx4_gated_backward(ctypes.byref(cg), ctypes.byref(cu), _GATES[act], ctypes.byref(sg), ctypes.byref(su),
+                                           _ptr(dh), _DT[dh.dtype], _ptr(dg), _ptr(du), _ptr(dx),
+                                           F32 if dx is None else _DT[dx.dtype], T, _flags(accumulate, static_weights),
+                                           _ptr(ws), 0 if ws is None else ws.numel(), s), "dbf_mx4_gated_backward")
+    return dx, dg, du

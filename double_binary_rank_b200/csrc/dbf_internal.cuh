@@ -148,6 +148,7 @@ cudaError_t gemm_backward(const dbf_layer &L, const uint32_t *b1t, const uint32_
 // ---- 4-bit base layer and 8-bit activations (dbf_mx_*.cu)
 namespace mx {
 struct Product;
+struct Gradient;
 }
 bool mx_size_ok(int64_t rows, int64_t k);
 cudaError_t launch_quantize4(const void *src, dbf_dtype dt, int64_t rows, int64_t k, uint8_t *codes, uint8_t *scales,
@@ -163,6 +164,10 @@ bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats);
 cudaError_t mx_decode(const mx::Product &c, cudaStream_t s);
 size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats);
 cudaError_t mx_gemm(const mx::Product &c, cudaStream_t s);
+size_t mx_back_workspace_bytes(int64_t N, int64_t T, dbf_dtype d, int mats);
+cudaError_t mx_backward(const mx::Gradient &c, cudaStream_t s);
+cudaError_t mx_gated_backward(const mx::Gradient &c, int act, const dbf_act8 &sg, const dbf_act8 &su, void *dg, void *du,
+                              cudaStream_t s);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

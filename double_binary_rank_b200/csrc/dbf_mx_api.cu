@@ -30,6 +30,14 @@ bool tokens_ok(const dbf_mx4_layer *L, int64_t T)
            mx_size_ok(L->N, L->M);
 }
 
+// the gradient's rows, three pieces of each, are counted in 32 bits; its
+// columns, rows of W, are 65535 * 256 at most
+bool gradient_ok(const dbf_mx4_layer *L, int64_t T)
+{
+    return T >= 0 && 3 * T < (int64_t{1} << 31) - 4096 && ((L->M + 255) / 256) * ((T + 31) / 32) < (int64_t{1} << 31) &&
+           mx_size_ok(L->N, L->M) && L->N <= 65535 * 256;
+}
+
 dbf_status check_layer(const dbf_mx4_layer *L)
 {
     if (!L->codes || !L->scales) return DBF_ERR_INVALID_ARG;
@@ -180,6 +188,71 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
     c.ep.N = gate->N, c.ep.T = T;
     c.flags = flags, c.ws = ws;
     return run(c, product_workspace(gate, T, 2), ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t dbf_mx4_backward_workspace_bytes(const dbf_mx4_layer *L, int64_t T, dbf_dtype dy_dtype)
+{
+    if (!layer_shape_ok(L) || !gradient_ok(L, T) || !act_dtype_ok(dy_dtype)) return 0;
+    return mx_back_workspace_bytes(L->N, T, dy_dtype, 1);
+}
+
+dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy_dtype, void *dx, dbf_dtype dx_dtype, int64_t T,
+                            int flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!layer_shape_ok(L) || T < 0 || !act_dtype_ok(dy_dtype) || !act_dtype_ok(dx_dtype) ||
+        (flags & ~(DBF_ACCUMULATE | DBF_WEIGHTS_STATIC)))
+        return DBF_ERR_INVALID_ARG;
+    if (!gradient_ok(L, T)) return DBF_ERR_UNSUPPORTED;
+    if (T == 0) return DBF_OK;
+    if (!dy || !dx) return DBF_ERR_INVALID_ARG;
+    const dbf_status st = check_layer(L);
+    if (st != DBF_OK) return st;
+    if (!aligned(dy, 16) || !aligned(dx, 16)) return DBF_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < mx_back_workspace_bytes(L->N, T, dy_dtype, 1)) return DBF_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return DBF_ERR_ALIGNMENT;
+    mx::Gradient c = {};
+    c.M = L->M, c.N = L->N, c.T = T;
+    c.codes[0] = L->codes, c.scales[0] = L->scales;
+    c.dy = dy, c.dyd = dy_dtype, c.dx = dx, c.dxd = dx_dtype;
+    c.flags = flags, c.ws = ws;
+    return from_cuda(mx_backward(c, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dbf_mx4_gated_backward_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T, dbf_dtype dh_dtype)
+{
+    if (!same_shape(gate, up) || !gradient_ok(gate, T) || !act_dtype_ok(dh_dtype)) return 0;
+    return mx_back_workspace_bytes(gate->N, T, dh_dtype, 2);
+}
+
+dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const dbf_act8 *saved_g,
+                                  const dbf_act8 *saved_u, const void *dh, dbf_dtype dh_dtype, void *dg, void *du, void *dx,
+                                  dbf_dtype dx_dtype, int64_t T, int flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!same_shape(gate, up) || T < 0 || (act != DBF_GATE_SILU && act != DBF_GATE_GELU) || !act_dtype_ok(dh_dtype) ||
+        (dx && !act_dtype_ok(dx_dtype)) || (flags & ~(DBF_ACCUMULATE | DBF_WEIGHTS_STATIC)))
+        return DBF_ERR_INVALID_ARG;
+    if (!gradient_ok(gate, T)) return DBF_ERR_UNSUPPORTED;
+    if (T == 0) return DBF_OK;
+    if (!saved_g || !saved_u || !saved_g->codes || !saved_g->scales || !saved_u->codes || !saved_u->scales || !dh || !dg || !du)
+        return DBF_ERR_INVALID_ARG;
+    if (!aligned(saved_g->codes, 16) || !aligned(saved_g->scales, 16) || !aligned(saved_u->codes, 16) ||
+        !aligned(saved_u->scales, 16) || !aligned(dh, 16) || !aligned(dg, 16) || !aligned(du, 16) || !aligned(dx, 16))
+        return DBF_ERR_ALIGNMENT;
+    mx::Gradient c = {};
+    c.M = gate->M, c.N = gate->N, c.T = T;
+    c.dy = dh, c.dyd = dh_dtype, c.dx = dx, c.dxd = dx_dtype;
+    c.flags = flags;
+    if (dx) {
+        dbf_status st = check_layer(gate);
+        if (st == DBF_OK) st = check_layer(up);
+        if (st != DBF_OK) return st;
+        if (!ws || ws_bytes < mx_back_workspace_bytes(gate->N, T, dh_dtype, 2)) return DBF_ERR_WORKSPACE;
+        if (!aligned(ws, 256)) return DBF_ERR_ALIGNMENT;
+        c.codes[0] = gate->codes, c.scales[0] = gate->scales;
+        c.codes[1] = up->codes, c.scales[1] = up->scales;
+        c.ws = ws;
+    }
+    return from_cuda(mx_gated_backward(c, act, *saved_g, *saved_u, dg, du, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

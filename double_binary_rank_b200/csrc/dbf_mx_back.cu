@@ -1,0 +1,604 @@
+// Gradients through the 4-bit layer and its gated block.
+//
+//   dx = [acc] dx + dy W            (the product's gradient for q(x); the
+//                                    rounding of x is passed straight through)
+//   du = dh act(g), dg = dh u act'(g), dx = [acc] dx + dg Wg + du Wu
+//
+// with g and u as the 8-bit checkpoints hold them. The scales of W run along
+// the columns, which are now the rows of the product and not its contraction,
+// so the block-scaled MMA cannot take them: the codes are expanded on chip to
+// bf16, exactly (E2M1 times a power of two has two significant bits), and the
+// product runs at the bf16 rate with fp32 accumulators. bf16 gradients are
+// operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
+// each (v = p0 + p1 + p2 exactly), three times the products.
+//
+// A CTA pair owns 256 columns of W x 256 tokens of dx, contraction over the
+// rows of W in stages of 64:
+//   warp 0       TMA: 128 token rows of the gradient, 64 columns each;
+//   warps 2..9   expansion: a thread takes 32 codes of one row of W (16 bytes
+//                and a scale, loaded two stages ahead) and writes them as 64
+//                bytes of a 128-byte-swizzled tile whose rows are rows of W:
+//                the A operand in its M-major form, so nothing is transposed;
+//                a warp's lanes hold 32 different rows, whose swizzled chunks
+//                lie in different banks;
+//   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N = w, K = 16);
+//   warps 10..17 epilogue, overlapped with the next tile (two accumulators).
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "dbf_mx_layer.cuh"
+#include "dbf_tc.cuh"
+
+namespace dbf {
+namespace {
+
+using namespace mx;
+using namespace tc;
+
+constexpr int kStages = 6;
+constexpr int kExpand = 8, kEpiWarps = 8;   // warps
+constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
+constexpr int kRowsK = 64;                          // rows of W per stage
+constexpr uint32_t kABytes = 128 * kRowsK * 2, kBBytes = 128 * kRowsK * 2;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kTmemCols = 512;
+
+struct Smem {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain, exit_bar;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Args {
+    const uint8_t *codes[2], *scales[2];
+    int64_t pitch;       // bytes of a row of codes
+    int64_t sf_tiles;    // scale tiles of a row tile
+    int nb;              // blocks of a row of W
+    int N;               // rows of W (contraction)
+    int nn;              // stages of one product: ceil(N / 64)
+    int mats, planes;    // products summed: weights, pieces of the gradient
+    int64_t plane_rows;  // rows from one piece to the next in the gradient's map
+    int w;               // tokens per tile
+    int n_p, tiles;
+    int early;           // W may be read before earlier work is done
+    Epilogue ep;
+    int32_t *status;
+};
+
+// kind::f16 on bf16 operands, A M-major ("transposed"), B K-major
+__device__ __forceinline__ uint32_t bf16_idesc(int n)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(256 >> 4) << 24;
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two codes of a word (nibbles 2i and 2i + 1) as bf16 bit patterns: sign to
+// bit 15, the three magnitude bits to the lowest exponent bits and the highest
+// mantissa bit. That pattern is the code's value times 2^-126 (0.5 becomes a
+// bf16 subnormal), so one multiplication by 2^(126 + s) gives value * 2^s.
+__device__ __forceinline__ uint32_t bf16_pattern(uint32_t w, uint32_t w_hi, int i)
+{
+    // bytes 0 and 2: byte i of the word and of the word shifted by a nibble (the others are masked off below)
+    const uint32_t x = __byte_perm(w, w_hi, ((4u + i) << 8) | i);
+    return ((x << 6) & 0x01C001C0u) | ((x << 12) & 0x80008000u);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Tiles (256 columns of W x w tokens) in column order, so that pairs that run
+// together share the gradient's rows.
+__global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_constant__ CUtensorMap mB0,
+                                                              const __grid_constant__ CUtensorMap mB1,
+                                                              const __grid_constant__ Args g)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Smem *sh = reinterpret_cast<Smem *>(stage0 + kStages * kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+    const int nseg = g.mats * g.planes, nk = nseg * g.nn;
+    volatile int *abort = &sh->abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(&sh->full[i], 1 + 2 * kExpand);
+            bar_init(&sh->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh->acc_full[i], 1);
+            bar_init(&sh->acc_empty[i], 2 * kEpiWarps);
+        }
+        bar_init(&sh->drain, 1);
+        bar_init(&sh->exit_bar, 1);
+        sh->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<2>(&sh->tmem_base, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before either is reached from the other
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            griddep_wait();   // the gradient belongs to earlier work until then
+            const int half_w = g.w / 2;
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int tile = unit; tile < g.tiles && ok; tile += units) {
+                const int tok = tile / g.n_p * g.w + static_cast<int>(rank) * half_w;
+                for (int seg = 0; seg < nseg && ok; ++seg) {
+                    const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
+                    const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
+                    for (int i = 0; i < g.nn; ++i) {
+                        if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) bar_expect_tx(&sh->full[s], 2 * half_w * kRowsK * 2);
+                        tma_2d_pair(stage0 + s * kStageBytes + kABytes, map, i * kRowsK, row, &sh->full[s]);
+                        ++issued;
+                        if (++s == kStages) s = 0, ph ^= 1u;
+                    }
+                }
+            }
+            if (*abort && rank == 0)
+                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                    drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int s = 0, n_tile = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t id = bf16_idesc(g.w);
+            for (int tile = unit; tile < g.tiles && ok; tile += units, ++n_tile) {
+                const int acc = n_tile & 1;
+                ok = bar_wait(&sh->acc_empty[acc], ((n_tile >> 1) & 1u) ^ 1u, abort);
+                if (!ok) break;
+                tc_fence_after();
+                for (int ks = 0; ks < nk; ++ks) {
+                    if (!bar_wait(&sh->full[s], ph, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(stage0) + s * kStageBytes;
+                    // A: 64 columns of W to a 128-byte row; groups of 8 rows 1 KB apart, the second
+                    // 64 columns 8 KB on
+                    const uint64_t a = sw128_desc(st, 1024, 8192), b = sw128_desc(st + kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_pair(tmem + acc * 256, a + kk * (2048 >> 4), b + 2 * kk, id, ks > 0 || kk > 0 ? 1u : 0u);
+                    commit_pair_both(&sh->empty[s]);
+                    if (++s == kStages) s = 0, ph ^= 1u;
+                }
+                if (!ok) break;
+                commit_pair_both(&sh->acc_full[acc]);
+            }
+            if (*abort) {
+                commit_pair_own(&sh->drain);
+                drain_wait(&sh->drain, 0);
+            }
+        }
+    } else if (warp < 2 + kExpand) {
+        if (!g.early) griddep_wait();
+        const int e = warp - 2, q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
+        uint8_t *dst = stage0 + (q >> 1) * 8192 + r * 128;
+        const int chunk0 = (q & 1) * 4;
+        // a cursor over (tile, product, stage) that runs two stages ahead of the expansion
+        struct Cursor {
+            int tile, seg, i;
+        } c = {unit, 0, 0};
+        auto load = [&](uint4 &codes, uint32_t &scale) {
+            codes = make_uint4(0u, 0u, 0u, 0u);
+            scale = 0;
+            if (c.tile >= g.tiles) return;
+            const int block = (c.tile % g.n_p) * 8 + static_cast<int>(rank) * 4 + q;
+            const int n = c.i * kRowsK + r;
+            const int m = c.seg < g.planes ? 0 : 1;
+            if (n < g.N && block < g.nb) {   // others stay zero: they meet zeros of the gradient, or unused rows of dx
+                codes = *reinterpret_cast<const uint4 *>(g.codes[m] + n * g.pitch + block * 16);
+                scale = g.scales[m][scale_at(n, block, g.sf_tiles)];
+            }
+            if (++c.i == g.nn) {
+                c.i = 0;
+                if (++c.seg == nseg) c.seg = 0, c.tile += units;
+            }
+        };
+        uint4 codes[3];
+        uint32_t scale[3];
+        load(codes[0], scale[0]);
+        load(codes[1], scale[1]);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const int64_t total = unit < g.tiles ? static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * nk : 0;
+        for (int64_t k = 0; k < total && ok; ++k) {
+            load(codes[2], scale[2]);
+            // exponent field of 2^(126 + s); what passes 254 is a second factor
+            const uint32_t field = scale[0] + 126u;
+            const uint32_t f1 = scale[0] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
+            const uint32_t f1x2 = f1 | f1 << 16;
+            const uint32_t words[4] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w};
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * j + i] = mul_bf16x2(bf16_pattern(words[j], words[j] >> 4, i), f1x2);
+            if (field > 254u && scale[0] != 255u) {
+                const uint32_t f2 = (127u + field - 254u) << 7, f2x2 = f2 | f2 << 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], f2x2);
+            }
+            ok = bar_wait(&sh->empty[s], ph ^ 1u, abort);
+            if (!ok) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(dst + s * kStageBytes + (((chunk0 + j) ^ (r & 7)) << 4)) =
+                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive_leader(&sh->full[s]);
+            if (++s == kStages) s = 0, ph ^= 1u;
+            codes[0] = codes[1], scale[0] = scale[1];
+            codes[1] = codes[2], scale[1] = scale[2];
+        }
+    } else {
+        griddep_wait();
+        griddep_launch();   // all earlier work is done
+        const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2;
+        int n_tile = 0;
+        for (int tile = unit; tile < g.tiles; tile += units, ++n_tile) {
+            const int acc = n_tile & 1;
+            if (!bar_wait(&sh->acc_full[acc], (n_tile >> 1) & 1u, abort)) break;
+            tc_fence_after();
+            const int64_t t0 = static_cast<int64_t>(tile / g.n_p) * g.w;
+            const int n = (tile % g.n_p) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            const uint32_t from = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+            for (int j0 = half * 16; j0 < g.w; j0 += 32) {
+                float v[16];
+                tmem_ld16(from + j0, v);
+                const int64_t left = g.ep.T - (t0 + j0);
+                if (left > 0) finish_plain(g.ep, t0 + j0, static_cast<int>(left < 16 ? left : 16), n, v);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_leader(&sh->acc_empty[acc]);
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    // neither CTA ends while the other may still reach its shared memory
+    if (threadIdx.x == 0) {
+        bar_arrive_rank(&sh->exit_bar, rank ^ 1u);
+        drain_wait(&sh->exit_bar, 0);
+        if (sh->abort && g.status) atomicExch(g.status, static_cast<int32_t>(DBF_ERR_TIMEOUT));
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<2>(tmem, kTmemCols);
+    }
+}
+
+// fp32 to three bf16 pieces by truncation: p0 the upper half of the word, then
+// the same of what is left (each difference is exact); the last has at most
+// eight bits left. A NaN or an infinity stays whole in p0.
+__device__ __forceinline__ void split3(float v, uint16_t (&p)[3])
+{
+    const uint32_t b = __float_as_uint(v);
+    if ((b & 0x7F800000u) == 0x7F800000u) {
+        p[0] = static_cast<uint16_t>((b >> 16) | ((b & 0x7FFFFFu) ? 0x40u : 0u));
+        p[1] = p[2] = 0;
+        return;
+    }
+    p[0] = static_cast<uint16_t>(b >> 16);
+    const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
+    p[1] = static_cast<uint16_t>(__float_as_uint(r1) >> 16);
+    const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
+    p[2] = static_cast<uint16_t>(__float_as_uint(r2) >> 16);
+}
+
+// Eight gradient values to the product's operand planes [planes][T][ld].
+__device__ __forceinline__ void store_planes(uint16_t *op, int64_t ld, int64_t plane, int64_t t, int64_t c, int planes,
+                                             const float (&v)[8])
+{
+    uint16_t p[8][3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (planes == 3)
+            split3(v[i], p[i]);
+        else
+            p[i][0] = static_cast<uint16_t>(__float_as_uint(v[i]) >> 16);   // a bf16 value already
+    }
+    for (int k = 0; k < planes; ++k) {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = static_cast<uint32_t>(k == 0 ? p[2 * i][0] : k == 1 ? p[2 * i][1] : p[2 * i][2]) |
+                   static_cast<uint32_t>(k == 0 ? p[2 * i + 1][0] : k == 1 ? p[2 * i + 1][1] : p[2 * i + 1][2]) << 16;
+        *reinterpret_cast<uint4 *>(op + k * plane + t * ld + c) = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+}
+
+// dy to operand planes where it cannot be an operand itself (fp32, or rows
+// that are no multiple of 16 bytes).
+__global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy, dbf_dtype dt, int64_t T, int64_t N, bool vec,
+                                                     uint16_t *__restrict__ op, int64_t ld, int planes)
+{
+    griddep_wait();
+    griddep_launch();
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31)) * 8;
+    if (c >= ld) return;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += static_cast<int64_t>(gridDim.x) * 8) {
+        float v[8];
+        load8(dy, dt, t * N, c, N, vec, v);
+        store_planes(op, ld, T * ld, t, c, planes, v);
+    }
+}
+
+// dg and du of 32 tokens x 256 columns from dh and the 8-bit g and u, and their
+// operand planes where op_g is set.
+struct GateArgs {
+    const uint8_t *g8, *gs, *u8, *us;
+    const void *dh;
+    void *dg, *du;
+    uint16_t *op_g, *op_u;
+    int64_t T, N, pitch8, ld;
+    int act, planes;
+    bool vec;
+};
+
+template <dbf_dtype DT>
+__global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateArgs a)
+{
+    __shared__ uint8_t sc[2][8][32];
+    griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+    const int64_t b = static_cast<int64_t>(blockIdx.y) * 8 + warp;
+    const bool has = b < blocks(a.N) && r0 + lane < a.T;
+    sc[0][warp][lane] = has ? a.gs[b * a.T + r0 + lane] : 0;
+    sc[1][warp][lane] = has ? a.us[b * a.T + r0 + lane] : 0;
+    __syncthreads();
+    if (c >= a.pitch8) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = r0 + 8 * i + warp;
+        if (t >= a.T) break;
+        const uint2 wg = *reinterpret_cast<const uint2 *>(a.g8 + t * a.pitch8 + c);
+        const uint2 wu = *reinterpret_cast<const uint2 *>(a.u8 + t * a.pitch8 + c);
+        float dh[8], g[8], u[8];
+        load8(a.dh, DT, t * a.N, c, a.N, a.vec, dh);
+        const float sg = scale_value(sc[0][lane >> 2][8 * i + warp]), su = scale_value(sc[1][lane >> 2][8 * i + warp]);
+        float q[4];
+        from_e4m3x4(wg.x, q);
+        g[0] = q[0] * sg, g[1] = q[1] * sg, g[2] = q[2] * sg, g[3] = q[3] * sg;
+        from_e4m3x4(wg.y, q);
+        g[4] = q[0] * sg, g[5] = q[1] * sg, g[6] = q[2] * sg, g[7] = q[3] * sg;
+        from_e4m3x4(wu.x, q);
+        u[0] = q[0] * su, u[1] = q[1] * su, u[2] = q[2] * su, u[3] = q[3] * su;
+        from_e4m3x4(wu.y, q);
+        u[4] = q[0] * su, u[5] = q[1] * su, u[6] = q[2] * su, u[7] = q[3] * su;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float value;
+            const float slope = gate_slope(a.act, g[j], value);
+            g[j] = dh[j] * u[j] * slope;
+            u[j] = dh[j] * value;
+            if (DT == DBF_BF16) {
+                g[j] = __bfloat162float(__float2bfloat16_rn(g[j]));
+                u[j] = __bfloat162float(__float2bfloat16_rn(u[j]));
+            }
+            if (c + j >= a.N) g[j] = u[j] = 0.0f;
+        }
+        const int64_t at = t * a.N + c;
+        if (a.vec && c < a.N) {   // N is a multiple of 8
+            if (DT == DBF_F32) {
+                float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.dg) + at);
+                p[0] = make_float4(g[0], g[1], g[2], g[3]), p[1] = make_float4(g[4], g[5], g[6], g[7]);
+                p = reinterpret_cast<float4 *>(static_cast<float *>(a.du) + at);
+                p[0] = make_float4(u[0], u[1], u[2], u[3]), p[1] = make_float4(u[4], u[5], u[6], u[7]);
+            } else {
+                uint32_t x[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = __float_as_uint(g[2 * j]) >> 16 | (__float_as_uint(g[2 * j + 1]) & 0xFFFF0000u);
+                    y[j] = __float_as_uint(u[2 * j]) >> 16 | (__float_as_uint(u[2 * j + 1]) & 0xFFFF0000u);
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dg) + at) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.du) + at) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (c + j >= a.N) break;
+                store_act(a.dg, DT, at + j, g[j]);
+                store_act(a.du, DT, at + j, u[j]);
+            }
+        }
+        if (a.op_g && c < a.ld) {
+            store_planes(a.op_g, a.ld, a.T * a.ld, t, c, a.planes, g);
+            store_planes(a.op_u, a.ld, a.T * a.ld, t, c, a.planes, u);
+        }
+    }
+}
+
+int resident_pairs(cudaLaunchConfig_t cfg)
+{
+    static std::mutex lock;
+    static std::map<int, int> known;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> guard(lock);
+    auto it = known.find(dev);
+    if (it == known.end()) {
+        const int pairs = std::max(1, device_sms() / 2);
+        cfg.gridDim = dim3(2 * pairs);
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, mx_back_kernel, &cfg);
+        (void)cudaGetLastError();
+        it = known.emplace(dev, e == cudaSuccess && n > 0 ? std::min(n, pairs) : pairs).first;
+    }
+    return it->second;
+}
+
+// Tokens per tile: the width whose waves of tiles end first; below 128 tokens
+// the expansion of W, the same for every width, bounds a stage.
+int tile_width(int64_t M, int64_t T)
+{
+    const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    int best = 32;
+    double least = 0;
+    for (int w = 32; w <= 256; w += 32) {
+        const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
+        const double cost = static_cast<double>(waves) * std::max(128.0, static_cast<double>(w));
+        if (w == 32 || cost <= least) least = cost, best = w;
+        if (w >= T) break;
+    }
+    return best;
+}
+
+int64_t operand_ld(int64_t N) { return (N + 7) / 8 * 8; }
+bool direct_operand(int64_t N, dbf_dtype d) { return d == DBF_BF16 && N % 8 == 0; }
+size_t plane_bytes(int64_t N, int64_t T, dbf_dtype d)
+{
+    return align_up(static_cast<size_t>(T * operand_ld(N)) * 2 * (d == DBF_F32 ? 3 : 1), 256);
+}
+
+struct PdlAttr {
+    cudaLaunchAttribute attr[2];
+    PdlAttr()
+    {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    }
+};
+
+// dx from the operands (one map per weight)
+cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, int planes, bool pre, cudaStream_t s)
+{
+    const int mats = c.codes[1] ? 2 : 1;
+    const int w = tile_width(c.M, c.T);
+    CUtensorMap map[2];
+    for (int m = 0; m < 2; ++m) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.T * planes)};
+        const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
+        const uint32_t box[2] = {kRowsK, static_cast<uint32_t>(w / 2)};
+        if (!tc_map(&map[m], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, operand[m < mats ? m : 0], dims, strides, box, true))
+            return cudaErrorInvalidValue;
+    }
+    Args g = {};
+    for (int m = 0; m < 2; ++m) g.codes[m] = c.codes[m], g.scales[m] = c.scales[m];
+    g.pitch = code_pitch(c.M);
+    g.sf_tiles = scale_tiles(c.M);
+    g.nb = static_cast<int>(blocks(c.M));
+    g.N = static_cast<int>(c.N);
+    g.nn = static_cast<int>((c.N + kRowsK - 1) / kRowsK);
+    g.mats = mats;
+    g.planes = planes;
+    g.plane_rows = c.T;
+    g.w = w;
+    g.n_p = static_cast<int>((c.M + 255) / 256);
+    g.tiles = static_cast<int>(g.n_p * ((c.T + w - 1) / w));
+    g.early = pre || (c.flags & DBF_WEIGHTS_STATIC) ? 1 : 0;
+    g.ep.y = c.dx, g.ep.yd = c.dxd, g.ep.accumulate = c.flags & DBF_ACCUMULATE ? 1 : 0;
+    g.ep.N = static_cast<int32_t>(c.M), g.ep.T = c.T;
+    g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
+
+    const int smem = 1024 + kStages * kStageBytes + sizeof(Smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(mx_back_kernel), smem);
+    if (e != cudaSuccess) return e;
+    PdlAttr attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr.attr + 1;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2 * std::min(resident_pairs(cfg), g.tiles));
+    cfg.attrs = attr.attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mx_back_kernel, map[0], map[1], g);
+}
+
+}  // namespace
+
+size_t mx_back_workspace_bytes(int64_t N, int64_t T, dbf_dtype d, int mats)
+{
+    return kWsHeaderBytes + (direct_operand(N, d) ? 0 : mats * plane_bytes(N, T, d));
+}
+
+cudaError_t mx_backward(const Gradient &c, cudaStream_t s)
+{
+    const void *operand[2] = {c.dy, nullptr};
+    const int planes = c.dyd == DBF_F32 ? 3 : 1;
+    if (direct_operand(c.N, c.dyd)) return product(c, operand, c.N, 1, false, s);
+    uint16_t *op = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
+    const int64_t ld = operand_ld(c.N);
+    PdlAttr attr;
+    cudaLaunchConfig_t pre = {};
+    pre.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((c.T + 7) / 8, 1 << 20)), static_cast<unsigned>((ld / 8 + 31) / 32));
+    pre.blockDim = dim3(256);
+    pre.stream = s;
+    pre.attrs = attr.attr;
+    pre.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&pre, planes_kernel, c.dy, c.dyd, c.T, c.N, c.N % 8 == 0, op, ld, planes);
+    if (e != cudaSuccess) return e;
+    operand[0] = op;
+    return product(c, operand, ld, planes, true, s);
+}
+
+cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, const dbf_act8 &su, void *dg, void *du, cudaStream_t s)
+{
+    const bool want = c.dx != nullptr, direct = direct_operand(c.N, c.dyd);
+    GateArgs a = {};
+    a.g8 = sg.codes, a.gs = sg.scales, a.u8 = su.codes, a.us = su.scales;
+    a.dh = c.dy, a.dg = dg, a.du = du;
+    a.T = c.T, a.N = c.N, a.pitch8 = blocks(c.N) * kBlock, a.ld = operand_ld(c.N);
+    a.act = act;
+    a.planes = c.dyd == DBF_F32 ? 3 : 1;
+    a.vec = c.N % 8 == 0;
+    const void *operand[2] = {dg, du};
+    if (want && !direct) {
+        a.op_g = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
+        a.op_u = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(a.op_g) + plane_bytes(c.N, c.T, c.dyd));
+        operand[0] = a.op_g, operand[1] = a.op_u;
+    }
+    PdlAttr attr;
+    cudaLaunchConfig_t pre = {};
+    pre.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.N + 255) / 256));
+    pre.blockDim = dim3(256);
+    pre.stream = s;
+    pre.attrs = attr.attr;
+    pre.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&pre, c.dyd == DBF_F32 ? gate_back_kernel<DBF_F32> : gate_back_kernel<DBF_BF16>, a);
+    if (e != cudaSuccess || !want) return e;
+    return product(c, operand, direct ? c.N : a.ld, direct ? 1 : a.planes, true, s);
+}
+
+}  // namespace dbf

@@ -189,16 +189,16 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
         const uint32_t base = smem_u32(part);
         for (int u = rank + S * (warp - 2); u < 4 * g.T; u += S * kWorkers) {
             const int t = u >> 2, r = (u & 3) * 32 + lane;
-            float sum[kMats];
+            float sum[kMats][1];
 #pragma unroll
             for (int m = 0; m < kMats; ++m) {
-                sum[m] = 0.0f;
-                for (int s = 0; s < S; ++s) sum[m] += ld_cluster_f32(base + ((m * g.w + t) * 128 + r) * 4, s);
+                sum[m][0] = 0.0f;
+                for (int s = 0; s < S; ++s) sum[m][0] += ld_cluster_f32(base + ((m * g.w + t) * 128 + r) * 4, s);
             }
             if (kGated)
-                finish_gated(g.ep, t, row0 + r, sum[0], sum[kMats - 1]);
+                finish_gated(g.ep, t, 1, row0 + r, sum[0], sum[kMats - 1]);
             else
-                finish_plain(g.ep, t, row0 + r, sum[0]);
+                finish_plain(g.ep, t, 1, row0 + r, sum[0]);
         }
     }
     __syncwarp();

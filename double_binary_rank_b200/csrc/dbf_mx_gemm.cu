@@ -62,6 +62,8 @@ struct Args {
     int32_t *status;
 };
 
+__device__ __forceinline__ int tokens_left(int64_t T, int64_t t) { return static_cast<int>(T - t < 16 ? T - t : 16); }
+
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1, const __grid_constant__ CUtensorMap mS0,
@@ -202,9 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                     float vg[16], vu[16];
                     tmem_ld16(lanes + j0, vg);
                     tmem_ld16(lanes + g.w + j0, vu);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (t0 + j0 + j < g.ep.T) finish_gated(g.ep, t0 + j0 + j, n, vg[j], vu[j]);
+                    const int count = tokens_left(g.ep.T, t0 + j0);
+                    if (count > 0) finish_gated(g.ep, t0 + j0, count, n, vg, vu);
                 }
             } else {
                 // each of the two warps takes one accumulator
@@ -212,9 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                 for (int j0 = 0; j0 < g.w; j0 += 16) {
                     float v[16];
                     tmem_ld16(lanes + half * g.w + j0, v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (t0 + j0 + j < g.ep.T) finish_plain(g.ep, t0 + j0 + j, n, v[j]);
+                    const int count = tokens_left(g.ep.T, t0 + j0);
+                    if (count > 0) finish_plain(g.ep, t0 + j0, count, n, v);
                 }
             }
             tc_fence_before();

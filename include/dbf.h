@@ -518,6 +518,20 @@ size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T);
 dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dtype, void *y, dbf_dtype y_dtype, int64_t T,
                            int flags, void *ws, size_t ws_bytes, void *stream);
 
+/* Gradient of dbf_mx4_forward for the values it multiplies: dx = [acc] dx +
+ * dy W. The rounding of x to q(x) is passed straight through. W is expanded
+ * exactly and bf16 gradients are used as they are; fp32 ones are cut into three
+ * bf16 pieces that add up to them (parts below 2^-133 are lost), so products
+ * are exact and sums fp32.
+ * dy: T x N and dx: T x M, DBF_F32 or DBF_BF16, 16-byte aligned, not
+ *    overlapping. flags: DBF_ACCUMULATE | DBF_WEIGHTS_STATIC.
+ * ws: dbf_mx4_backward_workspace_bytes(L, T, dy_dtype) bytes, 256-byte
+ *    aligned, header as in dbf_forward. T == 0 is a no-op. Errors as
+ *    dbf_mx4_forward (DBF_ERR_UNSUPPORTED also for N above 65535 * 256). */
+size_t dbf_mx4_backward_workspace_bytes(const dbf_mx4_layer *L, int64_t T, dbf_dtype dy_dtype);
+dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy_dtype, void *dx, dbf_dtype dx_dtype, int64_t T,
+                            int flags, void *ws, size_t ws_bytes, void *stream);
+
 /* ---- 8-bit activations ------------------------------------------------------
  * A T x C activation kept for the backward pass at a little over one byte a
  * value: blocks of 32 columns as above, E4M3 codes and one E8M0 scale 2^s, s
@@ -565,6 +579,24 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
                                  dbf_dtype x_dtype, const void *g_add, const void *u_add, dbf_dtype add_dtype, void *h,
                                  dbf_dtype h_dtype, const dbf_act8 *save_g, const dbf_act8 *save_u, int64_t T, int flags,
                                  void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of the gated block from dh = dL/dh and the 8-bit g and u that
+ * dbf_mx4_gated_forward kept, with the values these stand for:
+ *   du = dh . act(g),  dg = dh . u . act'(g)        (T x N, in dh's type)
+ *   dx = [acc] dx + dg Wg + du Wu                   (T x M; dg and du as stored)
+ * dg and du are also what the adapters on the two projections take as their
+ * dy (dbf_backward). dx NULL: only dg and du; the layers' codes and scales are
+ * not read then and ws may be NULL.
+ * saved_g, saved_u: T x N. dh, dg, du: T x N, DBF_F32 or DBF_BF16; all
+ *    16-byte aligned; dg and du overlap neither each other nor dh.
+ * flags: DBF_ACCUMULATE (dx) | DBF_WEIGHTS_STATIC.
+ * ws: dbf_mx4_gated_backward_workspace_bytes(gate, up, T, dh_dtype) bytes,
+ *    256-byte aligned, header as in dbf_forward. T == 0 is a no-op. Errors as
+ *    dbf_mx4_backward. */
+size_t dbf_mx4_gated_backward_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T, dbf_dtype dh_dtype);
+dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const dbf_act8 *saved_g,
+                                  const dbf_act8 *saved_u, const void *dh, dbf_dtype dh_dtype, void *dg, void *du, void *dx,
+                                  dbf_dtype dx_dtype, int64_t T, int flags, void *ws, size_t ws_bytes, void *stream);
 
 /* Static description of a status code. */
 const char *dbf_status_string(dbf_status s);

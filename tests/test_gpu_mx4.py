@@ -192,3 +192,55 @@ def test_gated_forward(dbf, T, M, N, act, add):
         assert np.array_equal(a.scales.cpu().numpy(), byte.T.astype(np.uint8))
     hb = dbf.mx4_gated_forward(gl, ul, t, act=act, h_dtype=torch.bfloat16, **kw)
     assert np.all(np.abs(host(hb) - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
+
+
+# ---- gradients
+@pytest.mark.parametrize("T,M,N", [(1, 1, 1), (1, 32, 8), (2, 33, 5), (3, 64, 129), (16, 256, 128), (17, 1000, 130), (33, 2048, 257),
+                                   (65, 512, 512), (77, 1000, 2200), (130, 288, 640), (257, 520, 64), (300, 95, 511), (1000, 768, 1536)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_backward_is_exact(dbf, T, M, N, kind):
+    """Whole-number gradients (up to 100, or up to 2^15 + 1 in fp32, which needs three pieces) and exact weights."""
+    rng = np.random.default_rng(T * 7 + M * 3 + N)
+    w = exact_operand(rng, N, M)
+    dy = rng.integers(-100, 101, (T, N)).astype(np.float64)
+    if kind == "f32" and N <= 512:   # terms below 2^15 * 24, sums below 2^24 units of 0.5 for a handful of them
+        big = rng.random((T, N)) < 1.0 / N
+        dy = np.where(big, rng.integers(-(2 ** 15) - 1, 2 ** 15 + 2, (T, N)), np.sign(dy))
+    ref = dy @ w
+    assert np.max(np.abs(dy) @ np.abs(w)) < 2 ** 23   # every partial sum is a multiple of 0.5 below 2^23
+    t = torch.tensor(dy).to(DT[kind]).cuda()
+    L = layer_of(dbf, w)
+    assert np.array_equal(host(dbf.mx4_backward(L, t, dx_dtype=torch.float32)), ref)
+    acc = dbf.mx4_backward(L, t, dx=torch.full((T, M), -3.0, device="cuda"), accumulate=True)
+    assert np.array_equal(host(acc), ref - 3)
+    b = dbf.mx4_backward(L, t, dx_dtype=torch.bfloat16)
+    assert torch.equal(b.cpu(), torch.tensor(ref).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,M,N", [(1, 32, 8), (2, 33, 5), (70, 300, 1000), (129, 512, 264), (33, 95, 255)])
+def test_gated_backward(dbf, T, M, N, act, kind):
+    rng = np.random.default_rng(T + N)
+    wg, wu = (rng.standard_normal((N, M)) / np.sqrt(N) for _ in range(2))
+    g, u, dh = rng.standard_normal((T, N)) * 3, rng.standard_normal((T, N)), rng.standard_normal((T, N))
+    g[0, 0], u[0, 0] = 0.0, 0.0
+    saved = tuple(dbf.act8_save(torch.tensor(v, dtype=torch.float32).cuda()) for v in (g, u))
+    t = torch.tensor(dh).to(DT[kind]).cuda()
+    g, u = (R.act8(v.astype(np.float32))[0] for v in (g, u))
+    dh = host(t)
+    dg, du = dh * u * R.gate_slope(act, g), dh * R.gate(act, g)
+    gl, ul = layer_of(dbf, wg), layer_of(dbf, wu)
+    dx, gg, gu = dbf.mx4_gated_backward(gl, ul, t, saved, act=act, dx_dtype=torch.float32)
+    tol = gate_tol(g) * (1 + np.abs(g)) * np.abs(dh)
+    for got, ref, by in ((gg, dg, np.abs(u)), (gu, du, 1.0)):
+        assert got.dtype == DT[kind]
+        assert np.all(np.abs(host(got) - ref) <= tol * by + STEP[kind] * (np.abs(ref) + tol * by) + 1e-37)
+    # dx is the gradient of what the block hands on
+    gg, gu = host(gg), host(gu)
+    wgq, wuq = R.mx4(wg.astype(np.float32))[0], R.mx4(wu.astype(np.float32))[0]
+    ref, S = gg @ wgq + gu @ wuq, np.abs(gg) @ np.abs(wgq) + np.abs(gu) @ np.abs(wuq)
+    pieces = 3 if kind == "f32" else 1
+    assert np.all(np.abs(host(dx) - ref) <= 2 * pieces * N * 2.0 ** -23 * S + 1e-37)
+    none, g2, u2 = dbf.mx4_gated_backward(gl, ul, t, saved, act=act, want_dx=False)
+    assert none is None and np.array_equal(host(g2), gg) and np.array_equal(host(u2), gu)
