@@ -154,6 +154,86 @@ __device__ __forceinline__ void load8(const void *src, dbf_dtype dt, int64_t row
     }
 }
 
+// The reverse: eight values to columns c .. c + 7 of a row, those at or past k
+// left out.
+__device__ __forceinline__ void store8(void *dst, dbf_dtype dt, int64_t row_start, int64_t c, int64_t k, bool vec,
+                                       const float (&v)[8])
+{
+    if (c >= k) return;
+    const int64_t at = row_start + c;
+    if (vec) {
+        if (dt == DBF_F32) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(dst) + at);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (dt == DBF_BF16) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    q[i] = *reinterpret_cast<const uint32_t *>(&b);
+                } else {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    q[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (c + i >= k) break;
+        if (dt == DBF_F16)
+            static_cast<__half *>(dst)[at + i] = __float2half_rn(v[i]);
+        else
+            store_act(dst, dt, at + i, v[i]);
+    }
+}
+
+// Eight values as loaded, so that the load can be issued long before its
+// conversion: bf16 in 'lo', fp32 in both.
+struct Raw8 {
+    uint4 lo, hi;
+};
+__device__ __forceinline__ Raw8 load_raw8(const void *src, dbf_dtype dt, int64_t row_start, int64_t c, int64_t k, bool vec)
+{
+    Raw8 r;
+    r.lo = r.hi = make_uint4(0u, 0u, 0u, 0u);
+    if (c >= k) return r;
+    const int64_t at = row_start + c;
+    if (vec) {
+        if (dt == DBF_F32) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + at);
+            r.lo = p[0], r.hi = p[1];
+        } else {
+            r.lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at);
+        }
+        return r;
+    }
+    float v[8];
+    load8(src, dt, row_start, c, k, false, v);
+    r.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    r.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    return r;
+}
+// v += the eight values
+__device__ __forceinline__ void add_raw8(const Raw8 &r, dbf_dtype dt, bool vec, float (&v)[8])
+{
+    const uint32_t a[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if (dt == DBF_F32 || !vec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(a[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += __uint_as_float(a[i] << 16);
+            v[2 * i + 1] += __uint_as_float(a[i] & 0xFFFF0000u);
+        }
+    }
+}
+
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
 {
     uint32_t m = 0;

@@ -16,7 +16,7 @@
 // rows of W in stages of 64:
 //   warp 0       TMA: 128 token rows of the gradient, 64 columns each;
 //   warps 2..9   expansion: a thread takes 32 codes of one row of W (16 bytes
-//                and a scale, loaded two stages ahead) and writes them as 64
+//                and a scale, loaded four stages ahead) and writes them as 64
 //                bytes of a 128-byte-swizzled tile whose rows are rows of W:
 //                the A operand in its M-major form, so nothing is transposed;
 //                a warp's lanes hold 32 different rows, whose swizzled chunks
@@ -39,6 +39,7 @@ using namespace tc;
 constexpr int kStages = 6;
 constexpr int kExpand = 8, kEpiWarps = 8;   // warps
 constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
+constexpr int kAhead = 4;                           // stages that the expansion's loads run ahead
 constexpr int kRowsK = 64;                          // rows of W per stage
 constexpr uint32_t kABytes = 128 * kRowsK * 2, kBBytes = 128 * kRowsK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
@@ -106,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
 {
     extern __shared__ uint8_t raw[];
     uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Smem *sh = reinterpret_cast<Smem *>(stage0 + kStages * kStageBytes);
+    float *turn = reinterpret_cast<float *>(stage0 + kStages * kStageBytes);
+    Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kTurnFloats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
@@ -202,81 +204,98 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
         const int e = warp - 2, q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
         uint8_t *dst = stage0 + (q >> 1) * 8192 + r * 128;
         const int chunk0 = (q & 1) * 4;
-        // a cursor over (tile, product, stage) that runs two stages ahead of the expansion
-        struct Cursor {
-            int tile, seg, i;
-        } c = {unit, 0, 0};
+        // A cursor over (tile, product, stage) runs kAhead stages ahead of the
+        // expansion; its loads land in slots with fixed names, so that nothing
+        // waits for a load before the stage that uses it.
+        const uint8_t *code_at = nullptr, *scale_base = nullptr;
+        int tile = unit, seg = -1, i = g.nn, block = 0, left = 0;   // left: rows of W from this thread's on
         auto load = [&](uint4 &codes, uint32_t &scale) {
+            if (i == g.nn) {
+                i = 0;
+                if (++seg == nseg) seg = 0, tile += units;
+                block = (tile % g.n_p) * 8 + static_cast<int>(rank) * 4 + q;
+                const int m = seg < g.planes ? 0 : 1;
+                // columns past the last stay zero (rows of dx that are not stored)
+                left = tile < g.tiles && block < g.nb ? g.N - r : 0;
+                code_at = g.codes[m] + r * g.pitch + block * 16;
+                scale_base = g.scales[m];
+            }
             codes = make_uint4(0u, 0u, 0u, 0u);
             scale = 0;
-            if (c.tile >= g.tiles) return;
-            const int block = (c.tile % g.n_p) * 8 + static_cast<int>(rank) * 4 + q;
-            const int n = c.i * kRowsK + r;
-            const int m = c.seg < g.planes ? 0 : 1;
-            if (n < g.N && block < g.nb) {   // others stay zero: they meet zeros of the gradient, or unused rows of dx
-                codes = *reinterpret_cast<const uint4 *>(g.codes[m] + n * g.pitch + block * 16);
-                scale = g.scales[m][scale_at(n, block, g.sf_tiles)];
+            if (left > 0) {   // rows past the last stay zero (they meet zeros of the gradient)
+                codes = *reinterpret_cast<const uint4 *>(code_at);
+                scale = scale_base[scale_at(i * kRowsK + r, block, g.sf_tiles)];
             }
-            if (++c.i == g.nn) {
-                c.i = 0;
-                if (++c.seg == nseg) c.seg = 0, c.tile += units;
-            }
+            ++i;
+            left -= kRowsK;
+            code_at += kRowsK * g.pitch;
         };
-        uint4 codes[3];
-        uint32_t scale[3];
-        load(codes[0], scale[0]);
-        load(codes[1], scale[1]);
+        uint4 codes[kAhead];
+        uint32_t scale[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) load(codes[a], scale[a]);
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        const int64_t total = unit < g.tiles ? static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * nk : 0;
-        for (int64_t k = 0; k < total && ok; ++k) {
-            load(codes[2], scale[2]);
-            // exponent field of 2^(126 + s); what passes 254 is a second factor
-            const uint32_t field = scale[0] + 126u;
-            const uint32_t f1 = scale[0] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
-            const uint32_t f1x2 = f1 | f1 << 16;
-            const uint32_t words[4] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w};
-            uint32_t v[16];
+        const int64_t total = static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * nk;   // unit < tiles
+        for (int64_t k = 0; k < total && ok; k += kAhead) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int a = 0; a < kAhead; ++a) {
+                if (k + a >= total) break;
+                // exponent field of 2^(126 + s); what passes 254 is a second factor
+                const uint32_t field = scale[a] + 126u;
+                const uint32_t f1 = scale[a] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
+                const uint32_t f1x2 = f1 | f1 << 16;
+                const uint32_t words[4] = {codes[a].x, codes[a].y, codes[a].z, codes[a].w};
+                uint32_t v[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[4 * j + i] = mul_bf16x2(bf16_pattern(words[j], words[j] >> 4, i), f1x2);
-            if (field > 254u && scale[0] != 255u) {
-                const uint32_t f2 = (127u + field - 254u) << 7, f2x2 = f2 | f2 << 16;
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], f2x2);
+                    for (int b = 0; b < 4; ++b) v[4 * j + b] = mul_bf16x2(bf16_pattern(words[j], words[j] >> 4, b), f1x2);
+                if (field > 254u && scale[a] != 255u) {
+                    const uint32_t f2 = (127u + field - 254u) << 7, f2x2 = f2 | f2 << 16;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = mul_bf16x2(v[j], f2x2);
+                }
+                load(codes[a], scale[a]);
+                ok = bar_wait(&sh->empty[s], ph ^ 1u, abort);
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4 *>(dst + s * kStageBytes + (((chunk0 + j) ^ (r & 7)) << 4)) =
+                        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive_leader(&sh->full[s]);
+                if (++s == kStages) s = 0, ph ^= 1u;
             }
-            ok = bar_wait(&sh->empty[s], ph ^ 1u, abort);
-            if (!ok) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4 *>(dst + s * kStageBytes + (((chunk0 + j) ^ (r & 7)) << 4)) =
-                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive_leader(&sh->full[s]);
-            if (++s == kStages) s = 0, ph ^= 1u;
-            codes[0] = codes[1], scale[0] = scale[1];
-            codes[1] = codes[2], scale[1] = scale[2];
         }
     } else {
         griddep_wait();
         griddep_launch();   // all earlier work is done
         const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2;
+        float *own = turn + (warp - 2 - kExpand) * kTurnFloats;
         int n_tile = 0;
         for (int tile = unit; tile < g.tiles; tile += units, ++n_tile) {
             const int acc = n_tile & 1;
+            const int64_t t = static_cast<int64_t>(tile / g.n_p) * g.w + (lane >> 2);
+            const int n = (tile % g.n_p) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + (lane & 3) * 8;
+            Raw8 x[2][1];   // what a chunk of 8 tokens reads is asked for a chunk ahead
+            epilogue_reads<false>(g.ep, t + half * 8, n, t + half * 8 < g.ep.T, x[0]);
             if (!bar_wait(&sh->acc_full[acc], (n_tile >> 1) & 1u, abort)) break;
             tc_fence_after();
-            const int64_t t0 = static_cast<int64_t>(tile / g.n_p) * g.w;
-            const int n = (tile % g.n_p) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
             const uint32_t from = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int j0 = half * 16; j0 < g.w; j0 += 32) {
-                float v[16];
-                tmem_ld16(from + j0, v);
-                const int64_t left = g.ep.T - (t0 + j0);
-                if (left > 0) finish_plain(g.ep, t0 + j0, static_cast<int>(left < 16 ? left : 16), n, v);
+            for (int j0 = half * 8; j0 < g.w; j0 += 32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + i * 16, next = j + 16;
+                    if (j >= g.w) break;
+                    epilogue_reads<false>(g.ep, t + next, n, next < g.w && t + next < g.ep.T, x[i ^ 1]);
+                    float col[1][8], row[1][8];
+                    tmem_ld8(from + j, col);
+                    turn8<1>(own, col, row);
+                    epilogue_finish<false>(g.ep, t + j, n, t + j < g.ep.T, x[i], row);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -413,31 +432,8 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ 
             }
             if (c + j >= a.N) g[j] = u[j] = 0.0f;
         }
-        const int64_t at = t * a.N + c;
-        if (a.vec && c < a.N) {   // N is a multiple of 8
-            if (DT == DBF_F32) {
-                float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.dg) + at);
-                p[0] = make_float4(g[0], g[1], g[2], g[3]), p[1] = make_float4(g[4], g[5], g[6], g[7]);
-                p = reinterpret_cast<float4 *>(static_cast<float *>(a.du) + at);
-                p[0] = make_float4(u[0], u[1], u[2], u[3]), p[1] = make_float4(u[4], u[5], u[6], u[7]);
-            } else {
-                uint32_t x[4], y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] = __float_as_uint(g[2 * j]) >> 16 | (__float_as_uint(g[2 * j + 1]) & 0xFFFF0000u);
-                    y[j] = __float_as_uint(u[2 * j]) >> 16 | (__float_as_uint(u[2 * j + 1]) & 0xFFFF0000u);
-                }
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dg) + at) = make_uint4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.du) + at) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (c + j >= a.N) break;
-                store_act(a.dg, DT, at + j, g[j]);
-                store_act(a.du, DT, at + j, u[j]);
-            }
-        }
+        store8(a.dg, DT, t * a.N, c, a.N, a.vec, g);
+        store8(a.du, DT, t * a.N, c, a.N, a.vec, u);
         if (a.op_g && c < a.ld) {
             store_planes(a.op_g, a.ld, a.T * a.ld, t, c, a.planes, g);
             store_planes(a.op_u, a.ld, a.T * a.ld, t, c, a.planes, u);
@@ -530,7 +526,7 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     g.ep.N = static_cast<int32_t>(c.M), g.ep.T = c.T;
     g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
 
-    const int smem = 1024 + kStages * kStageBytes + sizeof(Smem);
+    const int smem = 1024 + kStages * kStageBytes + kEpiWarps * kTurnFloats * 4 + sizeof(Smem);
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(mx_back_kernel), smem);
     if (e != cudaSuccess) return e;
     PdlAttr attr;

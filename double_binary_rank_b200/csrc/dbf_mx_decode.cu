@@ -187,18 +187,24 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
     cluster_sync();
     if (warp >= 2) {
         const uint32_t base = smem_u32(part);
-        for (int u = rank + S * (warp - 2); u < 4 * g.T; u += S * kWorkers) {
-            const int t = u >> 2, r = (u & 3) * 32 + lane;
-            float sum[kMats][1];
+        // a unit is 8 tokens x 32 rows, a lane eight rows of one token
+        for (int u = rank + S * (warp - 2); u < (g.T + 7) / 8 * 4; u += S * kWorkers) {
+            const int t = (u >> 2) * 8 + (lane >> 2), r = (u & 3) * 32 + (lane & 3) * 8;
+            Raw8 x[kMats];
+            epilogue_reads<kGated>(g.ep, t, row0 + r, t < g.T, x);
+            float sum[kMats][8];
 #pragma unroll
             for (int m = 0; m < kMats; ++m) {
-                sum[m][0] = 0.0f;
-                for (int s = 0; s < S; ++s) sum[m][0] += ld_cluster_f32(base + ((m * g.w + t) * 128 + r) * 4, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[m][i] = 0.0f;
+                const uint32_t at = base + ((m * g.w + t) * 128 + r) * 4;
+                for (int s = 0; s < S; ++s) {
+                    const float4 a = ld_cluster_f32x4(at, s), b = ld_cluster_f32x4(at + 16, s);
+                    sum[m][0] += a.x, sum[m][1] += a.y, sum[m][2] += a.z, sum[m][3] += a.w;
+                    sum[m][4] += b.x, sum[m][5] += b.y, sum[m][6] += b.z, sum[m][7] += b.w;
+                }
             }
-            if (kGated)
-                finish_gated(g.ep, t, 1, row0 + r, sum[0], sum[kMats - 1]);
-            else
-                finish_plain(g.ep, t, 1, row0 + r, sum[0]);
+            epilogue_finish<kGated>(g.ep, t, row0 + r, t < g.T, x, sum);
         }
     }
     __syncwarp();

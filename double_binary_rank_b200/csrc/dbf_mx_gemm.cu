@@ -62,7 +62,8 @@ struct Args {
     int32_t *status;
 };
 
-__device__ __forceinline__ int tokens_left(int64_t T, int64_t t) { return static_cast<int>(T - t < 16 ? T - t : 16); }
+__device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][8]) { tmem_ld8(at, col); }
+__device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][8]) { tmem_ld8(at, at + w, col); }
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
@@ -70,9 +71,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     const __grid_constant__ CUtensorMap mS1, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mSB,
     const __grid_constant__ Args g)
 {
+    constexpr int kMats = kGated ? 2 : 1;
     extern __shared__ uint8_t raw[];
     uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Smem *sh = reinterpret_cast<Smem *>(stage0 + kStages * kStageBytes);
+    float *turn = reinterpret_cast<float *>(stage0 + kStages * kStageBytes);
+    Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kMats * kTurnFloats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
@@ -189,32 +192,33 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     } else {
         griddep_wait();   // y (and the addends) belong to earlier work until then
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kGated ? 0 : half * g.w);
+        float *own = turn + (warp - 2) * kMats * kTurnFloats;
+        // gated: the two warps of a lane quarter take turns by 8 tokens of both
+        // accumulators; plain: each takes one accumulator
+        const int j_first = kGated ? half * 8 : 0, j_step = kGated ? 16 : 8;
         uint32_t acc_ph = 0;
         for (int tile = unit; tile < g.tiles; tile += units) {
             const int p = tile % g.n_p, c = tile / g.n_p;
+            const int n = p * g.row_step + (kGated ? 0 : half * g.row_off) + static_cast<int>(rank) * 128 + quarter * 32 +
+                          (lane & 3) * 8;
+            const int64_t t = static_cast<int64_t>(c) * g.w + (lane >> 2);
+            // what a chunk reads is asked for a chunk ahead, the first before the products are there
+            Raw8 x[2][kMats];
+            epilogue_reads<kGated>(g.ep, t + j_first, n, t + j_first < g.ep.T, x[0]);
             if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
             acc_ph ^= 1u;
             tc_fence_after();
-            const int64_t t0 = static_cast<int64_t>(c) * g.w;
-            if (kGated) {
-                const int n = p * g.row_step + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-                // the two warps of a lane quarter take turns by 16 tokens
-                for (int j0 = half * 16; j0 < g.w; j0 += 32) {
-                    float vg[16], vu[16];
-                    tmem_ld16(lanes + j0, vg);
-                    tmem_ld16(lanes + g.w + j0, vu);
-                    const int count = tokens_left(g.ep.T, t0 + j0);
-                    if (count > 0) finish_gated(g.ep, t0 + j0, count, n, vg, vu);
-                }
-            } else {
-                // each of the two warps takes one accumulator
-                const int n = p * g.row_step + half * g.row_off + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-                for (int j0 = 0; j0 < g.w; j0 += 16) {
-                    float v[16];
-                    tmem_ld16(lanes + half * g.w + j0, v);
-                    const int count = tokens_left(g.ep.T, t0 + j0);
-                    if (count > 0) finish_plain(g.ep, t0 + j0, count, n, v);
+            for (int j0 = j_first; j0 < g.w; j0 += 2 * j_step) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + i * j_step, next = j + j_step;
+                    if (j >= g.w) break;
+                    epilogue_reads<kGated>(g.ep, t + next, n, next < g.w && t + next < g.ep.T, x[i ^ 1]);
+                    float col[kMats][8], row[kMats][8];
+                    load_chunk(lanes + j, g.w, col);
+                    turn8<kMats>(own, col, row);
+                    epilogue_finish<kGated>(g.ep, t + j, n, t + j < g.ep.T, x[i], row);
                 }
             }
             tc_fence_before();
@@ -399,7 +403,7 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
     if (e != cudaSuccess) return e;
 
     const auto kernel = gated ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
-    const int smem = 1024 + kStages * kStageBytes + sizeof(Smem);
+    const int smem = 1024 + kStages * kStageBytes + kEpiWarps * c.mats * kTurnFloats * 4 + sizeof(Smem);
     e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     Args g = {};

@@ -53,96 +53,93 @@ __device__ __forceinline__ float gate_slope(int act, float g, float &value)
     return d == 0.0f ? s : s + g * d * kGelu2c * (1.0f + 3.0f * kGeluCube * g * g);   // d == 0: g * g may be infinite
 }
 
-// The epilogues below take, in each lane, one column n (32 consecutive columns
-// a warp, the first a multiple of 32) of kTok consecutive tokens from t0, of
-// which 'count' exist. Every lane of the warp calls them. All reads are issued
-// before the first result is formed, and no lane's control flow differs up to
-// its stores.
-template <int kTok>
-__device__ __forceinline__ void add_columns(const void *p, dbf_dtype dt, int64_t N, int64_t t0, int count, int n, float (&v)[kTok])
+// ---- epilogue. A lane finishes eight consecutive columns c .. c + 7 of one
+// token (four neighbouring lanes hold a block of 32, for the 8-bit format);
+// what it reads (y when accumulating, the addends) it asks for early with
+// epilogue_reads(). Every lane of the warp calls these; 'on' says whether the
+// lane's token exists.
+__device__ __forceinline__ bool epilogue_vec(const Epilogue &e) { return (e.N & 7) == 0; }
+
+template <bool kGated>
+__device__ __forceinline__ void epilogue_reads(const Epilogue &e, int64_t t, int c, bool on, Raw8 (&x)[kGated ? 2 : 1])
 {
-    float a[kTok];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) a[j] = n < N && j < count ? load_act(p, dt, (t0 + j) * N + n) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) v[j] += a[j];
+    const int64_t N = e.N;
+    if (kGated) {
+        x[0] = load_raw8(e.g_add, e.add_dt, t * N, on && e.g_add ? c : N, N, epilogue_vec(e));
+        x[kGated] = load_raw8(e.u_add, e.add_dt, t * N, on && e.u_add ? c : N, N, epilogue_vec(e));
+    } else {
+        x[0] = load_raw8(e.y, e.yd, t * N, on && e.accumulate ? c : N, N, epilogue_vec(e));
+    }
 }
 
-// bf16 rows of even length: neighbouring lanes swap one of two tokens, so that
-// a lane stores two columns of one token as one word (half the store
-// instructions).
-template <int kTok>
-__device__ __forceinline__ void store_columns(void *p, dbf_dtype dt, int64_t N, int64_t t0, int count, int n, const float (&v)[kTok])
+// One block of the 8-bit format from the four lanes that hold it; lanes past
+// the last column hold zeros.
+__device__ __forceinline__ void keep8(uint8_t *codes, uint8_t *scales, int64_t pitch, int64_t T, int64_t t, int c, bool on,
+                                      const float (&v)[8])
 {
-    const bool in = n < N;
-    if (dt == DBF_F32) {
-        float *y = static_cast<float *>(p) + t0 * N + n;
+    const uint32_t byte = scale_byte8(block_amax(amax_bits8(v)));
+    const float inv = inv_scale(byte);
+    uint2 w;
+    w.x = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    w.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    if (byte == 255u) w = make_uint2(0u, 0u);
+    if (!on || c >= pitch) return;
+    *reinterpret_cast<uint2 *>(codes + t * pitch + c) = w;
+    if ((c & 31) == 0) scales[static_cast<int64_t>(c / kBlock) * T + t] = static_cast<uint8_t>(byte);
+}
+
+template <bool kGated>
+__device__ __forceinline__ void epilogue_finish(const Epilogue &e, int64_t t, int c, bool on, const Raw8 (&x)[kGated ? 2 : 1],
+                                                float (&v)[kGated ? 2 : 1][8])
+{
+    const int64_t N = e.N;
+    const bool vec = epilogue_vec(e);
+    if (!kGated) {
+        if (e.accumulate) add_raw8(x[0], e.yd, vec, v[0]);
+    } else {
+        float(&g)[8] = v[0];
+        float(&u)[8] = v[kGated];
+        if (e.g_add) add_raw8(x[0], e.add_dt, vec, g);
+        if (e.u_add) add_raw8(x[kGated], e.add_dt, vec, u);
+        if (e.g8) {
+            if (c + 8 > N) {   // columns past the last may hold anything, a NaN too
 #pragma unroll
-        for (int j = 0; j < kTok; ++j)
-            if (in && j < count) y[j * N] = v[j];
-        return;
-    }
-    if (kTok % 2 == 0 && (N & 1) == 0) {
-        const int odd = threadIdx.x & 1;
-        // token j + odd, columns n - odd and n - odd + 1
-        uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + (t0 + odd) * N + (n - odd));
-#pragma unroll
-        for (int j = 0; j < kTok; j += 2) {
-            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-            const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
-            if (in && j + odd < count) y[j * (N / 2)] = *reinterpret_cast<const uint32_t *>(&w);
+                for (int i = 0; i < 8; ++i)
+                    if (c + i >= N) g[i] = u[i] = 0.0f;
+            }
+            keep8(e.g8, e.gs, e.pitch8, e.T, t, c, on, g);
+            keep8(e.u8, e.us, e.pitch8, e.T, t, c, on, u);
         }
-        return;
-    }
-    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p) + t0 * N + n;
 #pragma unroll
-    for (int j = 0; j < kTok; ++j)
-        if (in && j < count) y[j * N] = __float2bfloat16_rn(v[j]);
+        for (int i = 0; i < 8; ++i) g[i] = gate_value(e.act, g[i]) * u[i];
+    }
+    if (on) store8(e.y, e.yd, t * N, c, N, vec, v[0]);
 }
 
-// Keep the warp's 32 columns, a block of the 8-bit format, of each token; the
-// warp finds the largest magnitude together (as an integer: NaN above
-// infinity above all else). Columns at or past N hold 0.
-template <int kTok>
-__device__ __forceinline__ void keep8(uint8_t *codes, uint8_t *scales, int64_t pitch, int64_t T, int64_t t0, int count, int n,
-                                      const float (&v)[kTok])
+// Tensor memory holds a column of W's rows per lane and a token per register;
+// the epilogue wants eight columns of one token per lane. A warp turns 8
+// tokens x 32 columns in its own shared memory: rows of 36 floats, so that the
+// 16-byte reads of eight lanes (two tokens, four groups of columns) hit
+// different banks.
+constexpr int kTurnFloats = 8 * 36;   // per accumulator
+
+template <int kMats>
+__device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], float (&row)[kMats][8])
 {
-    static_assert(kTok <= 32, "lane j stores token j's scale");
     const int lane = threadIdx.x & 31;
-    if (n - lane >= pitch) return;   // the warp's block does not exist
-    uint32_t mine = 0;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const uint32_t byte = scale_byte8(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[j]) & 0x7FFFFFFFu));
-        const uint32_t w = byte == 255u ? 0u : e4m3x4(v[j] * inv_scale(byte), 0.0f, 0.0f, 0.0f);
-        if (j < count) codes[(t0 + j) * pitch + n] = static_cast<uint8_t>(w);
-        if (lane == j) mine = byte;
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) own[m * kTurnFloats + j * 36 + lane] = col[m][j];
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) {
+        const float4 *p = reinterpret_cast<const float4 *>(own + m * kTurnFloats + (lane >> 2) * 36 + (lane & 3) * 8);
+        const float4 a = p[0], b = p[1];
+        row[m][0] = a.x, row[m][1] = a.y, row[m][2] = a.z, row[m][3] = a.w;
+        row[m][4] = b.x, row[m][5] = b.y, row[m][6] = b.z, row[m][7] = b.w;
     }
-    if (lane < count && lane < kTok) scales[static_cast<int64_t>(n / kBlock) * T + t0 + lane] = static_cast<uint8_t>(mine);
-}
-
-template <int kTok>
-__device__ __forceinline__ void finish_plain(const Epilogue &e, int64_t t0, int count, int n, float (&v)[kTok])
-{
-    if (e.accumulate) add_columns(e.y, e.yd, e.N, t0, count, n, v);
-    store_columns(e.y, e.yd, e.N, t0, count, n, v);
-}
-template <int kTok>
-__device__ __forceinline__ void finish_gated(const Epilogue &e, int64_t t0, int count, int n, float (&g)[kTok], float (&u)[kTok])
-{
-    if (e.g_add) add_columns(e.g_add, e.add_dt, e.N, t0, count, n, g);
-    if (e.u_add) add_columns(e.u_add, e.add_dt, e.N, t0, count, n, u);
-    if (e.g8) {
-        if (n >= e.N) {
-#pragma unroll
-            for (int j = 0; j < kTok; ++j) g[j] = u[j] = 0.0f;
-        }
-        keep8(e.g8, e.gs, e.pitch8, e.T, t0, count, n, g);
-        keep8(e.u8, e.us, e.pitch8, e.T, t0, count, n, u);
-    }
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) g[j] = gate_value(e.act, g[j]) * u[j];
-    store_columns(e.y, e.yd, e.N, t0, count, n, g);
 }
 
 // One call: a weight (plain) or two of one shape (gated), and its tokens.

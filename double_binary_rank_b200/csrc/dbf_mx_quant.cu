@@ -57,42 +57,6 @@ __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__re
 }
 
 template <dbf_dtype DT>
-__device__ __forceinline__ void store8(void *dst, int64_t at, int64_t c, int64_t k, bool vec, const float (&v)[8])
-{
-    if (vec) {
-        if (DT == DBF_F32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(dst) + at);
-            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-            p[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            uint32_t q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (DT == DBF_BF16) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    q[i] = *reinterpret_cast<const uint32_t *>(&b);
-                } else {
-                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-                    q[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-            }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at) = make_uint4(q[0], q[1], q[2], q[3]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (c + i >= k) break;
-        if (DT == DBF_F32)
-            static_cast<float *>(dst)[at + i] = v[i];
-        else if (DT == DBF_BF16)
-            static_cast<__nv_bfloat16 *>(dst)[at + i] = __float2bfloat16_rn(v[i]);
-        else
-            static_cast<__half *>(dst)[at + i] = __float2half_rn(v[i]);
-    }
-}
-
-template <dbf_dtype DT>
 __global__ void __launch_bounds__(32 * kWarps) dequantize4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                    int64_t rows, int64_t k, bool vec, void *__restrict__ dst)
 {
@@ -120,7 +84,7 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize4_kernel(const uint8_t 
         from_e2m1x8(w[g], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= s;
-        store8<DT>(dst, r * k + c, c, k, vec, v);
+        store8(dst, DT, r * k, c, k, vec, v);
     }
 }
 
@@ -188,7 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps) act8_load_kernel(const uint8_t *_
         from_e4m3x4(w[g].x, lo);
         from_e4m3x4(w[g].y, hi);
         const float v[8] = {lo[0] * s, lo[1] * s, lo[2] * s, lo[3] * s, hi[0] * s, hi[1] * s, hi[2] * s, hi[3] * s};
-        store8<DT>(dst, r * k + c, c, k, vec, v);
+        store8(dst, DT, r * k, c, k, vec, v);
     }
 }
 
