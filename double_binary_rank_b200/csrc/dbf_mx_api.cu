@@ -47,15 +47,16 @@ dbf_status check_layer(const dbf_mx4_layer *L)
 size_t product_workspace(const dbf_mx4_layer *L, int64_t T, int mats)
 {
     if (!layer_shape_ok(L) || !tokens_ok(L, T)) return 0;
-    if (T == 0 || mx_decode_fits(L->M, L->N, T, mats)) return kWsHeaderBytes;
-    return mx_gemm_workspace_bytes(L->M, L->N, T, mats);
+    if (T == 0) return kWsHeaderBytes;
+    const size_t few = mx_decode_workspace_bytes(L->M, L->N, T, mats);
+    return few ? few : mx_gemm_workspace_bytes(L->M, L->N, T, mats);
 }
 
 dbf_status run(const mx::Product &c, size_t need, size_t ws_bytes, cudaStream_t s)
 {
     if (!c.ws || ws_bytes < need) return DBF_ERR_WORKSPACE;
     if (!aligned(c.ws, 256)) return DBF_ERR_ALIGNMENT;
-    return from_cuda(mx_decode_fits(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
+    return from_cuda(mx_decode_workspace_bytes(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
 }
 
 bool same_shape(const dbf_mx4_layer *a, const dbf_mx4_layer *b)
@@ -193,7 +194,7 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
 size_t dbf_mx4_backward_workspace_bytes(const dbf_mx4_layer *L, int64_t T, dbf_dtype dy_dtype)
 {
     if (!layer_shape_ok(L) || !gradient_ok(L, T) || !act_dtype_ok(dy_dtype)) return 0;
-    return mx_back_workspace_bytes(L->N, T, dy_dtype, 1);
+    return mx_back_workspace_bytes(L->M, L->N, T, dy_dtype, 1);
 }
 
 dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy_dtype, void *dx, dbf_dtype dx_dtype, int64_t T,
@@ -208,7 +209,7 @@ dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy
     const dbf_status st = check_layer(L);
     if (st != DBF_OK) return st;
     if (!aligned(dy, 16) || !aligned(dx, 16)) return DBF_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < mx_back_workspace_bytes(L->N, T, dy_dtype, 1)) return DBF_ERR_WORKSPACE;
+    if (!ws || ws_bytes < mx_back_workspace_bytes(L->M, L->N, T, dy_dtype, 1)) return DBF_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return DBF_ERR_ALIGNMENT;
     mx::Gradient c = {};
     c.M = L->M, c.N = L->N, c.T = T;
@@ -221,7 +222,7 @@ dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy
 size_t dbf_mx4_gated_backward_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T, dbf_dtype dh_dtype)
 {
     if (!same_shape(gate, up) || !gradient_ok(gate, T) || !act_dtype_ok(dh_dtype)) return 0;
-    return mx_back_workspace_bytes(gate->N, T, dh_dtype, 2);
+    return mx_back_workspace_bytes(gate->M, gate->N, T, dh_dtype, 2);
 }
 
 dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const dbf_act8 *saved_g,
@@ -246,7 +247,7 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
         dbf_status st = check_layer(gate);
         if (st == DBF_OK) st = check_layer(up);
         if (st != DBF_OK) return st;
-        if (!ws || ws_bytes < mx_back_workspace_bytes(gate->N, T, dh_dtype, 2)) return DBF_ERR_WORKSPACE;
+        if (!ws || ws_bytes < mx_back_workspace_bytes(gate->M, gate->N, T, dh_dtype, 2)) return DBF_ERR_WORKSPACE;
         if (!aligned(ws, 256)) return DBF_ERR_ALIGNMENT;
         c.codes[0] = gate->codes, c.scales[0] = gate->scales;
         c.codes[1] = up->codes, c.scales[1] = up->scales;

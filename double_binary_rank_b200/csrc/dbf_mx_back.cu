@@ -12,17 +12,20 @@
 // operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
 // each (v = p0 + p1 + p2 exactly), three times the products.
 //
-// A CTA pair owns 256 columns of W x 256 tokens of dx, contraction over the
-// rows of W in stages of 64:
-//   warp 0       TMA: 128 token rows of the gradient, 64 columns each;
+// A CTA pair owns 256 columns of W x w <= 512 tokens of dx as two accumulators
+// (an expanded stage feeds two MMAs a step), contraction over the rows of W in
+// stages of 64:
+//   warp 0       TMA: w / 2 token rows of the gradient, 64 columns each;
 //   warps 2..9   expansion: a thread takes 32 codes of one row of W (16 bytes
 //                and a scale, loaded four stages ahead) and writes them as 64
 //                bytes of a 128-byte-swizzled tile whose rows are rows of W:
 //                the A operand in its M-major form, so nothing is transposed;
 //                a warp's lanes hold 32 different rows, whose swizzled chunks
 //                lie in different banks;
-//   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N = w, K = 16);
-//   warps 10..17 epilogue, overlapped with the next tile (two accumulators).
+//   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N = w / 2, K = 16);
+//   warps 10..17 epilogue.
+// Where the tiles are fewer than the pairs, the contraction is cut into parts
+// whose fp32 sums a second launch adds in order.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -36,17 +39,17 @@ namespace {
 using namespace mx;
 using namespace tc;
 
-constexpr int kStages = 6;
+constexpr int kStages = 4;
 constexpr int kExpand = 8, kEpiWarps = 8;   // warps
 constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
 constexpr int kAhead = 4;                           // stages that the expansion's loads run ahead
 constexpr int kRowsK = 64;                          // rows of W per stage
-constexpr uint32_t kABytes = 128 * kRowsK * 2, kBBytes = 128 * kRowsK * 2;
+constexpr uint32_t kABytes = 128 * kRowsK * 2, kBBytes = 2 * 128 * kRowsK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr uint32_t kTmemCols = 512;
 
 struct Smem {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain, exit_bar;
+    uint64_t full[kStages], empty[kStages], acc_full, acc_empty, drain, exit_bar;
     uint32_t tmem_base;
     int abort;
 };
@@ -61,7 +64,10 @@ struct Args {
     int mats, planes;    // products summed: weights, pieces of the gradient
     int64_t plane_rows;  // rows from one piece to the next in the gradient's map
     int w;               // tokens per tile
-    int n_p, tiles;
+    int n_p, n_c;        // tiles along the columns of W and along the tokens
+    int splits;          // parts of the contraction; over 1, each writes fp32 sums [T][M] of its own
+    int tiles;           // n_p * n_c * splits
+    float *partial;
     int early;           // W may be read before earlier work is done
     Epilogue ep;
     int32_t *status;
@@ -99,8 +105,23 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Tiles (256 columns of W x w tokens) in column order, so that pairs that run
-// together share the gradient's rows.
+// Tiles (256 columns of W x w tokens, a part of the contraction) in column
+// order, so that pairs that run together share the gradient's rows.
+struct Tile {
+    int p, c, s, k0, k1;   // column and token tile, part, its stages [k0, k1)
+};
+__device__ __forceinline__ Tile tile_of(const Args &g, int tile, int nk)
+{
+    Tile t;
+    t.p = tile % g.n_p;
+    const int rest = tile / g.n_p;
+    t.c = rest % g.n_c;
+    t.s = rest / g.n_c;
+    t.k0 = static_cast<int>(static_cast<int64_t>(nk) * t.s / g.splits);
+    t.k1 = static_cast<int>(static_cast<int64_t>(nk) * (t.s + 1) / g.splits);
+    return t;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_constant__ CUtensorMap mB0,
                                                               const __grid_constant__ CUtensorMap mB1,
                                                               const __grid_constant__ Args g)
@@ -120,10 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
             bar_init(&sh->full[i], 1 + 2 * kExpand);
             bar_init(&sh->empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(&sh->acc_full[i], 1);
-            bar_init(&sh->acc_empty[i], 2 * kEpiWarps);
-        }
+        bar_init(&sh->acc_full, 1);
+        bar_init(&sh->acc_empty, 2 * kEpiWarps);
         bar_init(&sh->drain, 1);
         bar_init(&sh->exit_bar, 1);
         sh->abort = 0;
@@ -139,25 +158,28 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
     if (warp == 0) {
         if (lane == 0) {
             griddep_wait();   // the gradient belongs to earlier work until then
-            const int half_w = g.w / 2;
+            const int quarter_w = g.w / 4;
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int tile = unit; tile < g.tiles && ok; tile += units) {
-                const int tok = tile / g.n_p * g.w + static_cast<int>(rank) * half_w;
-                for (int seg = 0; seg < nseg && ok; ++seg) {
+                const Tile c = tile_of(g, tile, nk);
+                const int tok = c.c * g.w + static_cast<int>(rank) * quarter_w;
+                int seg = c.k0 / g.nn, i = c.k0 - seg * g.nn;
+                for (int k = c.k0; k < c.k1; ++k) {
+                    if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
                     const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
                     const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
-                    for (int i = 0; i < g.nn; ++i) {
-                        if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        if (rank == 0) bar_expect_tx(&sh->full[s], 2 * half_w * kRowsK * 2);
-                        tma_2d_pair(stage0 + s * kStageBytes + kABytes, map, i * kRowsK, row, &sh->full[s]);
-                        ++issued;
-                        if (++s == kStages) s = 0, ph ^= 1u;
-                    }
+                    uint8_t *st = stage0 + s * kStageBytes + kABytes;
+                    if (rank == 0) bar_expect_tx(&sh->full[s], 4 * quarter_w * kRowsK * 2);
+                    tma_2d_pair(st, map, i * kRowsK, row, &sh->full[s]);
+                    tma_2d_pair(st + quarter_w * kRowsK * 2, map, i * kRowsK, row + 2 * quarter_w, &sh->full[s]);
+                    ++issued;
+                    if (++s == kStages) s = 0, ph ^= 1u;
+                    if (++i == g.nn) i = 0, ++seg;
                 }
             }
             if (*abort && rank == 0)
@@ -166,16 +188,16 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            int s = 0, n_tile = 0;
-            uint32_t ph = 0;
+            int s = 0;
+            uint32_t ph = 0, acc_ph = 0;
             bool ok = true;
-            const uint32_t id = bf16_idesc(g.w);
-            for (int tile = unit; tile < g.tiles && ok; tile += units, ++n_tile) {
-                const int acc = n_tile & 1;
-                ok = bar_wait(&sh->acc_empty[acc], ((n_tile >> 1) & 1u) ^ 1u, abort);
+            const uint32_t id = bf16_idesc(g.w / 2), second = g.w / 4 * kRowsK * 2;
+            for (int tile = unit; tile < g.tiles && ok; tile += units) {
+                const Tile c = tile_of(g, tile, nk);
+                ok = bar_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
                 if (!ok) break;
                 tc_fence_after();
-                for (int ks = 0; ks < nk; ++ks) {
+                for (int k = c.k0; k < c.k1; ++k) {
                     if (!bar_wait(&sh->full[s], ph, abort)) {
                         ok = false;
                         break;
@@ -184,15 +206,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                     const uint32_t st = smem_u32(stage0) + s * kStageBytes;
                     // A: 64 columns of W to a 128-byte row; groups of 8 rows 1 KB apart, the second
                     // 64 columns 8 KB on
-                    const uint64_t a = sw128_desc(st, 1024, 8192), b = sw128_desc(st + kABytes);
+                    const uint64_t a = sw128_desc(st, 1024, 8192), b0 = sw128_desc(st + kABytes), b1 = sw128_desc(st + kABytes + second);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_pair(tmem + acc * 256, a + kk * (2048 >> 4), b + 2 * kk, id, ks > 0 || kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = k > c.k0 || kk > 0 ? 1u : 0u;
+                        mma_bf16_pair(tmem, a + kk * (2048 >> 4), b0 + 2 * kk, id, acc);
+                        mma_bf16_pair(tmem + 256, a + kk * (2048 >> 4), b1 + 2 * kk, id, acc);
+                    }
                     commit_pair_both(&sh->empty[s]);
                     if (++s == kStages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
-                commit_pair_both(&sh->acc_full[acc]);
+                commit_pair_both(&sh->acc_full);
+                acc_ph ^= 1u;
             }
             if (*abort) {
                 commit_pair_own(&sh->drain);
@@ -204,20 +230,24 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
         const int e = warp - 2, q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
         uint8_t *dst = stage0 + (q >> 1) * 8192 + r * 128;
         const int chunk0 = (q & 1) * 4;
-        // A cursor over (tile, product, stage) runs kAhead stages ahead of the
-        // expansion; its loads land in slots with fixed names, so that nothing
-        // waits for a load before the stage that uses it.
+        // A cursor over (tile, stage) runs kAhead stages ahead of the expansion;
+        // its loads land in slots with fixed names, so that nothing waits for a
+        // load before the stage that uses it.
         const uint8_t *code_at = nullptr, *scale_base = nullptr;
-        int tile = unit, seg = -1, i = g.nn, block = 0, left = 0;   // left: rows of W from this thread's on
+        int tile = unit, k = 0, k1 = 0, i = 0, block = 0, left = 0;   // left: rows of W from this thread's on
         auto load = [&](uint4 &codes, uint32_t &scale) {
-            if (i == g.nn) {
-                i = 0;
-                if (++seg == nseg) seg = 0, tile += units;
-                block = (tile % g.n_p) * 8 + static_cast<int>(rank) * 4 + q;
-                const int m = seg < g.planes ? 0 : 1;
+            if (k == k1 || i == g.nn) {
+                if (k == k1) {   // the next tile (the first: k and k1 are 0 and tile is this pair's)
+                    if (k1 > 0) tile += units;
+                    const Tile c = tile_of(g, tile < g.tiles ? tile : unit, nk);
+                    k = c.k0, k1 = c.k1, block = c.p * 8 + static_cast<int>(rank) * 4 + q;
+                }
+                const int seg = k / g.nn, m = seg < g.planes ? 0 : 1;
+                i = k - seg * g.nn;
+                const int r0 = i * kRowsK + r;
                 // columns past the last stay zero (rows of dx that are not stored)
-                left = tile < g.tiles && block < g.nb ? g.N - r : 0;
-                code_at = g.codes[m] + r * g.pitch + block * 16;
+                left = tile < g.tiles && block < g.nb ? g.N - r0 : 0;
+                code_at = g.codes[m] + r0 * g.pitch + block * 16;
                 scale_base = g.scales[m];
             }
             codes = make_uint4(0u, 0u, 0u, 0u);
@@ -226,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 codes = *reinterpret_cast<const uint4 *>(code_at);
                 scale = scale_base[scale_at(i * kRowsK + r, block, g.sf_tiles)];
             }
-            ++i;
+            ++i, ++k;
             left -= kRowsK;
             code_at += kRowsK * g.pitch;
         };
@@ -237,11 +267,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        const int64_t total = static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * nk;   // unit < tiles
-        for (int64_t k = 0; k < total && ok; k += kAhead) {
+        int64_t total = 0;   // stages of this pair
+        for (int t = unit; t < g.tiles; t += units) {
+            const Tile c = tile_of(g, t, nk);
+            total += c.k1 - c.k0;
+        }
+        for (int64_t done = 0; done < total && ok; done += kAhead) {
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (k + a >= total) break;
+                if (done + a >= total) break;
                 // exponent field of 2^(126 + s); what passes 254 is a second factor
                 const uint32_t field = scale[a] + 126u;
                 const uint32_t f1 = scale[a] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
@@ -275,31 +309,39 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
         griddep_launch();   // all earlier work is done
         const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2;
         float *own = turn + (warp - 2 - kExpand) * kTurnFloats;
-        int n_tile = 0;
-        for (int tile = unit; tile < g.tiles; tile += units, ++n_tile) {
-            const int acc = n_tile & 1;
-            const int64_t t = static_cast<int64_t>(tile / g.n_p) * g.w + (lane >> 2);
-            const int n = (tile % g.n_p) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + (lane & 3) * 8;
+        // one warp of a lane quarter takes the first w / 2 tokens, the other the rest
+        const int first = half * (g.w / 2);
+        const uint32_t from = tmem + half * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint32_t acc_ph = 0;
+        for (int tile = unit; tile < g.tiles; tile += units) {
+            const Tile c = tile_of(g, tile, nk);
+            const int64_t t = static_cast<int64_t>(c.c) * g.w + first + (lane >> 2);
+            const int n = c.p * 256 + static_cast<int>(rank) * 128 + quarter * 32 + (lane & 3) * 8;
+            Epilogue ep = g.ep;
+            if (g.splits > 1) {
+                ep.y = g.partial + c.s * g.ep.T * g.ep.N;
+                ep.yd = DBF_F32;
+                ep.accumulate = 0;
+            }
             Raw8 x[2][1];   // what a chunk of 8 tokens reads is asked for a chunk ahead
-            epilogue_reads<false>(g.ep, t + half * 8, n, t + half * 8 < g.ep.T, x[0]);
-            if (!bar_wait(&sh->acc_full[acc], (n_tile >> 1) & 1u, abort)) break;
+            epilogue_reads<false>(ep, t, n, t < ep.T, x[0]);
+            if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
+            acc_ph ^= 1u;
             tc_fence_after();
-            const uint32_t from = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int j0 = half * 8; j0 < g.w; j0 += 32) {
+            for (int j0 = 0; j0 < g.w / 2; j0 += 16) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int j = j0 + i * 16, next = j + 16;
-                    if (j >= g.w) break;
-                    epilogue_reads<false>(g.ep, t + next, n, next < g.w && t + next < g.ep.T, x[i ^ 1]);
+                    const int j = j0 + i * 8, next = j + 8;
+                    epilogue_reads<false>(ep, t + next, n, next < g.w / 2 && t + next < ep.T, x[i ^ 1]);
                     float col[1][8], row[1][8];
                     tmem_ld8(from + j, col);
                     turn8<1>(own, col, row);
-                    epilogue_finish<false>(g.ep, t + j, n, t + j < g.ep.T, x[i], row);
+                    epilogue_finish<false>(ep, t + j, n, t + j < ep.T, x[i], row);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_leader(&sh->acc_empty[acc]);
+            if (lane == 0) bar_arrive_leader(&sh->acc_empty);
         }
     }
 
@@ -365,7 +407,6 @@ __global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy
                                                      uint16_t *__restrict__ op, int64_t ld, int planes)
 {
     griddep_wait();
-    griddep_launch();
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31)) * 8;
     if (c >= ld) return;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += static_cast<int64_t>(gridDim.x) * 8) {
@@ -373,6 +414,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy
         load8(dy, dt, t * N, c, N, vec, v);
         store_planes(op, ld, T * ld, t, c, planes, v);
     }
+    griddep_launch();   // at the end: the product's CTAs would take this kernel's registers
 }
 
 // dg and du of 32 tokens x 256 columns from dh and the 8-bit g and u, and their
@@ -392,7 +434,6 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ 
 {
     __shared__ uint8_t sc[2][8][32];
     griddep_wait();
-    griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
@@ -439,6 +480,27 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ 
             store_planes(a.op_u, a.ld, a.T * a.ld, t, c, a.planes, u);
         }
     }
+    griddep_launch();   // at the end: the product's CTAs would take this kernel's registers
+}
+
+// dx = [acc] dx + the parts' sums, in order.
+__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ partial, int splits, const __grid_constant__ Epilogue e)
+{
+    griddep_wait();
+    griddep_launch();
+    const int64_t N = e.N, plane = e.T * N;
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31)) * 8;
+    const bool vec = epilogue_vec(e);
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < e.T; t += static_cast<int64_t>(gridDim.x) * 8) {
+        Raw8 x[1];
+        epilogue_reads<false>(e, t, static_cast<int>(c), c < N, x);
+        float v[1][8] = {};
+        for (int s = 0; s < splits; ++s) {
+            const Raw8 r = load_raw8(partial + s * plane, DBF_F32, t * N, c, N, vec);
+            add_raw8(r, DBF_F32, vec, v[0]);
+        }
+        epilogue_finish<false>(e, t, static_cast<int>(c), c < N, x, v);
+    }
 }
 
 int resident_pairs(cudaLaunchConfig_t cfg)
@@ -460,21 +522,34 @@ int resident_pairs(cudaLaunchConfig_t cfg)
     return it->second;
 }
 
-// Tokens per tile: the width whose waves of tiles end first; below 128 tokens
-// the expansion of W, the same for every width, bounds a stage.
-int tile_width(int64_t M, int64_t T)
+// Tokens per tile (a multiple of 32 up to 512) and parts of the contraction.
+// Cost of the last pair to finish, in cycles: waves of tiles, each so many
+// stages, a stage taking its eight MMAs (2 w) or the expansion of W (the same
+// at every width), and an epilogue; the parts' sums are written and read once
+// more.
+struct Plan {
+    int w, splits;
+};
+Plan plan(int64_t M, int64_t T, int64_t nk)
 {
     const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
-    int best = 32;
-    double least = 0;
-    for (int w = 32; w <= 256; w += 32) {
-        const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
-        const double cost = static_cast<double>(waves) * std::max(128.0, static_cast<double>(w));
-        if (w == 32 || cost <= least) least = cost, best = w;
+    Plan best = {32, 1};
+    double least = -1;
+    for (int w = 32; w <= 512; w += 32) {
+        const int64_t tiles = n_p * ((T + w - 1) / w);
+        for (int splits = 1; splits <= 16 && splits <= nk; ++splits) {
+            if (splits > 1 && tiles * splits > pairs) break;
+            const double waves = static_cast<double>((tiles * splits + pairs - 1) / pairs);
+            const double stages = static_cast<double>((nk + splits - 1) / splits);
+            const double join = splits > 1 ? 4000.0 + 8.0 * T * M * (splits + 1) / 3500.0 : 0.0;   // a launch, and bytes at 3.5 KB a cycle
+            const double cost = waves * (stages * std::max(2.0 * w, 600.0) + 1500 + 12.0 * w) + join;
+            if (least < 0 || cost < least) least = cost, best = {w, splits};
+        }
         if (w >= T) break;
     }
     return best;
 }
+int64_t stages(int64_t N, int mats, int planes) { return (N + kRowsK - 1) / kRowsK * mats * planes; }
 
 int64_t operand_ld(int64_t N) { return (N + 7) / 8 * 8; }
 bool direct_operand(int64_t N, dbf_dtype d) { return d == DBF_BF16 && N % 8 == 0; }
@@ -495,16 +570,23 @@ struct PdlAttr {
     }
 };
 
+// a warp a row of eight-column lanes
+dim3 row_grid(int64_t T, int64_t cols)
+{
+    return dim3(static_cast<unsigned>(std::min<int64_t>((T + 7) / 8, 1 << 20)), static_cast<unsigned>((cols + 255) / 256));
+}
+
 // dx from the operands (one map per weight)
-cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, int planes, bool pre, cudaStream_t s)
+cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, int planes, bool pre, size_t partial_at, cudaStream_t s)
 {
     const int mats = c.codes[1] ? 2 : 1;
-    const int w = tile_width(c.M, c.T);
+    const Plan pl = plan(c.M, c.T, stages(c.N, mats, planes));
+    const int w = pl.w;
     CUtensorMap map[2];
     for (int m = 0; m < 2; ++m) {
         const uint64_t dims[2] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.T * planes)};
         const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
-        const uint32_t box[2] = {kRowsK, static_cast<uint32_t>(w / 2)};
+        const uint32_t box[2] = {kRowsK, static_cast<uint32_t>(w / 4)};
         if (!tc_map(&map[m], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, operand[m < mats ? m : 0], dims, strides, box, true))
             return cudaErrorInvalidValue;
     }
@@ -520,7 +602,10 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     g.plane_rows = c.T;
     g.w = w;
     g.n_p = static_cast<int>((c.M + 255) / 256);
-    g.tiles = static_cast<int>(g.n_p * ((c.T + w - 1) / w));
+    g.n_c = static_cast<int>((c.T + w - 1) / w);
+    g.splits = pl.splits;
+    g.tiles = g.n_p * g.n_c * g.splits;
+    g.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(c.ws) + partial_at);
     g.early = pre || (c.flags & DBF_WEIGHTS_STATIC) ? 1 : 0;
     g.ep.y = c.dx, g.ep.yd = c.dxd, g.ep.accumulate = c.flags & DBF_ACCUMULATE ? 1 : 0;
     g.ep.N = static_cast<int32_t>(c.M), g.ep.T = c.T;
@@ -539,26 +624,36 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     cfg.gridDim = dim3(2 * std::min(resident_pairs(cfg), g.tiles));
     cfg.attrs = attr.attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx_back_kernel, map[0], map[1], g);
+    e = cudaLaunchKernelEx(&cfg, mx_back_kernel, map[0], map[1], g);
+    if (e != cudaSuccess || pl.splits == 1) return e;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = row_grid(c.T, c.M);
+    join.blockDim = dim3(256);
+    join.stream = s;
+    join.attrs = attr.attr;
+    join.numAttrs = 1;
+    return cudaLaunchKernelEx(&join, join_kernel, static_cast<const float *>(g.partial), pl.splits, g.ep);
 }
 
 }  // namespace
 
-size_t mx_back_workspace_bytes(int64_t N, int64_t T, dbf_dtype d, int mats)
+size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int mats)
 {
-    return kWsHeaderBytes + (direct_operand(N, d) ? 0 : mats * plane_bytes(N, T, d));
+    const Plan pl = plan(M, T, stages(N, mats, d == DBF_F32 ? 3 : 1));
+    const size_t partial = pl.splits > 1 ? align_up(static_cast<size_t>(pl.splits) * static_cast<size_t>(T * M) * 4, 256) : 0;
+    return kWsHeaderBytes + (direct_operand(N, d) ? 0 : mats * plane_bytes(N, T, d)) + partial;
 }
 
 cudaError_t mx_backward(const Gradient &c, cudaStream_t s)
 {
     const void *operand[2] = {c.dy, nullptr};
     const int planes = c.dyd == DBF_F32 ? 3 : 1;
-    if (direct_operand(c.N, c.dyd)) return product(c, operand, c.N, 1, false, s);
+    if (direct_operand(c.N, c.dyd)) return product(c, operand, c.N, 1, false, kWsHeaderBytes, s);
     uint16_t *op = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
     const int64_t ld = operand_ld(c.N);
     PdlAttr attr;
     cudaLaunchConfig_t pre = {};
-    pre.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((c.T + 7) / 8, 1 << 20)), static_cast<unsigned>((ld / 8 + 31) / 32));
+    pre.gridDim = row_grid(c.T, ld);
     pre.blockDim = dim3(256);
     pre.stream = s;
     pre.attrs = attr.attr;
@@ -566,7 +661,7 @@ cudaError_t mx_backward(const Gradient &c, cudaStream_t s)
     const cudaError_t e = cudaLaunchKernelEx(&pre, planes_kernel, c.dy, c.dyd, c.T, c.N, c.N % 8 == 0, op, ld, planes);
     if (e != cudaSuccess) return e;
     operand[0] = op;
-    return product(c, operand, ld, planes, true, s);
+    return product(c, operand, ld, planes, true, kWsHeaderBytes + plane_bytes(c.N, c.T, c.dyd), s);
 }
 
 cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, const dbf_act8 &su, void *dg, void *du, cudaStream_t s)
@@ -594,7 +689,8 @@ cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, co
     pre.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&pre, c.dyd == DBF_F32 ? gate_back_kernel<DBF_F32> : gate_back_kernel<DBF_BF16>, a);
     if (e != cudaSuccess || !want) return e;
-    return product(c, operand, direct ? c.N : a.ld, direct ? 1 : a.planes, true, s);
+    return product(c, operand, direct ? c.N : a.ld, direct ? 1 : a.planes, true,
+                   kWsHeaderBytes + (direct ? 0 : 2 * plane_bytes(c.N, c.T, c.dyd)), s);
 }
 
 }  // namespace dbf

@@ -1,4 +1,4 @@
-// y = W q(x) and the gated block for few tokens: one launch, no pre-pass.
+// y = W q(x) and the gated block for few tokens.
 //
 // With few tokens every weight is used a handful of times, so the codes and
 // scales must stream from device memory at its full rate (17 bytes per 32
@@ -10,8 +10,10 @@
 //   warp 0      TMA ring of weight stages (256 columns), started before the
 //               kernel in front has ended where the caller allows it;
 //   warps 2..9  meanwhile quantise the CTA's columns of x into shared memory
-//               in the MMA's layout (each cluster does it again: T columns of
-//               a few KB that stay in L2, against one more launch);
+//               in the MMA's layout. Each cluster does it again, which up to
+//               kInline tokens is cheaper than a launch that does it once;
+//               beyond, a pre-pass leaves x's codes and scales in the workspace
+//               and warp 0 loads them;
 //   warp 1      one thread copies scales and issues the MMAs.
 // The partial sums then meet in shared memory: each CTA adds the S partials of
 // its share of (token, 32 rows) over distributed shared memory in CTA order,
@@ -28,7 +30,8 @@ using namespace mx;
 using namespace tc;
 
 constexpr int kMaxRing = 8;
-constexpr int kMaxTokens = 64;   // tokens of one tile, and of a call
+constexpr int kMaxTokens = 128;   // tokens of a call
+constexpr int kInline = 8;        // up to here the kernel quantises x itself
 constexpr int kWorkers = 8;
 constexpr int kThreads = 32 * (2 + kWorkers);
 constexpr uint32_t kABytes = 128 * 128, kSfBytes = 1024;
@@ -49,6 +52,7 @@ struct Args {
     const void *x;
     dbf_dtype xd;
     int vec;
+    int pre;     // x's codes and scales are in the workspace (mX, mXS)
     int early;   // weights may be read before earlier work is done
     uint32_t tmem_cols;
     Epilogue ep;
@@ -58,7 +62,8 @@ struct Args {
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
     const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1, const __grid_constant__ CUtensorMap mS0,
-    const __grid_constant__ CUtensorMap mS1, const __grid_constant__ Args g)
+    const __grid_constant__ CUtensorMap mS1, const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mXS,
+    const __grid_constant__ Args g)
 {
     constexpr int kMats = kGated ? 2 : 1;
     constexpr uint32_t kStage = kMats * (kABytes + kSfBytes);
@@ -79,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
             bar_init(&sh->full[i], 1);
             bar_init(&sh->empty[i], 1);
         }
-        bar_init(&sh->x_ready, kWorkers);
+        bar_init(&sh->x_ready, g.pre ? 1 : kWorkers);
         bar_init(&sh->done, 1);
         sh->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -96,6 +101,14 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
             if (!g.early) griddep_wait();
             int i = 0;
             for (; i < nks; ++i) {
+                if (g.pre && i == min(nks, g.ring) - 1) {   // after the first weights, before a wait for a free stage
+                    griddep_wait();
+                    bar_expect_tx(&sh->x_ready, nks * x_stage);
+                    for (int k = 0; k < nks; ++k) {
+                        tma_2d(xq + k * x_stage, &mX, (k0 + k) * 128, 0, &sh->x_ready);
+                        tma_3d(xq + k * x_stage + g.w * 128, &mXS, 0, (k0 + k) * 2, 0, &sh->x_ready);
+                    }
+                }
                 const int s = i % g.ring;
                 if (!bar_wait(&sh->empty[s], (static_cast<uint32_t>(i / g.ring) & 1u) ^ 1u, abort)) break;
                 uint8_t *st = ring + s * kStage;
@@ -105,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
                 tma_3d(st + kMats * kABytes, &mS0, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
                 if (kGated) tma_3d(st + kMats * kABytes + kSfBytes, &mS1, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
             }
+            if (*abort && g.pre && i >= min(nks, g.ring) - 1) drain_wait(&sh->x_ready, 0);
             if (*abort)
                 for (int j = i > g.ring ? i - g.ring : 0; j < i; ++j)
                     drain_wait(&sh->full[j % g.ring], static_cast<uint32_t>(j / g.ring) & 1u);
@@ -145,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
         const int worker = warp - 2;
         griddep_wait();     // x, y and the addends belong to earlier work until then
         griddep_launch();   // what follows may be set up: all earlier work is done
-        for (int u0 = worker; u0 < g.T * nks; u0 += 4 * kWorkers) {
+        for (int u0 = worker; u0 < g.T * nks && !g.pre; u0 += 4 * kWorkers) {
             float v[4][8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -170,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
         }
         fence_proxy_async();   // the MMA reads what these stores wrote
         __syncwarp();
-        if (lane == 0) bar_arrive(&sh->x_ready);
+        if (lane == 0 && !g.pre) bar_arrive(&sh->x_ready);
         if (bar_wait(&sh->done, 0, abort)) {
             tc_fence_after();
             const int quarter = warp & 3, half = worker >> 2;
@@ -217,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
 }
 
 struct Shape {
-    int w, split, ring, nks;
-    size_t smem;
+    int w, split, ring, nks, pre;
+    size_t smem, codes, scales, workspace;   // offsets of x's codes and scales in the workspace
 };
 
 // Split of the columns and ring depth; false when the CTA's columns of x do
@@ -236,13 +250,21 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
     while (split < std::min<int64_t>(8, nk) && (nk + split - 1) / split * x_stage > most) ++split;
     p.split = static_cast<int>(split);
     p.nks = static_cast<int>((nk + split - 1) / split);
-    const int64_t x_bytes = p.nks * x_stage;
+    const int64_t x_bytes = p.nks * x_stage, partials = int64_t{mats} * p.w * 512;
     if (x_bytes > most || row_blocks > 65535) return false;
+    p.pre = T > kInline ? 1 : 0;
+    p.codes = kWsHeaderBytes;
+    p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
+    p.workspace = p.pre ? align_up(p.scales + static_cast<size_t>(scale_tiles(M) * 512), 256) : kWsHeaderBytes;
     // two CTAs to an SM where that leaves three stages or all that are needed, else one
     const int want = std::min(kMaxRing, std::max(2, p.nks));
     const int64_t two = (113 * 1024 - fixed - x_bytes) / stage, one = (227 * 1024 - fixed - x_bytes) / stage;
     int64_t ring = two >= std::min(3, want) && row_blocks * split > device_sms() ? two : one;
-    p.ring = static_cast<int>(std::min<int64_t>(ring, want));
+    ring = std::min<int64_t>(ring, want);
+    // the partial sums take the place of the stages and of x
+    while (ring <= one && ring * stage + x_bytes < partials) ++ring;
+    if (ring > one) return false;
+    p.ring = static_cast<int>(ring);
     // at least a third of an SM: with two CTAs to an SM at most, their tensor
     // memory (256 columns each) is always there, so no CTA waits for it while
     // another of its cluster waits at the exchange
@@ -252,10 +274,10 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
 
 }  // namespace
 
-bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats)
+size_t mx_decode_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats)
 {
     Shape p;
-    return shape(M, N, T, mats, p);
+    return shape(M, N, T, mats, p) ? p.workspace : 0;
 }
 
 cudaError_t mx_decode(const Product &c, cudaStream_t s)
@@ -277,7 +299,23 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
             !tc_map(&sa[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, c.scales[from], sdims, sstrides, sbox, false))
             return cudaErrorInvalidValue;
     }
+    CUtensorMap xm = a[0], xs = sa[0];
+    uint8_t *codes = static_cast<uint8_t *>(c.ws) + p.codes, *scales = static_cast<uint8_t *>(c.ws) + p.scales;
+    if (p.pre) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(code_pitch(c.M)), static_cast<uint64_t>(c.T)};
+        const uint32_t box[2] = {128, static_cast<uint32_t>(p.w)};
+        const uint64_t tiles = static_cast<uint64_t>(scale_tiles(c.M));
+        const uint64_t sdims[3] = {128, tiles, 1};
+        const uint64_t sstrides[2] = {512, tiles * 512};
+        const uint32_t sbox[3] = {128, 2, 1};
+        if (!tc_map(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, dims, box, true) ||
+            !tc_map(&xs, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, scales, sdims, sstrides, sbox, false))
+            return cudaErrorInvalidValue;
+        const cudaError_t e = mx_quantize_x(c, p.w, 128, codes, scales, s);
+        if (e != cudaSuccess) return e;
+    }
     Args g = {};
+    g.pre = p.pre;
     g.nk = static_cast<int>((c.M + 255) / 256);
     g.w = p.w;
     g.ring = p.ring;
@@ -287,7 +325,7 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
     g.x = c.x;
     g.xd = c.xd;
     g.vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
-    g.early = c.flags & DBF_WEIGHTS_STATIC ? 1 : 0;
+    g.early = p.pre || (c.flags & DBF_WEIGHTS_STATIC) ? 1 : 0;
     const int cols = c.mats * p.w + 8 * c.mats + 8;
     g.tmem_cols = 32;
     while (static_cast<int>(g.tmem_cols) < cols) g.tmem_cols *= 2;
@@ -310,7 +348,7 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], sa[0], sa[1], g);
+    return cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], sa[0], sa[1], xm, xs, g);
 }
 
 }  // namespace dbf

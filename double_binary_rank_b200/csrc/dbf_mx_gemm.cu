@@ -249,8 +249,7 @@ template <dbf_dtype DT>
 __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict__ x, int64_t T, int64_t M, bool vec, int w, int pad,
                                   uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
 {
-    griddep_wait();     // the workspace may still be read by the call before
-    griddep_launch();   // so the product's launch starts with all earlier work done
+    griddep_wait();   // the workspace may still be read by the call before
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
     const int64_t nb = blocks(M), pitch = nb * 16, tiles = scale_tiles(M);
@@ -272,6 +271,10 @@ __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict_
         if ((lane & 15) == 0 && (c >> 7) < tiles)
             *reinterpret_cast<uint32_t *>(scales + scale_at(r / w * pad + r % w, c >> 5, tiles)) = word;
     }
+    // Only now: the product's CTAs would take the registers of this kernel's
+    // (one of its CTAs beside a product's on an SM against four alone). They
+    // then start with all earlier work done.
+    griddep_launch();
 }
 
 int resident_pairs(const void *kernel, cudaLaunchConfig_t cfg)
@@ -369,6 +372,22 @@ bool tc_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ba
 
 size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats) { return plan(M, N, T, mats).total; }
 
+cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint8_t *scales, cudaStream_t s)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+    return cudaLaunchKernelEx(&cfg, c.xd == DBF_F32 ? quantize_x_kernel<DBF_F32> : quantize_x_kernel<DBF_BF16>, c.x, c.T, c.M, vec,
+                              w, pad, codes, scales);
+}
+
 cudaError_t mx_gemm(const Product &c, cudaStream_t s)
 {
     const Plan pl = plan(c.M, c.N, c.T, c.mats);
@@ -391,15 +410,7 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
 
-    cudaLaunchConfig_t pre = {};
-    pre.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + 255) / 256));
-    pre.blockDim = dim3(256);
-    pre.stream = s;
-    pre.attrs = attr;
-    pre.numAttrs = 1;
-    const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
-    cudaError_t e = cudaLaunchKernelEx(&pre, c.xd == DBF_F32 ? quantize_x_kernel<DBF_F32> : quantize_x_kernel<DBF_BF16>, c.x, c.T,
-                                       c.M, vec, pl.w, pl.pad, codes, scales);
+    cudaError_t e = mx_quantize_x(c, pl.w, pl.pad, codes, scales, s);
     if (e != cudaSuccess) return e;
 
     const auto kernel = gated ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
