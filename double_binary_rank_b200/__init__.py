@@ -578,27 +578,28 @@ def forward_segmented(table: AdapterTable, seg_offsets: torch.Tensor, seg_adapte
 # current and, without an explicit stream, on its current stream.
 
 _GATES = {"silu": 0, "gelu": 1}
+_ACT = (torch.float32, torch.bfloat16)
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
 
 
-class _On:
-    """Makes the tensors' device current for a call and gives its stream."""
+def _enter(t: torch.Tensor, stream) -> Tuple[int, Optional[int]]:
+    """(stream handle, device to go back to after the call or None); makes the
+    tensor's device current."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    cur = torch.cuda.current_device()
+    if cur != dev:
+        torch.cuda.set_device(dev)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    return s.cuda_stream, None if cur == dev else cur
 
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        self.dev, self.stream, self.old = t.device.index, stream, None
 
-    def __enter__(self) -> int:
-        cur = torch.cuda.current_device()
-        if cur != self.dev:
-            self.old = cur
-            torch.cuda.set_device(self.dev)
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.old is not None:
-            torch.cuda.set_device(self.old)
+def _leave(back: Optional[int]) -> None:
+    if back is not None:
+        torch.cuda.set_device(back)
 
 
 def _need(t: Optional[torch.Tensor], name: str, shape, dtypes, like: torch.Tensor) -> None:
@@ -606,21 +607,21 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtypes, like: torch.Tenso
     type, on the same device."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != like.device:
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{name}: expected a contiguous {tuple(shape)} tensor of {[str(d) for d in dtypes]} on "
                          f"{like.device}, got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
 
 
-_ACT = (torch.float32, torch.bfloat16)
-_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
-_U8 = (torch.uint8,)
-
-
 def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
     """A workspace of one call: only its header has to be zero."""
-    ws = torch.empty(max(int(nbytes), WS_HEADER_BYTES), dtype=torch.uint8, device=like.device)
+    ws = like.new_empty(max(int(nbytes), WS_HEADER_BYTES), dtype=torch.uint8)
     ws[:WS_HEADER_BYTES].zero_()
     return ws
+
+
+def _ws(ws: Optional[torch.Tensor], like: torch.Tensor) -> None:
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != like.get_device()):
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {like.device}, got {ws.dtype} on {ws.device}")
 
 
 def _mx4_shapes(rows: int, k: int):
@@ -635,15 +636,19 @@ def mx4_quantize(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales
     Returns (codes [rows, ceil(k/32) * 16], scales [row tiles, block tiles, 32, 4, 4]), uint8."""
     rows, k = src.shape
     src = src.contiguous()
-    _need(src, "src", (rows, k), _FLOATS, src)
     cs, ss = _mx4_shapes(rows, k)
-    with _On(src, stream) as s:
-        codes = torch.empty(cs, dtype=torch.uint8, device=src.device) if codes is None else codes
-        scales = torch.empty(ss, dtype=torch.uint8, device=src.device) if scales is None else scales
+    _need(src, "src", (rows, k), _FLOATS, src)
+    _need(status, "status", (1,), _I32, src)
+    s, back = _enter(src, stream)
+    try:
+        codes = src.new_empty(cs, dtype=torch.uint8) if codes is None else codes
+        scales = src.new_empty(ss, dtype=torch.uint8) if scales is None else scales
         _need(codes, "codes", cs, _U8, src)
         _need(scales, "scales", ss, _U8, src)
         _check(_lib.dbf_mx4_quantize(_ptr(src), _DT[src.dtype], rows, k, _ptr(codes), codes.numel(), _ptr(scales),
                                      scales.numel(), _ptr(status), s), "dbf_mx4_quantize")
+    finally:
+        _leave(back)
     return codes, scales
 
 
@@ -653,15 +658,18 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int,
     cs, ss = _mx4_shapes(rows, k)
     _need(codes, "codes", cs, _U8, codes)
     _need(scales, "scales", ss, _U8, codes)
-    with _On(codes, stream) as s:
-        out = torch.empty((rows, k), dtype=dtype, device=codes.device) if out is None else out
+    s, back = _enter(codes, stream)
+    try:
+        out = codes.new_empty((rows, k), dtype=dtype) if out is None else out
         _need(out, "out", (rows, k), _FLOATS, codes)
         _check(_lib.dbf_mx4_dequantize(_ptr(codes), _ptr(scales), rows, k, _ptr(out), _DT[out.dtype], s),
                "dbf_mx4_dequantize")
+    finally:
+        _leave(back)
     return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class Mx4Layer:
     """Device-resident 4-bit layer W [N, M]: codes [N, ceil(M/32) * 16] and
     tiled scales [ceil(N/128), ceil(M/128), 32, 4, 4], uint8."""
@@ -669,6 +677,12 @@ class Mx4Layer:
     N: int
     codes: torch.Tensor
     scales: torch.Tensor
+
+    def __post_init__(self):
+        cs, ss = _mx4_shapes(self.N, self.M)
+        _need(self.codes, "codes", cs, _U8, self.codes)
+        _need(self.scales, "scales", ss, _U8, self.codes)
+        object.__setattr__(self, "_c", DbfMx4LayerC(self.M, self.N, _ptr(self.codes), _ptr(self.scales)))
 
     @staticmethod
     def quantize(W: torch.Tensor, stream=None) -> "Mx4Layer":
@@ -679,15 +693,11 @@ class Mx4Layer:
         return mx4_dequantize(self.codes, self.scales, self.N, self.M, dtype=dtype, stream=stream)
 
     def descriptor(self) -> DbfMx4LayerC:
-        cs, ss = _mx4_shapes(self.N, self.M)
-        _need(self.codes, "codes", cs, _U8, self.codes)
-        _need(self.scales, "scales", ss, _U8, self.codes)
-        return DbfMx4LayerC(self.M, self.N, _ptr(self.codes), _ptr(self.scales))
+        return self._c
 
 
 def mx4_workspace_bytes(layer: Mx4Layer, T: int) -> int:
-    d = layer.descriptor()
-    return int(_lib.dbf_mx4_workspace_bytes(ctypes.byref(d), T))
+    return int(_lib.dbf_mx4_workspace_bytes(layer._c, T))
 
 
 def mx4_forward(layer: Mx4Layer, x: torch.Tensor, y: Optional[torch.Tensor] = None, accumulate: bool = False,
@@ -696,21 +706,51 @@ def mx4_forward(layer: Mx4Layer, x: torch.Tensor, y: Optional[torch.Tensor] = No
     """y = [acc] y + W q(x) (dbf_mx4_forward). x: [T, M] float32/bfloat16."""
     T = x.shape[0]
     _need(x, "x", (T, layer.M), _ACT, layer.codes)
-    d = layer.descriptor()
-    with _On(x, stream) as s:
+    _ws(ws, x)
+    s, back = _enter(x, stream)
+    try:
         if y is None:
             if accumulate:
                 raise ValueError("accumulate needs y")
-            y = torch.empty((T, layer.N), dtype=y_dtype or x.dtype, device=x.device)
+            y = x.new_empty((T, layer.N), dtype=y_dtype)
         _need(y, "y", (T, layer.N), _ACT, x)
         if ws is None:
-            ws = _scratch(_lib.dbf_mx4_workspace_bytes(ctypes.byref(d), T), x)
-        _check(_lib.dbf_mx4_forward(ctypes.byref(d), _ptr(x), _DT[x.dtype], _ptr(y), _DT[y.dtype], T,
+            ws = _scratch(_lib.dbf_mx4_workspace_bytes(layer._c, T), x)
+        _check(_lib.dbf_mx4_forward(layer._c, _ptr(x), _DT[x.dtype], _ptr(y), _DT[y.dtype], T,
                                     _flags(accumulate, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_forward")
+    finally:
+        _leave(back)
     return y
 
 
-@dataclass
+def mx4_backward_workspace_bytes(layer: Mx4Layer, T: int, dtype: torch.dtype) -> int:
+    return int(_lib.dbf_mx4_backward_workspace_bytes(layer._c, T, _DT[dtype]))
+
+
+def mx4_backward(layer: Mx4Layer, dy: torch.Tensor, dx: Optional[torch.Tensor] = None, accumulate: bool = False,
+                 ws: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None, static_weights: bool = False,
+                 stream=None) -> torch.Tensor:
+    """dx = [acc] dx + dy W (dbf_mx4_backward). dy: [T, N] float32/bfloat16."""
+    T = dy.shape[0]
+    _need(dy, "dy", (T, layer.N), _ACT, layer.codes)
+    _ws(ws, dy)
+    s, back = _enter(dy, stream)
+    try:
+        if dx is None:
+            if accumulate:
+                raise ValueError("accumulate needs dx")
+            dx = dy.new_empty((T, layer.M), dtype=dx_dtype)
+        _need(dx, "dx", (T, layer.M), _ACT, dy)
+        if ws is None:
+            ws = _scratch(_lib.dbf_mx4_backward_workspace_bytes(layer._c, T, _DT[dy.dtype]), dy)
+        _check(_lib.dbf_mx4_backward(layer._c, _ptr(dy), _DT[dy.dtype], _ptr(dx), _DT[dx.dtype], T,
+                                     _flags(accumulate, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_backward")
+    finally:
+        _leave(back)
+    return dx
+
+
+@dataclass(frozen=True)
 class Act8:
     """An activation kept in 8 bits: codes [rows, ceil(cols/32) * 32] and
     scales [ceil(cols/32), rows], uint8."""
@@ -719,6 +759,12 @@ class Act8:
     codes: torch.Tensor
     scales: torch.Tensor
 
+    def __post_init__(self):
+        nb = -(-self.cols // 32)
+        _need(self.codes, "codes", (self.rows, nb * 32), _U8, self.codes)
+        _need(self.scales, "scales", (nb, self.rows), _U8, self.codes)
+        object.__setattr__(self, "_c", DbfAct8C(_ptr(self.codes), _ptr(self.scales)))
+
     @staticmethod
     def empty(rows: int, cols: int, device) -> "Act8":
         nb = -(-cols // 32)
@@ -726,10 +772,13 @@ class Act8:
                     torch.empty((nb, rows), dtype=torch.uint8, device=device))
 
     def descriptor(self) -> DbfAct8C:
-        nb = -(-self.cols // 32)
-        _need(self.codes, "codes", (self.rows, nb * 32), _U8, self.codes)
-        _need(self.scales, "scales", (nb, self.rows), _U8, self.codes)
-        return DbfAct8C(_ptr(self.codes), _ptr(self.scales))
+        return self._c
+
+
+def _act8(a: Act8, rows: int, cols: int, like: torch.Tensor) -> DbfAct8C:
+    if a.rows != rows or a.cols != cols or a.codes.get_device() != like.get_device():
+        raise ValueError(f"8-bit activation: expected {(rows, cols)} on {like.device}, got {(a.rows, a.cols)} on {a.codes.device}")
+    return a._c
 
 
 def act8_save(src: torch.Tensor, out: Optional[Act8] = None, status: Optional[torch.Tensor] = None, stream=None) -> Act8:
@@ -737,36 +786,31 @@ def act8_save(src: torch.Tensor, out: Optional[Act8] = None, status: Optional[to
     rows, cols = src.shape
     src = src.contiguous()
     _need(src, "src", (rows, cols), _FLOATS, src)
-    with _On(src, stream) as s:
+    _need(status, "status", (1,), _I32, src)
+    s, back = _enter(src, stream)
+    try:
         out = Act8.empty(rows, cols, src.device) if out is None else out
-        if (out.rows, out.cols) != (rows, cols) or out.codes.device != src.device:
-            raise ValueError("out: another shape or device than src")
-        d = out.descriptor()
-        _check(_lib.dbf_act8_save(_ptr(src), _DT[src.dtype], rows, cols, ctypes.byref(d), _ptr(status), s), "dbf_act8_save")
+        _check(_lib.dbf_act8_save(_ptr(src), _DT[src.dtype], rows, cols, _act8(out, rows, cols, src), _ptr(status), s),
+               "dbf_act8_save")
+    finally:
+        _leave(back)
     return out
 
 
 def act8_load(a: Act8, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The values an Act8 stands for (dbf_act8_load)."""
-    with _On(a.codes, stream) as s:
-        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.codes.device) if out is None else out
+    s, back = _enter(a.codes, stream)
+    try:
+        out = a.codes.new_empty((a.rows, a.cols), dtype=dtype) if out is None else out
         _need(out, "out", (a.rows, a.cols), _FLOATS, a.codes)
-        d = a.descriptor()
-        _check(_lib.dbf_act8_load(ctypes.byref(d), a.rows, a.cols, _ptr(out), _DT[out.dtype], s), "dbf_act8_load")
+        _check(_lib.dbf_act8_load(a._c, a.rows, a.cols, _ptr(out), _DT[out.dtype], s), "dbf_act8_load")
+    finally:
+        _leave(back)
     return out
 
 
-def _saved(a: Optional[Act8], T: int, N: int, like: torch.Tensor):
-    if a is None:
-        return None
-    if (a.rows, a.cols) != (T, N) or a.codes.device != like.device:
-        raise ValueError(f"saved activation: expected {(T, N)} on {like.device}, got {(a.rows, a.cols)} on {a.codes.device}")
-    return a.descriptor()
-
-
 def mx4_gated_workspace_bytes(gate: Mx4Layer, up: Mx4Layer, T: int) -> int:
-    dg, du = gate.descriptor(), up.descriptor()
-    return int(_lib.dbf_mx4_gated_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T))
+    return int(_lib.dbf_mx4_gated_workspace_bytes(gate._c, up._c, T))
 
 
 def mx4_gated_forward(gate: Mx4Layer, up: Mx4Layer, x: torch.Tensor, h: Optional[torch.Tensor] = None, act: str = "silu",
@@ -783,49 +827,25 @@ def mx4_gated_forward(gate: Mx4Layer, up: Mx4Layer, x: torch.Tensor, h: Optional
     _need(up.codes, "up.codes", gate.codes.shape, _U8, x)
     _need(g_add, "g_add", (T, N), _ACT, x)
     _need(u_add, "u_add", (T, N), _ACT if g_add is None else (g_add.dtype,), x)
-    dg, du = gate.descriptor(), up.descriptor()
-    sg, su = (_saved(a, T, N, x) for a in (save or (None, None)))
+    _ws(ws, x)
+    sg, su = (None, None) if save is None else (_act8(save[0], T, N, x), _act8(save[1], T, N, x))
     add = g_add if g_add is not None else u_add
-    with _On(x, stream) as s:
-        h = torch.empty((T, N), dtype=h_dtype or x.dtype, device=x.device) if h is None else h
+    s, back = _enter(x, stream)
+    try:
+        h = x.new_empty((T, N), dtype=h_dtype) if h is None else h
         _need(h, "h", (T, N), _ACT, x)
         if ws is None:
-            ws = _scratch(_lib.dbf_mx4_gated_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T), x)
-        _check(_lib.dbf_mx4_gated_forward(ctypes.byref(dg), ctypes.byref(du), _GATES[act], _ptr(x), _DT[x.dtype], _ptr(g_add),
-                                          _ptr(u_add), F32 if add is None else _DT[add.dtype], _ptr(h), _DT[h.dtype],
-                                          sg and ctypes.byref(sg), su and ctypes.byref(su), T, _flags(False, static_weights),
-                                          _ptr(ws), ws.numel(), s), "dbf_mx4_gated_forward")
+            ws = _scratch(_lib.dbf_mx4_gated_workspace_bytes(gate._c, up._c, T), x)
+        _check(_lib.dbf_mx4_gated_forward(gate._c, up._c, _GATES[act], _ptr(x), _DT[x.dtype], _ptr(g_add), _ptr(u_add),
+                                          F32 if add is None else _DT[add.dtype], _ptr(h), _DT[h.dtype], sg, su, T,
+                                          _flags(False, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_gated_forward")
+    finally:
+        _leave(back)
     return h
 
 
-def mx4_backward_workspace_bytes(layer: Mx4Layer, T: int, dtype: torch.dtype) -> int:
-    d = layer.descriptor()
-    return int(_lib.dbf_mx4_backward_workspace_bytes(ctypes.byref(d), T, _DT[dtype]))
-
-
-def mx4_backward(layer: Mx4Layer, dy: torch.Tensor, dx: Optional[torch.Tensor] = None, accumulate: bool = False,
-                 ws: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None, static_weights: bool = False,
-                 stream=None) -> torch.Tensor:
-    """dx = [acc] dx + dy W (dbf_mx4_backward). dy: [T, N] float32/bfloat16."""
-    T = dy.shape[0]
-    _need(dy, "dy", (T, layer.N), _ACT, layer.codes)
-    d = layer.descriptor()
-    with _On(dy, stream) as s:
-        if dx is None:
-            if accumulate:
-                raise ValueError("accumulate needs dx")
-            dx = torch.empty((T, layer.M), dtype=dx_dtype or dy.dtype, device=dy.device)
-        _need(dx, "dx", (T, layer.M), _ACT, dy)
-        if ws is None:
-            ws = _scratch(_lib.dbf_mx4_backward_workspace_bytes(ctypes.byref(d), T, _DT[dy.dtype]), dy)
-        _check(_lib.dbf_mx4_backward(ctypes.byref(d), _ptr(dy), _DT[dy.dtype], _ptr(dx), _DT[dx.dtype], T,
-                                     _flags(accumulate, static_weights), _ptr(ws), ws.numel(), s), "dbf_mx4_backward")
-    return dx
-
-
 def mx4_gated_backward_workspace_bytes(gate: Mx4Layer, up: Mx4Layer, T: int, dtype: torch.dtype) -> int:
-    dg, du = gate.descriptor(), up.descriptor()
-    return int(_lib.dbf_mx4_gated_backward_workspace_bytes(ctypes.byref(dg), ctypes.byref(du), T, _DT[dtype]))
+    return int(_lib.dbf_mx4_gated_backward_workspace_bytes(gate._c, up._c, T, _DT[dtype]))
 
 
 def mx4_gated_backward(gate: Mx4Layer, up: Mx4Layer, dh: torch.Tensor, saved: Tuple[Act8, Act8], act: str = "silu",
@@ -838,9 +858,10 @@ def mx4_gated_backward(gate: Mx4Layer, up: Mx4Layer, dh: torch.Tensor, saved: Tu
     T, N = dh.shape[0], gate.N
     _need(dh, "dh", (T, N), _ACT, gate.codes)
     _need(up.codes, "up.codes", gate.codes.shape, _U8, dh)
-    cg, cu = gate.descriptor(), up.descriptor()
-    sg, su = (_saved(a, T, N, dh) for a in saved)
-    with _On(dh, stream) as s:
+    _ws(ws, dh)
+    sg, su = _act8(saved[0], T, N, dh), _act8(saved[1], T, N, dh)
+    s, back = _enter(dh, stream)
+    try:
         dg = torch.empty_like(dh) if dg is None else dg
         du = torch.empty_like(dh) if du is None else du
         _need(dg, "dg", (T, N), (dh.dtype,), dh)
@@ -848,14 +869,16 @@ def mx4_gated_backward(gate: Mx4Layer, up: Mx4Layer, dh: torch.Tensor, saved: Tu
         if want_dx and dx is None:
             if accumulate:
                 raise ValueError("accumulate needs dx")
-            dx = torch.empty((T, gate.M), dtype=dx_dtype or dh.dtype, device=dh.device)
+            dx = dh.new_empty((T, gate.M), dtype=dx_dtype)
         if not want_dx:
             dx = None
         _need(dx, "dx", (T, gate.M), _ACT, dh)
         if ws is None and want_dx:
-            ws = _scratch(_lib.dbf_mx4_gated_backward_workspace_bytes(ctypes.byref(cg), ctypes.byref(cu), T, _DT[dh.dtype]), dh)
-        _check(_lib.dbf_mx4_gated_backward(ctypes.byref(cg), ctypes.byref(cu), _GATES[act], ctypes.byref(sg), ctypes.byref(su),
-                                           _ptr(dh), _DT[dh.dtype], _ptr(dg), _ptr(du), _ptr(dx),
-                                           F32 if dx is None else _DT[dx.dtype], T, _flags(accumulate, static_weights),
-                                           _ptr(ws), 0 if ws is None else ws.numel(), s), "dbf_mx4_gated_backward")
+            ws = _scratch(_lib.dbf_mx4_gated_backward_workspace_bytes(gate._c, up._c, T, _DT[dh.dtype]), dh)
+        _check(_lib.dbf_mx4_gated_backward(gate._c, up._c, _GATES[act], sg, su, _ptr(dh), _DT[dh.dtype], _ptr(dg), _ptr(du),
+                                           _ptr(dx), F32 if dx is None else _DT[dx.dtype], T,
+                                           _flags(accumulate, static_weights), _ptr(ws), 0 if ws is None else ws.numel(), s),
+               "dbf_mx4_gated_backward")
+    finally:
+        _leave(back)
     return dx, dg, du

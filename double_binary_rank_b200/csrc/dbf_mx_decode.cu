@@ -11,7 +11,7 @@
 //               kernel in front has ended where the caller allows it;
 //   warps 2..9  meanwhile quantise the CTA's columns of x into shared memory
 //               in the MMA's layout. Each cluster does it again, which up to
-//               kInline tokens is cheaper than a launch that does it once;
+//               kInline pieces of 256 columns is cheaper than a launch that does it once;
 //               beyond, a pre-pass leaves x's codes and scales in the workspace
 //               and warp 0 loads them;
 //   warp 1      one thread copies scales and issues the MMAs.
@@ -30,8 +30,8 @@ using namespace mx;
 using namespace tc;
 
 constexpr int kMaxRing = 8;
-constexpr int kMaxTokens = 128;   // tokens of a call
-constexpr int kInline = 8;        // up to here the kernel quantises x itself
+constexpr int kMaxColumns = 64;   // tokens of a call times its weights: beyond, dbf_mx_gemm.cu is faster
+constexpr int kInline = 48;       // rows of 256 columns of x up to which a CTA quantises its part itself
 constexpr int kWorkers = 8;
 constexpr int kThreads = 32 * (2 + kWorkers);
 constexpr uint32_t kABytes = 128 * 128, kSfBytes = 1024;
@@ -235,41 +235,46 @@ struct Shape {
     size_t smem, codes, scales, workspace;   // offsets of x's codes and scales in the workspace
 };
 
-// Split of the columns and ring depth; false when the CTA's columns of x do
-// not fit in shared memory.
+// Split of the columns, ring depth and CTAs to an SM; false when the CTA's
+// columns of x do not fit in shared memory.
 bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
 {
-    if (T > kMaxTokens) return false;
-    const int64_t nk = (M + 255) / 256, row_blocks = (N + 127) / 128;
-    const int stage = mats * static_cast<int>(kABytes + kSfBytes);
+    if (T > kMaxColumns / mats) return false;
+    const int64_t nk = (M + 255) / 256, row_blocks = (N + 127) / 128, sms = device_sms();
+    if (row_blocks > 65535) return false;
     p.w = static_cast<int>((T + 15) / 16 * 16);
-    const int64_t slots = 2 * device_sms();
-    int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, nk, slots / row_blocks}));
-    const int64_t x_stage = p.w * 128 + 1024;
-    const int64_t fixed = 1024 + sizeof(Smem), most = 227 * 1024 - fixed - 3 * stage;
-    while (split < std::min<int64_t>(8, nk) && (nk + split - 1) / split * x_stage > most) ++split;
-    p.split = static_cast<int>(split);
-    p.nks = static_cast<int>((nk + split - 1) / split);
-    const int64_t x_bytes = p.nks * x_stage, partials = int64_t{mats} * p.w * 512;
-    if (x_bytes > most || row_blocks > 65535) return false;
-    p.pre = T > kInline ? 1 : 0;
-    p.codes = kWsHeaderBytes;
-    p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
-    p.workspace = p.pre ? align_up(p.scales + static_cast<size_t>(scale_tiles(M) * 512), 256) : kWsHeaderBytes;
-    // two CTAs to an SM where that leaves three stages or all that are needed, else one
-    const int want = std::min(kMaxRing, std::max(2, p.nks));
-    const int64_t two = (113 * 1024 - fixed - x_bytes) / stage, one = (227 * 1024 - fixed - x_bytes) / stage;
-    int64_t ring = two >= std::min(3, want) && row_blocks * split > device_sms() ? two : one;
-    ring = std::min<int64_t>(ring, want);
-    // the partial sums take the place of the stages and of x
-    while (ring <= one && ring * stage + x_bytes < partials) ++ring;
-    if (ring > one) return false;
-    p.ring = static_cast<int>(ring);
-    // at least a third of an SM: with two CTAs to an SM at most, their tensor
-    // memory (256 columns each) is always there, so no CTA waits for it while
-    // another of its cluster waits at the exchange
-    p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + p.ring * stage, 77 * 1024));
-    return p.ring >= 2;
+    const int64_t stage = mats * int64_t{kABytes + kSfBytes}, x_stage = p.w * 128 + 1024, partials = int64_t{mats} * p.w * 512;
+    const int64_t fixed = 1024 + sizeof(Smem);
+    for (int per_sm = 2; per_sm >= 1; --per_sm) {
+        const int64_t room = (per_sm == 2 ? 113 : 227) * 1024 - fixed;
+        int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, nk, per_sm * sms / row_blocks}));
+        // one CTA to an SM where that occupies four fifths of them and a CTA's
+        // weights are all in flight at once (4096 x 4096 at one token: 6.2 us split
+        // in 4, 7.0 us in 8; 8192 x 8192, whose CTAs would take 16 stages: 13.0 us
+        // at one to an SM, 10.2 us at two)
+        const int64_t one = sms / row_blocks;
+        if (one >= 1 && one <= 8 && one * row_blocks * 5 >= sms * 4 && (nk + one - 1) / one <= kMaxRing) split = std::min(one, nk);
+        for (; split <= std::min<int64_t>(8, nk); ++split) {
+            p.split = static_cast<int>(split);
+            p.nks = static_cast<int>((nk + split - 1) / split);
+            const int64_t x_bytes = p.nks * x_stage, fit = (room - x_bytes) / stage;
+            if (fit < 2) continue;
+            int64_t ring = std::min<int64_t>({fit, kMaxRing, std::max(2, p.nks)});
+            while (ring < fit && ring * stage + x_bytes < partials) ++ring;   // the partial sums take this place
+            if (ring * stage + x_bytes < partials) continue;
+            p.ring = static_cast<int>(ring);
+            // at least a third of an SM: with two CTAs to an SM at most, their tensor
+            // memory (256 columns each) is always there, so no CTA waits for it while
+            // another of its cluster waits at the exchange
+            p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + ring * stage, 77 * 1024));
+            p.pre = T * p.nks > kInline ? 1 : 0;
+            p.codes = kWsHeaderBytes;
+            p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
+            p.workspace = p.pre ? align_up(p.scales + static_cast<size_t>(scale_tiles(M) * 512), 256) : kWsHeaderBytes;
+            return true;
+        }
+    }
+    return false;
 }
 
 }  // namespace
