@@ -323,6 +323,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 ep.yd = DBF_F32;
                 ep.accumulate = 0;
             }
+            if (epilogue_is_simple(ep)) {
+                if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
+                acc_ph ^= 1u;
+                tc_fence_after();
+                for (int j = 0; j < g.w / 2; j += 16) {
+                    float v[1][16];
+                    tmem_ld16(from + j, v);
+                    simple_finish<1>(ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+                continue;
+            }
             Raw8 x[2][1];   // what a chunk of 8 tokens reads is asked for a chunk ahead
             epilogue_reads<false>(ep, t, n, t < ep.T, x[0]);
             if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;

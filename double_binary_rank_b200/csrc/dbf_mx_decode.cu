@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
             tc_fence_after();
             const int quarter = warp & 3, half = worker >> 2;
             for (int col = half * 16; col < kMats * g.w; col += 32) {
-                float v[16];
+                float v[1][16];
                 tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col, v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(col + j) * 128 + quarter * 32 + lane] = v[j];
+                for (int j = 0; j < 16; ++j) part[(col + j) * 128 + quarter * 32 + lane] = v[0][j];
             }
         }
     }

@@ -15,12 +15,17 @@
 // 256 x 240 would take 34 KB per 480.
 //   warp 0      TMA: per stage of 256 columns, 2 x 128 rows of codes (128-byte
 //               swizzle), w/2 token rows, and their scale tiles;
-//   warp 1      tensor memory; in CTA 0 one thread copies the stage's scales
-//               into tensor memory (tcgen05.cp) and issues eight MMAs;
-//   warps 2..9  epilogue.
-// The token width w is chosen per call (a multiple of 16 up to 240, what 512
-// tensor-memory columns hold beside 32 of scales) so that the tiles fill whole
-// waves of pairs. Every wait is bounded; on expiry the status word is set.
+//   warp 1      tensor memory; in CTA 0 one thread issues eight MMAs a stage;
+//   warps 2..5  bring the stage's scales into tensor memory, each into its own
+//               32 lanes, through registers. tcgen05.cp would do it too, but
+//               runs in the MMAs' own queue: at about 70 cycles a copy, eight
+//               of them a stage took a fifth of the time of an 8192^3 product
+//               (316 us, and 249 us without them);
+//   warps 6..13 epilogue.
+// The token width w is chosen per call (a multiple of 16 up to 224, what 512
+// tensor-memory columns hold beside two buffers of 32 of scales) so that the
+// tiles fill whole waves of pairs. Every wait is bounded; on expiry the status
+// word is set.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -35,18 +40,19 @@ using namespace mx;
 using namespace tc;
 
 constexpr int kStages = 4;
-constexpr int kMaxW = 240;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kMaxW = 224;
+constexpr int kScaleWarps = 4, kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kScaleWarps + kEpiWarps);
 constexpr uint32_t kABytes = 128 * 128;            // 128 rows x 256 codes
 constexpr uint32_t kBBytes = kMaxW / 2 * 128;      // this CTA's half of the tokens
 constexpr uint32_t kSfABytes = 1024, kSfBBytes = 2048;
 constexpr uint32_t kStageBytes = 2 * kABytes + kBBytes + 2 * kSfABytes + kSfBBytes;
-constexpr uint32_t kSfCol = 480;   // tensor-memory columns: 2 w of accumulators, then scales
+constexpr uint32_t kSfCol = 448;   // tensor-memory columns: 2 w of accumulators, then scales
+constexpr uint32_t kSfCols = 32;   // of one stage: 8 per accumulator (4 per K half), then 16 of the tokens (8 per K half)
 constexpr uint32_t kTmemCols = 512;
 
 struct Smem {
-    uint64_t full[kStages], empty[kStages], acc_full, acc_empty, drain, exit_bar;
+    uint64_t full[kStages], sf_full[kStages], empty[kStages], sf_ready[2], acc_full, acc_empty, drain, exit_bar;
     uint32_t tmem_base;
     int abort;
 };
@@ -64,6 +70,8 @@ struct Args {
 
 __device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][8]) { tmem_ld8(at, col); }
 __device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][8]) { tmem_ld8(at, at + w, col); }
+__device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][16]) { tmem_ld16(at, col); }
+__device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][16]) { tmem_ld16(at, at + w, col); }
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
@@ -84,8 +92,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(&sh->full[i], 1);
+            bar_init(&sh->sf_full[i], 1);
             bar_init(&sh->empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) bar_init(&sh->sf_ready[i], 2 * kScaleWarps);
         bar_init(&sh->acc_full, 1);
         bar_init(&sh->acc_empty, 2 * kEpiWarps);
         bar_init(&sh->drain, 1);
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     if (warp == 0) {
         if (lane == 0) {
             const int half_w = g.w / 2, nrt = g.w > 128 ? 2 : 1;
-            const uint32_t bytes = 2 * (2 * kABytes + half_w * 128 + 2 * kSfABytes + nrt * 1024);
+            const uint32_t bytes = 2 * (2 * kABytes + half_w * 128), sf_bytes = 2 * kSfABytes + nrt * 1024;
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true, waited = false;
@@ -124,58 +134,49 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                     tma_2d_pair(st, &mA0, ks * 128, row0, &sh->full[s]);
                     tma_2d_pair(st + kABytes, &mA1, ks * 128, row1, &sh->full[s]);
                     uint8_t *sf = st + 2 * kABytes + kBBytes;
-                    tma_3d_pair(sf, &mS0, 0, ks * 2, row0 >> 7, &sh->full[s]);
-                    tma_3d_pair(sf + kSfABytes, &mS1, 0, ks * 2, row1 >> 7, &sh->full[s]);
+                    // the scales are counted by each CTA for itself
+                    bar_expect_tx(&sh->sf_full[s], sf_bytes);
+                    tma_3d(sf, &mS0, 0, ks * 2, row0 >> 7, &sh->sf_full[s]);
+                    tma_3d(sf + kSfABytes, &mS1, 0, ks * 2, row1 >> 7, &sh->sf_full[s]);
                     if (!waited) {
                         griddep_wait();
                         waited = true;
                     }
                     tma_2d_pair(st + 2 * kABytes, &mB, ks * 128, tok, &sh->full[s]);
-                    tma_3d_pair(sf + 2 * kSfABytes, &mSB, 0, ks * 2, c * nrt, &sh->full[s]);
+                    tma_3d(sf + 2 * kSfABytes, &mSB, 0, ks * 2, c * nrt, &sh->sf_full[s]);
                     ++issued;
                     if (++s == kStages) s = 0, ph ^= 1u;
                 }
             }
             // after a wait gave up, the loads in flight are still waited for
             // (CTA 0's barriers count both CTAs' bytes)
-            if (*abort && rank == 0)
-                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+            if (*abort)
+                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+                    drain_wait(&sh->sf_full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+                    if (rank == 0) drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+                }
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             int s = 0;
-            uint32_t ph = 0, acc_ph = 0;
+            uint32_t ph = 0, acc_ph = 0, k = 0;   // k: stages so far; its lowest bit is the scale buffer
             bool ok = true;
-            const int nrt = g.w > 128 ? 2 : 1;
             const uint32_t id0 = mxf4_idesc(256, g.w, 0), id2 = mxf4_idesc(256, g.w, 2);
             for (int tile = unit; tile < g.tiles && ok; tile += units) {
                 ok = bar_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
                 if (!ok) break;
-                tc_fence_after();
-                for (int ks = 0; ks < g.nk; ++ks) {
-                    if (!bar_wait(&sh->full[s], ph, abort)) {
-                        ok = false;
-                        break;
-                    }
+                for (int ks = 0; ks < g.nk; ++ks, ++k) {
+                    ok = bar_wait(&sh->full[s], ph, abort) && bar_wait(&sh->sf_ready[k & 1u], (k >> 1) & 1u, abort);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(stage0) + s * kStageBytes;
-                    const uint32_t sf = st + 2 * kABytes + kBBytes;
-                    // scales: columns kSfCol + 8 m + 4 c of accumulator m, K half c; tokens from kSfCol + 16 on
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        scale_copy<2>(tmem + kSfCol + 4 * c, scale_desc(sf + c * 512));
-                        scale_copy<2>(tmem + kSfCol + 8 + 4 * c, scale_desc(sf + kSfABytes + c * 512));
-                        for (int r = 0; r < nrt; ++r)
-                            scale_copy<2>(tmem + kSfCol + 16 + 8 * c + 4 * r, scale_desc(sf + 2 * kSfABytes + r * 1024 + c * 512));
-                    }
+                    const uint32_t st = smem_u32(stage0) + s * kStageBytes, sf = tmem + kSfCol + (k & 1u) * kSfCols;
                     const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + 2 * kABytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t id = kk & 1 ? id2 : id0, acc = ks > 0 || kk > 0 ? 1u : 0u;
-                        const uint32_t sb = tmem + kSfCol + 16 + 8 * (kk >> 1);
-                        mma_mxf4<2>(tmem, a0 + 2 * kk, b + 2 * kk, id, tmem + kSfCol + 4 * (kk >> 1), sb, acc);
-                        mma_mxf4<2>(tmem + g.w, a1 + 2 * kk, b + 2 * kk, id, tmem + kSfCol + 8 + 4 * (kk >> 1), sb, acc);
+                        const uint32_t sb = sf + 16 + 8 * (kk >> 1);
+                        mma_mxf4<2>(tmem, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, acc);
+                        mma_mxf4<2>(tmem + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
                     }
                     commit_pair_both(&sh->empty[s]);
                     if (++s == kStages) s = 0, ph ^= 1u;
@@ -189,20 +190,55 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                 drain_wait(&sh->drain, 0);
             }
         }
+    } else if (warp < 2 + kScaleWarps) {
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const int64_t total = static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * g.nk;   // stages of this pair
+        int s = 0;
+        uint32_t ph = 0;
+        for (int64_t k = 0; k < total; ++k) {
+            // buffer k % 2 is free once the MMAs of stage k - 2 are done
+            const int s2 = (s + kStages - 2) % kStages;
+            if (k >= 2 && !bar_wait(&sh->empty[s2], static_cast<uint32_t>((k - 2) / kStages) & 1u, abort)) break;
+            if (!bar_wait(&sh->sf_full[s], ph, abort)) break;
+            tc_fence_after();
+            const uint4 *sf = reinterpret_cast<const uint4 *>(stage0 + s * kStageBytes + 2 * kABytes + kBBytes) + lane;
+            // 512 bytes hold 128 rows x 4 blocks, a lane's 16 the rows lane, lane + 32, ...
+            const uint4 v[8] = {sf[0], sf[32], sf[64], sf[96], sf[128], sf[192], sf[160], sf[224]};
+            tmem_st32(lanes + kSfCol + static_cast<uint32_t>(k & 1) * kSfCols, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_leader(&sh->sf_ready[k & 1]);
+            if (++s == kStages) s = 0, ph ^= 1u;
+        }
     } else {
         griddep_wait();   // y (and the addends) belong to earlier work until then
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kGated ? 0 : half * g.w);
-        float *own = turn + (warp - 2) * kMats * kTurnFloats;
+        float *own = turn + (warp - 2 - kScaleWarps) * kMats * kTurnFloats;
         // gated: the two warps of a lane quarter take turns by 8 tokens of both
         // accumulators; plain: each takes one accumulator
         const int j_first = kGated ? half * 8 : 0, j_step = kGated ? 16 : 8;
+        const bool simple = epilogue_is_simple(g.ep);
         uint32_t acc_ph = 0;
         for (int tile = unit; tile < g.tiles; tile += units) {
             const int p = tile % g.n_p, c = tile / g.n_p;
             const int n = p * g.row_step + (kGated ? 0 : half * g.row_off) + static_cast<int>(rank) * 128 + quarter * 32 +
                           (lane & 3) * 8;
             const int64_t t = static_cast<int64_t>(c) * g.w + (lane >> 2);
+            if (simple) {
+                if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
+                acc_ph ^= 1u;
+                tc_fence_after();
+                for (int j = kGated ? half * 16 : 0; j < g.w; j += kGated ? 32 : 16) {
+                    float v[kMats][16];
+                    load_chunk(lanes + j, g.w, v);
+                    simple_finish<kMats>(g.ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+                continue;
+            }
             // what a chunk reads is asked for a chunk ahead, the first before the products are there
             Raw8 x[2][kMats];
             epilogue_reads<kGated>(g.ep, t + j_first, n, t + j_first < g.ep.T, x[0]);

@@ -142,6 +142,45 @@ __device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], 
     }
 }
 
+// The epilogue where nothing but the products is read and the output is bf16
+// with rows of whole 16-byte vectors: 16 tokens at once are finished as they
+// come, a column of 16 tokens per lane, and turned as pairs of tokens in one
+// word: a third of the instructions of the general one, whose issue bounds the
+// prefill kernel's epilogue.
+__device__ __forceinline__ bool epilogue_is_simple(const Epilogue &e)
+{
+    return epilogue_vec(e) && e.yd == DBF_BF16 && !e.accumulate && !e.g_add && !e.u_add && !e.g8;
+}
+// n0: the warp's first column; own: kTurnFloats words
+template <int kMats>
+__device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, int64_t t0, int n0, const float (&v)[kMats][16])
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        float a = v[0][2 * p], b = v[0][2 * p + 1];
+        if (kMats == 2) {
+            a = gate_value(e.act, a) * v[kMats - 1][2 * p];
+            b = gate_value(e.act, b) * v[kMats - 1][2 * p + 1];
+        }
+        const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
+        own[p * 36 + lane] = *reinterpret_cast<const uint32_t *>(&w);
+    }
+    __syncwarp();
+    const int p = lane >> 2, c = n0 + (lane & 3) * 8;
+    const uint4 a = *reinterpret_cast<const uint4 *>(own + p * 36 + (lane & 3) * 8);
+    const uint4 b = *reinterpret_cast<const uint4 *>(own + p * 36 + (lane & 3) * 8 + 4);
+    if (c >= e.N) return;
+    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(e.y) + (t0 + 2 * p) * e.N + c;
+    if (t0 + 2 * p < e.T)
+        *reinterpret_cast<uint4 *>(y) = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                                   __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+    if (t0 + 2 * p + 1 < e.T)
+        *reinterpret_cast<uint4 *>(y + e.N) = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                                         __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+}
+
 // One call: a weight (plain) or two of one shape (gated), and its tokens.
 struct Product {
     int64_t M, N, T;
