@@ -193,7 +193,7 @@ __device__ __forceinline__ void store8(void *dst, dbf_dtype dt, int64_t row_star
 }
 
 // Eight values as loaded, so that the load can be issued long before its
-// conversion: bf16 in 'lo', fp32 in both.
+// conversion: 16-bit types in 'lo', fp32 (and all types without 'vec') in both.
 struct Raw8 {
     uint4 lo, hi;
 };
@@ -218,7 +218,27 @@ __device__ __forceinline__ Raw8 load_raw8(const void *src, dbf_dtype dt, int64_t
     r.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     return r;
 }
-// v += the eight values
+__device__ __forceinline__ void raw8_values(const Raw8 &r, dbf_dtype dt, bool vec, float (&v)[8])
+{
+    const uint32_t a[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if (dt == DBF_F32 || !vec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (dt == DBF_BF16) {
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+// v += the eight values (bf16 or fp32)
 __device__ __forceinline__ void add_raw8(const Raw8 &r, dbf_dtype dt, bool vec, float (&v)[8])
 {
     const uint32_t a[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
@@ -234,15 +254,19 @@ __device__ __forceinline__ void add_raw8(const Raw8 &r, dbf_dtype dt, bool vec, 
     }
 }
 
+// fp32 bits of the largest magnitude; a NaN among them gives a NaN (as
+// integers NaN > infinity > finite, so the comparisons across lanes keep it)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
 {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;   // as integers, NaN > infinity > finite
-        m = b > m ? b : m;
-    }
-    return m;
+    const float a = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
+    const float b = max_nan(max_nan(fabsf(v[4]), fabsf(v[5])), max_nan(fabsf(v[6]), fabsf(v[7])));
+    return __float_as_uint(max_nan(a, b)) & 0x7FFFFFFFu;
 }
 
 // The four lanes that hold one block agree on its largest magnitude.
@@ -254,27 +278,54 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t m)
     return b > m ? b : m;
 }
 
+// fp32 bits of the largest magnitude of the block that this lane and its three
+// neighbours hold. 16-bit values are compared two at a time, as integers.
+__device__ __forceinline__ uint32_t block_amax_raw(const Raw8 &r, dbf_dtype dt, bool vec)
+{
+    if (dt == DBF_F32 || !vec) {
+        float v[8];
+        raw8_values(r, DBF_F32, true, v);
+        return block_amax(amax_bits8(v));
+    }
+    uint32_t m = __vmaxu2(__vmaxu2(r.lo.x & 0x7FFF7FFFu, r.lo.y & 0x7FFF7FFFu), __vmaxu2(r.lo.z & 0x7FFF7FFFu, r.lo.w & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t hi = m >> 16, lo = m & 0xFFFFu;
+    const uint32_t top = hi > lo ? hi : lo;
+    return dt == DBF_BF16 ? top << 16 : __float_as_uint(h2f(static_cast<uint16_t>(top)));
+}
+
 // A lane's eight values to codes; four neighbouring lanes hold one block.
 // Returns the code word and the block's scale byte.
-__device__ __forceinline__ uint32_t quantize8_e2m1(float (&v)[8], uint32_t &byte)
+__device__ __forceinline__ uint32_t quantize8_e2m1(const Raw8 &r, dbf_dtype dt, bool vec, uint32_t &byte)
 {
-    byte = scale_byte4(block_amax(amax_bits8(v)));
+    byte = scale_byte4(block_amax_raw(r, dt, vec));
     const float inv = inv_scale(byte);
+    float v[8];
+    raw8_values(r, dt, vec, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
     const uint32_t w = e2m1x8(v);
     return byte == 255u ? 0u : w;
+}
+__device__ __forceinline__ uint2 quantize8_e4m3(const Raw8 &r, dbf_dtype dt, bool vec, uint32_t &byte)
+{
+    byte = scale_byte8(block_amax_raw(r, dt, vec));
+    const float inv = inv_scale(byte);
+    float v[8];
+    raw8_values(r, dt, vec, v);
+    const uint2 w = make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                               e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    return byte == 255u ? make_uint2(0u, 0u) : w;
 }
 
 // The scale bytes of the four blocks that a half-warp holds, as one word
 // (the same in every lane of the half).
 __device__ __forceinline__ uint32_t half_warp_scales(uint32_t byte, int lane)
 {
-    const int base = lane & 16;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= __shfl_sync(0xFFFFFFFFu, byte, base + 4 * i) << (8 * i);
-    return w;
+    uint32_t w = byte << (lane * 2 & 24);   // 8 * (lane / 4 % 4)
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+    return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
 }
 
 }  // namespace mx

@@ -432,69 +432,85 @@ __global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy
 }
 
 // dg and du of 32 tokens x 256 columns from dh and the 8-bit g and u, and their
-// operand planes where op_g is set.
+// operand planes (kOperands: fp32, or rows that cannot be operands themselves).
 struct GateArgs {
     const uint8_t *g8, *gs, *u8, *us;
     const void *dh;
     void *dg, *du;
     uint16_t *op_g, *op_u;
     int64_t T, N, pitch8, ld;
-    int act, planes;
-    bool vec;
+    int planes;
 };
 
-template <dbf_dtype DT>
-__global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateArgs a)
+template <dbf_dtype DT, bool kVec, bool kOperands, int kAct>
+__global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const __grid_constant__ GateArgs a)
 {
     __shared__ uint8_t sc[2][8][32];
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32, row = r0 + warp;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
     const int64_t b = static_cast<int64_t>(blockIdx.y) * 8 + warp;
     const bool has = b < blocks(a.N) && r0 + lane < a.T;
     sc[0][warp][lane] = has ? a.gs[b * a.T + r0 + lane] : 0;
     sc[1][warp][lane] = has ? a.us[b * a.T + r0 + lane] : 0;
-    __syncthreads();
-    if (c >= a.pitch8) return;
+    const int left = static_cast<int>(a.T - row < 32 ? a.T - row : 32);   // row + 8 i exists where 8 i < left
+    // all reads of the lane's four tokens before the first is used
+    uint2 wg[4], wu[4];
+    Raw8 in[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t t = r0 + 8 * i + warp;
-        if (t >= a.T) break;
-        const uint2 wg = *reinterpret_cast<const uint2 *>(a.g8 + t * a.pitch8 + c);
-        const uint2 wu = *reinterpret_cast<const uint2 *>(a.u8 + t * a.pitch8 + c);
-        float dh[8], g[8], u[8];
-        load8(a.dh, DT, t * a.N, c, a.N, a.vec, dh);
-        const float sg = scale_value(sc[0][lane >> 2][8 * i + warp]), su = scale_value(sc[1][lane >> 2][8 * i + warp]);
-        float q[4];
-        from_e4m3x4(wg.x, q);
-        g[0] = q[0] * sg, g[1] = q[1] * sg, g[2] = q[2] * sg, g[3] = q[3] * sg;
-        from_e4m3x4(wg.y, q);
-        g[4] = q[0] * sg, g[5] = q[1] * sg, g[6] = q[2] * sg, g[7] = q[3] * sg;
-        from_e4m3x4(wu.x, q);
-        u[0] = q[0] * su, u[1] = q[1] * su, u[2] = q[2] * su, u[3] = q[3] * su;
-        from_e4m3x4(wu.y, q);
-        u[4] = q[0] * su, u[5] = q[1] * su, u[6] = q[2] * su, u[7] = q[3] * su;
+        const bool on = 8 * i < left && c < a.pitch8;
+        const int64_t at = (row + 8 * i) * a.pitch8 + c;
+        wg[i] = on ? *reinterpret_cast<const uint2 *>(a.g8 + at) : make_uint2(0u, 0u);
+        wu[i] = on ? *reinterpret_cast<const uint2 *>(a.u8 + at) : make_uint2(0u, 0u);
+        in[i] = load_raw8(a.dh, DT, (row + 8 * i) * a.N, on ? c : a.N, a.N, kVec);
+    }
+    __syncthreads();
+    if (c < a.pitch8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float value;
-            const float slope = gate_slope(a.act, g[j], value);
-            g[j] = dh[j] * u[j] * slope;
-            u[j] = dh[j] * value;
-            if (DT == DBF_BF16) {
-                g[j] = __bfloat162float(__float2bfloat16_rn(g[j]));
-                u[j] = __bfloat162float(__float2bfloat16_rn(u[j]));
+        for (int i = 0; i < 4; ++i) {
+            if (8 * i >= left) break;
+            const int64_t t = row + 8 * i;
+            float dh[8], g[8], u[8];
+            raw8_values(in[i], DT, kVec, dh);
+            const float sg = scale_value(sc[0][lane >> 2][8 * i + warp]), su = scale_value(sc[1][lane >> 2][8 * i + warp]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float p[4], q[4];
+                from_e4m3x4(h ? wg[i].y : wg[i].x, p);
+                from_e4m3x4(h ? wu[i].y : wu[i].x, q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float value;
+                    const float slope = gate_slope(kAct, p[j] * sg, value);
+                    g[4 * h + j] = dh[4 * h + j] * (q[j] * su) * slope;
+                    u[4 * h + j] = dh[4 * h + j] * value;
+                }
             }
-            if (c + j >= a.N) g[j] = u[j] = 0.0f;
-        }
-        store8(a.dg, DT, t * a.N, c, a.N, a.vec, g);
-        store8(a.du, DT, t * a.N, c, a.N, a.vec, u);
-        if (a.op_g && c < a.ld) {
-            store_planes(a.op_g, a.ld, a.T * a.ld, t, c, a.planes, g);
-            store_planes(a.op_u, a.ld, a.T * a.ld, t, c, a.planes, u);
+            store8(a.dg, DT, t * a.N, c, a.N, kVec, g);
+            store8(a.du, DT, t * a.N, c, a.N, kVec, u);
+            if (kOperands && c < a.ld) {
+                // columns past the last are not read: the maps end at column N
+#pragma unroll
+                for (int j = 0; j < 8 && DT == DBF_BF16; ++j) {
+                    g[j] = __bfloat162float(__float2bfloat16_rn(g[j]));
+                    u[j] = __bfloat162float(__float2bfloat16_rn(u[j]));
+                }
+                store_planes(a.op_g, a.ld, a.T * a.ld, t, c, a.planes, g);
+                store_planes(a.op_u, a.ld, a.T * a.ld, t, c, a.planes, u);
+            }
         }
     }
     griddep_launch();   // at the end: the product's CTAs would take this kernel's registers
+}
+
+template <dbf_dtype DT, bool kVec>
+auto gate_back(bool operands, int act)
+{
+    if (act == DBF_GATE_SILU)
+        return operands ? gate_back_kernel<DT, kVec, true, DBF_GATE_SILU> : gate_back_kernel<DT, kVec, false, DBF_GATE_SILU>;
+    return operands ? gate_back_kernel<DT, kVec, true, DBF_GATE_GELU> : gate_back_kernel<DT, kVec, false, DBF_GATE_GELU>;
 }
 
 // dx = [acc] dx + the parts' sums, in order.
@@ -685,9 +701,7 @@ cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, co
     a.g8 = sg.codes, a.gs = sg.scales, a.u8 = su.codes, a.us = su.scales;
     a.dh = c.dy, a.dg = dg, a.du = du;
     a.T = c.T, a.N = c.N, a.pitch8 = blocks(c.N) * kBlock, a.ld = operand_ld(c.N);
-    a.act = act;
     a.planes = c.dyd == DBF_F32 ? 3 : 1;
-    a.vec = c.N % 8 == 0;
     const void *operand[2] = {dg, du};
     if (want && !direct) {
         a.op_g = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
@@ -701,7 +715,10 @@ cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, co
     pre.stream = s;
     pre.attrs = attr.attr;
     pre.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&pre, c.dyd == DBF_F32 ? gate_back_kernel<DBF_F32> : gate_back_kernel<DBF_BF16>, a);
+    const bool vec = c.N % 8 == 0, op = a.op_g != nullptr;
+    const auto kernel = c.dyd == DBF_F32 ? (vec ? gate_back<DBF_F32, true>(op, act) : gate_back<DBF_F32, false>(op, act))
+                                         : (vec ? gate_back<DBF_BF16, true>(op, act) : gate_back<DBF_BF16, false>(op, act));
+    const cudaError_t e = cudaLaunchKernelEx(&pre, kernel, a);
     if (e != cudaSuccess || !want) return e;
     return product(c, operand, direct ? c.N : a.ld, direct ? 1 : a.planes, true,
                    kWsHeaderBytes + (direct ? 0 : 2 * plane_bytes(c.N, c.T, c.dyd)), s);

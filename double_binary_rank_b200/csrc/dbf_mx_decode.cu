@@ -160,13 +160,13 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
         griddep_wait();     // x, y and the addends belong to earlier work until then
         griddep_launch();   // what follows may be set up: all earlier work is done
         for (int u0 = worker; u0 < g.T * nks && !g.pre; u0 += 4 * kWorkers) {
-            float v[4][8];
+            Raw8 in[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int u = u0 + i * kWorkers;
                 const int t = u / nks, ks = u - t * nks;
                 const int64_t c = static_cast<int64_t>(k0 + ks) * 256 + lane * 8;
-                load8(g.x, g.xd, t * g.M, u < g.T * nks ? c : g.M, g.M, g.vec, v[i]);
+                in[i] = load_raw8(g.x, g.xd, t * g.M, u < g.T * nks ? c : g.M, g.M, g.vec);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
                 if (u >= g.T * nks) break;
                 const int t = u / nks, ks = u - t * nks;
                 uint32_t byte;
-                const uint32_t q = quantize8_e2m1(v[i], byte);
+                const uint32_t q = quantize8_e2m1(in[i], g.xd, g.vec, byte);
                 const uint32_t word = half_warp_scales(byte, lane);
                 uint8_t *xs = xq + ks * x_stage;
                 *reinterpret_cast<uint32_t *>(xs + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = q;

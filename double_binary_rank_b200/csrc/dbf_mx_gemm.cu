@@ -73,6 +73,43 @@ __device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][8
 __device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][16]) { tmem_ld16(at, col); }
 __device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][16]) { tmem_ld16(at, at + w, col); }
 
+// A tile's addends into L2 while its products are computed: w tokens x 128
+// columns (two lines of 128 bytes a row) of both, over the epilogue's warps.
+__device__ __forceinline__ void prefetch_addends(const Epilogue &e, int64_t t0, int w, int n0, int warp)
+{
+    for (int i = warp * 32 + (threadIdx.x & 31); i < 4 * w; i += kEpiWarps * 32) {
+        const int64_t t = t0 + (i >> 2);
+        const int c = n0 + (i & 1) * 64;
+        if (t < e.T && c < e.N) {
+            const uint16_t *p = static_cast<const uint16_t *>(i & 2 ? e.u_add : e.g_add) + t * e.N + c;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        }
+    }
+}
+
+// A warp's share of a gated tile: 16 tokens of both accumulators at a time,
+// every second 16 from j0; addends asked for a chunk ahead, the first before
+// the products are there. False when the wait for them gave up.
+template <bool kAdd, bool kSave, class Ready>
+__device__ __forceinline__ bool gated_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, Ready ready)
+{
+    uint4 x[2][2][2];
+    gated_reads<kAdd>(g.ep, t + j0, n, j0 < g.w, x[0]);
+    if (!ready()) return false;
+    for (; j0 < g.w; j0 += 64) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = j0 + 32 * i, next = j + 32;
+            if (j >= g.w) break;
+            gated_reads<kAdd>(g.ep, t + next, n, next < g.w, x[i ^ 1]);
+            float v[2][16];
+            load_chunk(lanes + j, g.w, v);
+            gated_finish<kAdd, kSave>(g.ep, own, t + j, n, v, x[i]);
+        }
+    }
+    return true;
+}
+
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1, const __grid_constant__ CUtensorMap mS0,
@@ -218,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
         // gated: the two warps of a lane quarter take turns by 8 tokens of both
         // accumulators; plain: each takes one accumulator
         const int j_first = kGated ? half * 8 : 0, j_step = kGated ? 16 : 8;
-        const bool simple = epilogue_is_simple(g.ep);
+        const bool simple = epilogue_is_simple(g.ep), bf16 = epilogue_is_bf16(g.ep);
         uint32_t acc_ph = 0;
         for (int tile = unit; tile < g.tiles; tile += units) {
             const int p = tile % g.n_p, c = tile / g.n_p;
@@ -238,6 +275,26 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(&sh->acc_empty);
                 continue;
+            }
+            if constexpr (kGated) {
+                if (bf16) {
+                    const bool add = g.ep.g_add != nullptr, save = g.ep.g8 != nullptr;
+                    if (add) prefetch_addends(g.ep, t - (lane >> 2), g.w, n - (lane & 3) * 8 - quarter * 32, warp - 2 - kScaleWarps);
+                    auto ready = [&] {
+                        const bool ok = bar_wait(&sh->acc_full, acc_ph, abort);
+                        acc_ph ^= 1u;
+                        tc_fence_after();
+                        return ok;
+                    };
+                    const bool ok = add ? (save ? gated_tile<true, true>(g, own, lanes, t, n, half * 16, ready)
+                                                : gated_tile<true, false>(g, own, lanes, t, n, half * 16, ready))
+                                        : gated_tile<false, true>(g, own, lanes, t, n, half * 16, ready);
+                    if (!ok) break;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+                    continue;
+                }
             }
             // what a chunk reads is asked for a chunk ahead, the first before the products are there
             Raw8 x[2][kMats];
@@ -281,29 +338,28 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
 // Pre-pass: x to codes and scales in the workspace. The scales of the tokens
 // of one tile start a new 128-row scale tile, since a tile of w tokens is no
 // multiple of 128: token t has scale row (t / w) * pad + t % w.
-template <dbf_dtype DT>
-__global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict__ x, int64_t T, int64_t M, bool vec, int w, int pad,
-                                  uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
+template <dbf_dtype DT, bool kVec>
+__global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict__ x, int64_t T, int64_t M, int w, int pad,
+                                                         uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
 {
     griddep_wait();   // the workspace may still be read by the call before
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
     const int64_t nb = blocks(M), pitch = nb * 16, tiles = scale_tiles(M);
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-    float v[4][8];
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    const int left = static_cast<int>(T - row < 32 ? T - row : 32);   // row + 8 i exists where 8 i < left
+    Raw8 in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + 8 * i;
-        load8(x, DT, r * M, r < T ? c : M, M, vec, v[i]);
-    }
+    for (int i = 0; i < 4; ++i) in[i] = load_raw8(x, DT, (row + 8 * i) * M, 8 * i < left ? c : M, M, kVec);
+    uint8_t *out = codes + row * pitch + c / 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + 8 * i;
+    for (int i = 0; i < 4; ++i, out += 8 * pitch) {
+        const int r = static_cast<int>(row) + 8 * i;
         uint32_t byte;
-        const uint32_t q = quantize8_e2m1(v[i], byte);
+        const uint32_t q = quantize8_e2m1(in[i], DT, kVec, byte);
         const uint32_t word = half_warp_scales(byte, lane);
-        if (r >= T) continue;
-        if (c < nb * kBlock) *reinterpret_cast<uint32_t *>(codes + r * pitch + c / 2) = q;
+        if (8 * i >= left) continue;
+        if (c < nb * kBlock) *reinterpret_cast<uint32_t *>(out) = q;
         if ((lane & 15) == 0 && (c >> 7) < tiles)
             *reinterpret_cast<uint32_t *>(scales + scale_at(r / w * pad + r % w, c >> 5, tiles)) = word;
     }
@@ -420,8 +476,9 @@ cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
-    return cudaLaunchKernelEx(&cfg, c.xd == DBF_F32 ? quantize_x_kernel<DBF_F32> : quantize_x_kernel<DBF_BF16>, c.x, c.T, c.M, vec,
-                              w, pad, codes, scales);
+    const auto kernel = c.xd == DBF_F32 ? (vec ? quantize_x_kernel<DBF_F32, true> : quantize_x_kernel<DBF_F32, false>)
+                                        : (vec ? quantize_x_kernel<DBF_BF16, true> : quantize_x_kernel<DBF_BF16, false>);
+    return cudaLaunchKernelEx(&cfg, kernel, c.x, c.T, c.M, w, pad, codes, scales);
 }
 
 cudaError_t mx_gemm(const Product &c, cudaStream_t s)

@@ -181,6 +181,58 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
                                                          __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
 }
 
+// The same rows for the gated block with bf16 addends and 8-bit copies of g and
+// u, 16 tokens at once as two turns of 8.
+__device__ __forceinline__ bool epilogue_is_bf16(const Epilogue &e)
+{
+    return epilogue_vec(e) && e.yd == DBF_BF16 && !e.g_add == !e.u_add && (!e.g_add || e.add_dt == DBF_BF16);
+}
+template <bool kAdd>
+__device__ __forceinline__ void gated_reads(const Epilogue &e, int64_t t, int c, bool on, uint4 (&x)[2][2])
+{
+    if (!kAdd) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool in = on && c < e.N && t + 8 * i < e.T;
+        const int64_t at = (t + 8 * i) * e.N + c;
+        x[i][0] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.g_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+        x[i][1] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.u_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+template <bool kAdd, bool kSave>
+__device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int64_t t, int c, const float (&v)[2][16],
+                                             const uint4 (&x)[2][2])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float col[2][8], row[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) col[0][j] = v[0][8 * i + j], col[1][j] = v[1][8 * i + j];
+        turn8<2>(own, col, row);
+        const bool on = t + 8 * i < e.T;
+        if (kAdd) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const Raw8 r = {x[i][m], make_uint4(0u, 0u, 0u, 0u)};
+                add_raw8(r, DBF_BF16, true, row[m]);
+            }
+        }
+        if (kSave) {
+            if (c >= e.N) {   // rows past the last may have given anything, a NaN too
+#pragma unroll
+                for (int j = 0; j < 8; ++j) row[0][j] = row[1][j] = 0.0f;
+            }
+            keep8(e.g8, e.gs, e.pitch8, e.T, t + 8 * i, c, on, row[0]);
+            keep8(e.u8, e.us, e.pitch8, e.T, t + 8 * i, c, on, row[1]);
+        }
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) row[0][j] = gate_value(e.act, row[0][j]) * row[1][j];
+            store8(e.y, DBF_BF16, (t + 8 * i) * e.N, c, e.N, true, row[0]);
+        }
+    }
+}
+
 // One call: a weight (plain) or two of one shape (gated), and its tokens.
 struct Product {
     int64_t M, N, T;
