@@ -584,6 +584,13 @@ _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
 
 
+try:   # the handle alone, without building a Stream object (1.2 us of a call's 11)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _enter(t: torch.Tensor, stream) -> Tuple[int, Optional[int]]:
     """(stream handle, device to go back to after the call or None); makes the
     tensor's device current."""
@@ -593,8 +600,7 @@ def _enter(t: torch.Tensor, stream) -> Tuple[int, Optional[int]]:
     cur = torch.cuda.current_device()
     if cur != dev:
         torch.cuda.set_device(dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    return s.cuda_stream, None if cur == dev else cur
+    return _raw_stream(dev) if stream is None else stream.cuda_stream, None if cur == dev else cur
 
 
 def _leave(back: Optional[int]) -> None:

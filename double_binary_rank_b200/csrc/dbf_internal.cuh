@@ -160,11 +160,10 @@ cudaError_t launch_act8_save(const void *src, dbf_dtype dt, int64_t rows, int64_
 cudaError_t launch_act8_load(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
                              dbf_dtype dt, cudaStream_t s);
 // products: mats 1 (y = W q(x)) or 2 (the gated block)
-size_t mx_decode_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats);   // 0: mx_gemm takes the call
+bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats);   // else mx_gemm takes the call
 // x to codes and scales (dbf_mx_gemm.cu); token t has scale row t / w * pad + t % w
 cudaError_t mx_quantize_x(const mx::Product &c, int w, int pad, uint8_t *codes, uint8_t *scales, cudaStream_t s);
 cudaError_t mx_decode(const mx::Product &c, cudaStream_t s);
-size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats);
 cudaError_t mx_gemm(const mx::Product &c, cudaStream_t s);
 size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int mats);
 cudaError_t mx_backward(const mx::Gradient &c, cudaStream_t s);

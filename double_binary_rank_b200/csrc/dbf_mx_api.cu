@@ -44,19 +44,16 @@ dbf_status check_layer(const dbf_mx4_layer *L)
     return aligned(L->codes, 16) && aligned(L->scales, 16) ? DBF_OK : DBF_ERR_ALIGNMENT;
 }
 
-size_t product_workspace(const dbf_mx4_layer *L, int64_t T, int mats)
+size_t product_workspace(const dbf_mx4_layer *L, int64_t T)
 {
-    if (!layer_shape_ok(L) || !tokens_ok(L, T)) return 0;
-    if (T == 0) return kWsHeaderBytes;
-    const size_t few = mx_decode_workspace_bytes(L->M, L->N, T, mats);
-    return few ? few : mx_gemm_workspace_bytes(L->M, L->N, T, mats);
+    return layer_shape_ok(L) && tokens_ok(L, T) ? mx::product_workspace_bytes(L->M, T) : 0;
 }
 
 dbf_status run(const mx::Product &c, size_t need, size_t ws_bytes, cudaStream_t s)
 {
     if (!c.ws || ws_bytes < need) return DBF_ERR_WORKSPACE;
     if (!aligned(c.ws, 256)) return DBF_ERR_ALIGNMENT;
-    return from_cuda(mx_decode_workspace_bytes(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
+    return from_cuda(mx_decode_fits(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
 }
 
 bool same_shape(const dbf_mx4_layer *a, const dbf_mx4_layer *b)
@@ -125,7 +122,7 @@ dbf_status dbf_act8_load(const dbf_act8 *src, int64_t rows, int64_t cols, void *
     return from_cuda(launch_act8_load(src->codes, src->scales, rows, cols, dst, dst_dtype, static_cast<cudaStream_t>(stream)));
 }
 
-size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T) { return product_workspace(L, T, 1); }
+size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T) { return product_workspace(L, T); }
 
 dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dtype, void *y, dbf_dtype y_dtype, int64_t T,
                            int flags, void *ws, size_t ws_bytes, void *stream)
@@ -146,12 +143,12 @@ dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dt
     c.ep.y = y, c.ep.yd = y_dtype, c.ep.accumulate = flags & DBF_ACCUMULATE ? 1 : 0;
     c.ep.N = L->N, c.ep.T = T;
     c.flags = flags, c.ws = ws;
-    return run(c, product_workspace(L, T, 1), ws_bytes, static_cast<cudaStream_t>(stream));
+    return run(c, product_workspace(L, T), ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 size_t dbf_mx4_gated_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T)
 {
-    return same_shape(gate, up) ? product_workspace(gate, T, 2) : 0;
+    return same_shape(gate, up) ? product_workspace(gate, T) : 0;
 }
 
 dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const void *x,
@@ -188,7 +185,7 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
     c.ep.pitch8 = mx::blocks(gate->N) * mx::kBlock;
     c.ep.N = gate->N, c.ep.T = T;
     c.flags = flags, c.ws = ws;
-    return run(c, product_workspace(gate, T, 2), ws_bytes, static_cast<cudaStream_t>(stream));
+    return run(c, product_workspace(gate, T), ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 size_t dbf_mx4_backward_workspace_bytes(const dbf_mx4_layer *L, int64_t T, dbf_dtype dy_dtype)

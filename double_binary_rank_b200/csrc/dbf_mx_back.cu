@@ -557,6 +557,7 @@ int resident_pairs(cudaLaunchConfig_t cfg)
 // stages, a stage taking its eight MMAs (2 w) or the expansion of W (the same
 // at every width), and an epilogue; the parts' sums are written and read once
 // more.
+constexpr int64_t kMaxSplits = 16;
 struct Plan {
     int w, splits;
 };
@@ -567,7 +568,7 @@ Plan plan(int64_t M, int64_t T, int64_t nk)
     double least = -1;
     for (int w = 32; w <= 512; w += 32) {
         const int64_t tiles = n_p * ((T + w - 1) / w);
-        for (int splits = 1; splits <= 16 && splits <= nk; ++splits) {
+        for (int splits = 1; splits <= kMaxSplits && splits <= nk; ++splits) {
             if (splits > 1 && tiles * splits > pairs) break;
             const double waves = static_cast<double>((tiles * splits + pairs - 1) / pairs);
             const double stages = static_cast<double>((nk + splits - 1) / splits);
@@ -669,8 +670,10 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
 
 size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int mats)
 {
-    const Plan pl = plan(M, T, stages(N, mats, d == DBF_F32 ? 3 : 1));
-    const size_t partial = pl.splits > 1 ? align_up(static_cast<size_t>(pl.splits) * static_cast<size_t>(T * M) * 4, 256) : 0;
+    // parts of the contraction times tokens: at most 16 T, and no more tiles (of
+    // 512 tokens at most) than pairs. It grows with T.
+    const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    const size_t partial = static_cast<size_t>(std::min(kMaxSplits * T, pairs * 512 / n_p)) * static_cast<size_t>(M) * 4;
     return kWsHeaderBytes + (direct_operand(N, d) ? 0 : mats * plane_bytes(N, T, d)) + partial;
 }
 

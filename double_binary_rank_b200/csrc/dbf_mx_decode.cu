@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
 
 struct Shape {
     int w, split, ring, nks, pre;
-    size_t smem, codes, scales, workspace;   // offsets of x's codes and scales in the workspace
+    size_t smem;
 };
 
 // Split of the columns, ring depth and CTAs to an SM; false when the CTA's
@@ -268,9 +268,6 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
             // another of its cluster waits at the exchange
             p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + ring * stage, 77 * 1024));
             p.pre = T * p.nks > kInline ? 1 : 0;
-            p.codes = kWsHeaderBytes;
-            p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
-            p.workspace = p.pre ? align_up(p.scales + static_cast<size_t>(scale_tiles(M) * 512), 256) : kWsHeaderBytes;
             return true;
         }
     }
@@ -279,10 +276,10 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
 
 }  // namespace
 
-size_t mx_decode_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats)
+bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats)
 {
     Shape p;
-    return shape(M, N, T, mats, p) ? p.workspace : 0;
+    return shape(M, N, T, mats, p);
 }
 
 cudaError_t mx_decode(const Product &c, cudaStream_t s)
@@ -305,7 +302,7 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
             return cudaErrorInvalidValue;
     }
     CUtensorMap xm = a[0], xs = sa[0];
-    uint8_t *codes = static_cast<uint8_t *>(c.ws) + p.codes, *scales = static_cast<uint8_t *>(c.ws) + p.scales;
+    uint8_t *codes = static_cast<uint8_t *>(c.ws) + x_codes_at(), *scales = static_cast<uint8_t *>(c.ws) + x_scales_at(c.M, c.T);
     if (p.pre) {
         const uint64_t dims[2] = {static_cast<uint64_t>(code_pitch(c.M)), static_cast<uint64_t>(c.T)};
         const uint32_t box[2] = {128, static_cast<uint32_t>(p.w)};

@@ -24,7 +24,8 @@
 //   warps 6..13 epilogue.
 // The token width w is chosen per call (a multiple of 16 up to 224, what 512
 // tensor-memory columns hold beside two buffers of 32 of scales) so that the
-// tiles fill whole waves of pairs. Every wait is bounded; on expiry the status
+// tiles fill whole waves of pairs; narrower tiles, whose stages take less time
+// than scales need to get there, have up to four buffers. Every wait is bounded; on expiry the status
 // word is set.
 #include <algorithm>
 #include <map>
@@ -47,12 +48,13 @@ constexpr uint32_t kABytes = 128 * 128;            // 128 rows x 256 codes
 constexpr uint32_t kBBytes = kMaxW / 2 * 128;      // this CTA's half of the tokens
 constexpr uint32_t kSfABytes = 1024, kSfBBytes = 2048;
 constexpr uint32_t kStageBytes = 2 * kABytes + kBBytes + 2 * kSfABytes + kSfBBytes;
-constexpr uint32_t kSfCol = 448;   // tensor-memory columns: 2 w of accumulators, then scales
-constexpr uint32_t kSfCols = 32;   // of one stage: 8 per accumulator (4 per K half), then 16 of the tokens (8 per K half)
+// tensor-memory columns: 2 w per set of accumulators, then buffers of scales: 8
+// per weight block (4 per K half), then 4 per K half and 128 tokens
+__host__ __device__ constexpr uint32_t sf_cols(int w) { return w > 128 ? 32u : 24u; }
 constexpr uint32_t kTmemCols = 512;
 
 struct Smem {
-    uint64_t full[kStages], sf_full[kStages], empty[kStages], sf_ready[2], acc_full, acc_empty, drain, exit_bar;
+    uint64_t full[kStages], sf_full[kStages], empty[kStages], sf_ready[kStages], acc_full[2], acc_empty[2], drain, exit_bar;
     uint32_t tmem_base;
     int abort;
 };
@@ -60,6 +62,8 @@ struct Smem {
 struct Args {
     int nk;         // stages of 256 columns
     int w;          // tokens per tile
+    int sf_bufs;    // scale buffers, 2 to kStages
+    int bufs;       // 2: two sets of accumulators, so that an epilogue overlaps the next tile's products
     int n_p;        // row tiles
     int tiles;
     int row_step;   // weight rows of a tile: 512 plain, 256 gated
@@ -72,6 +76,15 @@ __device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][8])
 __device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][8]) { tmem_ld8(at, at + w, col); }
 __device__ __forceinline__ void load_chunk(uint32_t at, int, float (&col)[1][16]) { tmem_ld16(at, col); }
 __device__ __forceinline__ void load_chunk(uint32_t at, int w, float (&col)[2][16]) { tmem_ld16(at, at + w, col); }
+
+// Which set of accumulators a tile uses, and the phase of its barriers.
+struct Turn {
+    uint32_t buf = 0, phase = 0;
+    __device__ __forceinline__ void next(int bufs)
+    {
+        if (++buf == static_cast<uint32_t>(bufs)) buf = 0, phase ^= 1u;
+    }
+};
 
 // A tile's addends into L2 while its products are computed: w tokens x 128
 // columns (two lines of 128 bytes a row) of both, over the epilogue's warps.
@@ -130,11 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
         for (int i = 0; i < kStages; ++i) {
             bar_init(&sh->full[i], 1);
             bar_init(&sh->sf_full[i], 1);
+            bar_init(&sh->sf_ready[i], 2 * kScaleWarps);
             bar_init(&sh->empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) bar_init(&sh->sf_ready[i], 2 * kScaleWarps);
-        bar_init(&sh->acc_full, 1);
-        bar_init(&sh->acc_empty, 2 * kEpiWarps);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh->acc_full[i], 1);
+            bar_init(&sh->acc_empty[i], 2 * kEpiWarps);
+        }
         bar_init(&sh->drain, 1);
         bar_init(&sh->exit_bar, 1);
         sh->abort = 0;
@@ -196,31 +211,33 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             int s = 0;
-            uint32_t ph = 0, acc_ph = 0, k = 0;   // k: stages so far; its lowest bit is the scale buffer
+            uint32_t ph = 0;
+            Turn acc, sf_turn;
+            const uint32_t sf0 = tmem + 2 * g.w * g.bufs, b_half = g.w > 128 ? 8 : 4;
             bool ok = true;
             const uint32_t id0 = mxf4_idesc(256, g.w, 0), id2 = mxf4_idesc(256, g.w, 2);
-            for (int tile = unit; tile < g.tiles && ok; tile += units) {
-                ok = bar_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
+            for (int tile = unit; tile < g.tiles && ok; tile += units, acc.next(g.bufs)) {
+                ok = bar_wait(&sh->acc_empty[acc.buf], acc.phase ^ 1u, abort);
                 if (!ok) break;
-                for (int ks = 0; ks < g.nk; ++ks, ++k) {
-                    ok = bar_wait(&sh->full[s], ph, abort) && bar_wait(&sh->sf_ready[k & 1u], (k >> 1) & 1u, abort);
+                const uint32_t d = tmem + acc.buf * 2 * g.w;
+                for (int ks = 0; ks < g.nk; ++ks, sf_turn.next(g.sf_bufs)) {
+                    ok = bar_wait(&sh->full[s], ph, abort) && bar_wait(&sh->sf_ready[sf_turn.buf], sf_turn.phase, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(stage0) + s * kStageBytes, sf = tmem + kSfCol + (k & 1u) * kSfCols;
+                    const uint32_t st = smem_u32(stage0) + s * kStageBytes, sf = sf0 + sf_turn.buf * sf_cols(g.w);
                     const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + 2 * kABytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t id = kk & 1 ? id2 : id0, acc = ks > 0 || kk > 0 ? 1u : 0u;
-                        const uint32_t sb = sf + 16 + 8 * (kk >> 1);
-                        mma_mxf4<2>(tmem, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, acc);
-                        mma_mxf4<2>(tmem + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
+                        const uint32_t sb = sf + 16 + b_half * (kk >> 1);
+                        mma_mxf4<2>(d, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, acc);
+                        mma_mxf4<2>(d + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
                     }
                     commit_pair_both(&sh->empty[s]);
                     if (++s == kStages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
-                commit_pair_both(&sh->acc_full);
-                acc_ph ^= 1u;
+                commit_pair_both(&sh->acc_full[acc.buf]);
             }
             if (*abort) {
                 commit_pair_own(&sh->drain);
@@ -232,39 +249,48 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
         const int64_t total = static_cast<int64_t>((g.tiles - 1 - unit) / units + 1) * g.nk;   // stages of this pair
         int s = 0;
         uint32_t ph = 0;
-        for (int64_t k = 0; k < total; ++k) {
-            // buffer k % 2 is free once the MMAs of stage k - 2 are done
-            const int s2 = (s + kStages - 2) % kStages;
-            if (k >= 2 && !bar_wait(&sh->empty[s2], static_cast<uint32_t>((k - 2) / kStages) & 1u, abort)) break;
+        Turn buf;
+        for (int64_t k = 0; k < total; ++k, buf.next(g.sf_bufs)) {
+            // the buffer is free once the MMAs of stage k - sf_bufs are done (with as many
+            // buffers as stages that stage's place in shared memory is this one's, and its
+            // load has waited for them)
+            const int64_t before = k - g.sf_bufs;
+            if (before >= 0 && !bar_wait(&sh->empty[before % kStages], static_cast<uint32_t>(before / kStages) & 1u, abort)) break;
             if (!bar_wait(&sh->sf_full[s], ph, abort)) break;
             tc_fence_after();
             const uint4 *sf = reinterpret_cast<const uint4 *>(stage0 + s * kStageBytes + 2 * kABytes + kBBytes) + lane;
             // 512 bytes hold 128 rows x 4 blocks, a lane's 16 the rows lane, lane + 32, ...
-            const uint4 v[8] = {sf[0], sf[32], sf[64], sf[96], sf[128], sf[192], sf[160], sf[224]};
-            tmem_st32(lanes + kSfCol + static_cast<uint32_t>(k & 1) * kSfCols, v);
+            const uint32_t to = lanes + 2 * g.w * g.bufs + buf.buf * sf_cols(g.w);
+            tmem_st16(to, sf[0], sf[32], sf[64], sf[96]);
+            if (g.w > 128)
+                tmem_st16(to + 16, sf[128], sf[192], sf[160], sf[224]);
+            else
+                tmem_st8(to + 16, sf[128], sf[160]);
+            tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_leader(&sh->sf_ready[k & 1]);
+            if (lane == 0) bar_arrive_leader(&sh->sf_ready[buf.buf]);
             if (++s == kStages) s = 0, ph ^= 1u;
         }
     } else {
         griddep_wait();   // y (and the addends) belong to earlier work until then
         const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kGated ? 0 : half * g.w);
+        const uint32_t lanes0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kGated ? 0 : half * g.w);
         float *own = turn + (warp - 2 - kScaleWarps) * kMats * kTurnFloats;
         // gated: the two warps of a lane quarter take turns by 8 tokens of both
         // accumulators; plain: each takes one accumulator
         const int j_first = kGated ? half * 8 : 0, j_step = kGated ? 16 : 8;
         const bool simple = epilogue_is_simple(g.ep), bf16 = epilogue_is_bf16(g.ep);
-        uint32_t acc_ph = 0;
-        for (int tile = unit; tile < g.tiles; tile += units) {
+        Turn acc;
+        for (int tile = unit; tile < g.tiles; tile += units, acc.next(g.bufs)) {
+            const uint32_t lanes = lanes0 + acc.buf * 2 * g.w;
+            uint64_t *full = &sh->acc_full[acc.buf], *empty = &sh->acc_empty[acc.buf];
             const int p = tile % g.n_p, c = tile / g.n_p;
             const int n = p * g.row_step + (kGated ? 0 : half * g.row_off) + static_cast<int>(rank) * 128 + quarter * 32 +
                           (lane & 3) * 8;
             const int64_t t = static_cast<int64_t>(c) * g.w + (lane >> 2);
             if (simple) {
-                if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
-                acc_ph ^= 1u;
+                if (!bar_wait(full, acc.phase, abort)) break;
                 tc_fence_after();
                 for (int j = kGated ? half * 16 : 0; j < g.w; j += kGated ? 32 : 16) {
                     float v[kMats][16];
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+                if (lane == 0) bar_arrive_leader(empty);
                 continue;
             }
             if constexpr (kGated) {
@@ -281,8 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                     const bool add = g.ep.g_add != nullptr, save = g.ep.g8 != nullptr;
                     if (add) prefetch_addends(g.ep, t - (lane >> 2), g.w, n - (lane & 3) * 8 - quarter * 32, warp - 2 - kScaleWarps);
                     auto ready = [&] {
-                        const bool ok = bar_wait(&sh->acc_full, acc_ph, abort);
-                        acc_ph ^= 1u;
+                        const bool ok = bar_wait(full, acc.phase, abort);
                         tc_fence_after();
                         return ok;
                     };
@@ -292,15 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                     if (!ok) break;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+                    if (lane == 0) bar_arrive_leader(empty);
                     continue;
                 }
             }
             // what a chunk reads is asked for a chunk ahead, the first before the products are there
             Raw8 x[2][kMats];
             epilogue_reads<kGated>(g.ep, t + j_first, n, t + j_first < g.ep.T, x[0]);
-            if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
-            acc_ph ^= 1u;
+            if (!bar_wait(full, acc.phase, abort)) break;
             tc_fence_after();
             for (int j0 = j_first; j0 < g.w; j0 += 2 * j_step) {
 #pragma unroll
@@ -316,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_leader(&sh->acc_empty);
+            if (lane == 0) bar_arrive_leader(empty);
         }
     }
 
@@ -388,38 +412,46 @@ int resident_pairs(const void *kernel, cudaLaunchConfig_t cfg)
     return it->second;
 }
 
-// Tokens per tile. Cost in cycles of the last pair to finish: waves of tiles,
-// each nk stages and an epilogue. A stage takes its eight MMAs (4 w cycles) or
-// its operands' way into the SM, whichever is longer.
-int tile_width(int64_t N, int64_t M, int64_t T, int mats)
+// What an epilogue costs per token of a tile, in cycles: plain bf16 rows, the
+// gate, addends, 8-bit copies (from 6 waves of 4096 -> 11008 at 2048 tokens).
+enum Kind { kPlain, kGate, kGateAdd, kGateSave, kKinds };
+constexpr double kEpilogueCycles[kKinds] = {25, 29, 73, 98};
+
+Kind kind_of(const Product &c)
 {
-    const int64_t n_p = (N + (mats == 2 ? 255 : 511)) / (mats == 2 ? 256 : 512);
-    const int64_t nk = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
-    int best = 16;
-    double least = 0;
-    for (int w = 16; w <= kMaxW; w += 16) {
-        const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
-        const double bytes = 2 * (kABytes + 1024.0) + w / 2 * 128 + (w > 128 ? 2048 : 1024);
-        const double cost = static_cast<double>(waves) * (nk * std::max(4.0 * w, bytes / 45) + 800 + 12.0 * w);
-        if (w == 16 || cost < least) least = cost, best = w;
-        if (w >= T) break;
-    }
-    return best;
+    if (c.mats == 1) return kPlain;
+    return c.ep.g8 ? kGateSave : c.ep.g_add || c.ep.u_add ? kGateAdd : kGate;
 }
 
 struct Plan {
-    int w, pad;
-    size_t codes, scales, total;   // offsets in the workspace, and its size
+    int w, bufs, pad;   // pad: scale rows of a tile
 };
 
-Plan plan(int64_t M, int64_t N, int64_t T, int mats)
+// Tokens per tile, and one or two sets of accumulators (up to 224 tokens, or
+// 112). Cost of the last pair to finish, in cycles: waves of tiles, each nk
+// stages and an epilogue, which two sets hide behind the next tile's stages. A
+// stage takes its eight MMAs (4 w cycles) or its operands' way from L2 (about
+// 45 bytes a cycle and SM, 40 beside a running epilogue), whichever is longer:
+// narrow tiles pay for their weights' way there, so two sets win only where the
+// epilogue is long against K. 2048 x 8192 at 4096 tokens with addends: 120 us on
+// one set, 101 us on two; 4096 x 11008 at 2048 tokens: 114 us and 126 us.
+Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
 {
-    Plan p;
-    p.w = tile_width(N, M, T, mats);
+    const int64_t n_p = (N + (mats == 2 ? 255 : 511)) / (mats == 2 ? 256 : 512);
+    const int64_t nk = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    Plan p = {};
+    double least = -1;
+    for (int bufs = 1; bufs <= 2; ++bufs)
+        for (int w = 16; w <= kMaxW / bufs; w += 16) {
+            const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
+            const double bytes = 2 * (kABytes + 1024.0) + w / 2 * 128 + (w > 128 ? 2048 : 1024);
+            const double products = nk * std::max(4.0 * w, bytes / (bufs == 1 ? 45 : 40)), epilogue = 800 + kEpilogueCycles[kind] * w;
+            const double cost = bufs == 1 ? waves * (products + epilogue)
+                                          : (waves - 1) * std::max(products, epilogue) + products + epilogue;
+            if (least < 0 || cost < least) least = cost, p.w = w, p.bufs = bufs;
+            if (w >= T) break;
+        }
     p.pad = p.w > 128 ? 256 : 128;
-    p.codes = kWsHeaderBytes;
-    p.scales = align_up(p.codes + static_cast<size_t>(T * code_pitch(M)), 256);
-    p.total = align_up(p.scales + static_cast<size_t>((T + p.w - 1) / p.w * (p.pad / 128) * scale_tiles(M) * 512), 256);
     return p;
 }
 
@@ -462,8 +494,6 @@ bool tc_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ba
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t T, int mats) { return plan(M, N, T, mats).total; }
-
 cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint8_t *scales, cudaStream_t s)
 {
     cudaLaunchAttribute attr;
@@ -483,8 +513,8 @@ cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint
 
 cudaError_t mx_gemm(const Product &c, cudaStream_t s)
 {
-    const Plan pl = plan(c.M, c.N, c.T, c.mats);
-    uint8_t *codes = static_cast<uint8_t *>(c.ws) + pl.codes, *scales = static_cast<uint8_t *>(c.ws) + pl.scales;
+    const Plan pl = plan(c.M, c.N, c.T, c.mats, kind_of(c));
+    uint8_t *codes = static_cast<uint8_t *>(c.ws) + x_codes_at(), *scales = static_cast<uint8_t *>(c.ws) + x_scales_at(c.M, c.T);
 
     CUtensorMap a[2], sa[2], b, sb;
     const bool gated = c.mats == 2;
@@ -513,6 +543,8 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
     Args g = {};
     g.nk = static_cast<int>((c.M + 255) / 256);
     g.w = pl.w;
+    g.bufs = pl.bufs;
+    g.sf_bufs = std::min<int>(kStages, (kTmemCols - 2 * pl.w * pl.bufs) / sf_cols(pl.w));
     g.row_step = gated ? 256 : 512;
     g.row_off = gated ? 0 : 256;
     g.n_p = static_cast<int>((c.N + g.row_step - 1) / g.row_step);

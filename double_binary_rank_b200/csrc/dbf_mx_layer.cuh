@@ -233,6 +233,16 @@ __device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int6
     }
 }
 
+// The workspace of a product: x's codes, and its scales in whole tiles of 128
+// rows, one at most per 16 tokens however the tokens are cut into tiles. It
+// grows with T, so one made for the largest T serves every call.
+inline size_t x_codes_at() { return kWsHeaderBytes; }
+inline size_t x_scales_at(int64_t M, int64_t T) { return align_up(x_codes_at() + static_cast<size_t>(T * code_pitch(M)), 256); }
+inline size_t product_workspace_bytes(int64_t M, int64_t T)
+{
+    return x_scales_at(M, T) + static_cast<size_t>((T + 15) / 16 * scale_tiles(M) * 512);
+}
+
 // One call: a weight (plain) or two of one shape (gated), and its tokens.
 struct Product {
     int64_t M, N, T;

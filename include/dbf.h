@@ -26,7 +26,8 @@
  *   below, in memory the caller owns; host-side, the library caches per
  *   device the SM count and the kernel attributes it has set.
  * - Workspace header: every workspace (dbf_forward, dbf_backward,
- *   dbf_forward_segmented, dbf_forward_segmented_planned, dbf_mbok_forward)
+ *   dbf_forward_segmented, dbf_forward_segmented_planned, dbf_mbok_forward and
+ *   the dbf_mx4_ products)
  *   starts with DBF_WS_HEADER_BYTES bytes that must be zero before its first
  *   use (cudaMemsetAsync once after allocating it); the rest is scratch.
  *     bytes 0..7   the grid-barrier word of the single-launch decode kernel
@@ -499,8 +500,9 @@ typedef struct {
     const uint8_t *scales;
 } dbf_mx4_layer;
 
-/* Workspace bytes of dbf_mx4_forward (0 for invalid input): the header, and
- * for many tokens the quantised x. */
+/* Workspace bytes of dbf_mx4_forward (0 for invalid input): the header and
+ * the quantised x. As those of the other 4-bit calls, they grow with T: one
+ * workspace made for the largest T serves every call. */
 size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T);
 
 /* y = [acc] y + W q(x) for T tokens, q(x) being x quantised row by row as

@@ -244,3 +244,289 @@ def test_gated_backward(dbf, T, M, N, act, kind):
     assert np.all(np.abs(host(dx) - ref) <= 2 * pieces * N * 2.0 ** -23 * S + 1e-37)
     none, g2, u2 = dbf.mx4_gated_backward(gl, ul, t, saved, act=act, want_dx=False)
     assert none is None and np.array_equal(host(g2), gg) and np.array_equal(host(u2), gu)
+
+
+# ---- values that are not finite, and the limits of the format
+@pytest.mark.parametrize("T,M,N", [(3, 100, 40), (70, 300, 260), (90, 520, 130)])
+def test_not_finite_values_stay_where_they_are(dbf, T, M, N):
+    """A NaN or infinity in x spoils its token alone, one in W its output column alone (and, in the gradient, the 32
+    columns of its block)."""
+    rng = np.random.default_rng(5)
+    w, x = exact_operand(rng, N, M), exact_operand(rng, T, M)
+    ref = x @ w.T
+    w[N // 2, 33], x[T - 1, 5], x[1, M - 1] = np.nan, np.inf, np.nan
+    L = layer_of(dbf, w)
+    y = host(dbf.mx4_forward(L, torch.tensor(x).to(torch.bfloat16).cuda(), y_dtype=torch.float32))
+    bad = np.zeros((T, N), bool)
+    bad[:, N // 2] = bad[T - 1] = bad[1] = True
+    assert np.isnan(y[bad]).all() and np.array_equal(y[~bad], ref[~bad])
+    gl = layer_of(dbf, np.nan_to_num(w, nan=4.0))
+    saved = dbf.Act8.empty(T, N, "cuda"), dbf.Act8.empty(T, N, "cuda")
+    h = host(dbf.mx4_gated_forward(L, gl, torch.tensor(x).to(torch.bfloat16).cuda(), save=saved, h_dtype=torch.float32))
+    assert np.array_equal(np.isnan(h), bad)
+    # in 8 bits the whole block of 32 is spoiled
+    blocks = np.zeros((T, -(-N // 32) * 32), bool)
+    blocks[:, :N] = bad
+    spread = np.repeat(blocks.reshape(T, -1, 32).any(2), 32, axis=1)[:, :N]
+    assert np.array_equal(np.isnan(host(dbf.act8_load(saved[0], dtype=torch.float32))), spread)
+    dy = torch.ones(T, N, device="cuda", dtype=torch.bfloat16)
+    dx = host(dbf.mx4_backward(L, dy, dx_dtype=torch.float32))
+    col = np.zeros(M, bool)
+    col[32:64] = True
+    assert np.isnan(dx[:, col]).all() and np.isfinite(dx[:, ~col]).all()
+    dyn = dy.clone()
+    dyn[0, N - 1] = float("inf")
+    for t in (dyn, dyn.float()):
+        dx = host(dbf.mx4_backward(gl, t, dx_dtype=torch.float32))
+        assert not np.isfinite(dx[0]).any() and np.isfinite(dx[1:]).all()
+
+
+def test_every_code_and_scale(dbf):
+    """All 16 codes at every scale that the bf16 expansion of the gradient and fp32 can hold, one term per output."""
+    codes = np.arange(16, dtype=np.uint8)
+    table = np.concatenate([R.E2M1, -R.E2M1])
+    bytes_ = np.arange(0, 253)
+    N, M = len(bytes_), 32
+    packed = torch.from_numpy(np.tile((codes[0::2] | codes[1::2] << 4).astype(np.uint8), (N, 2))).cuda()
+    scales = np.zeros((2, 1, 32, 4, 4), np.uint8)
+    for r, b in enumerate(bytes_):
+        scales[r // 128, 0, r % 32, r % 128 // 32, 0] = b
+    L = dbf.Mx4Layer(M, N, packed, torch.from_numpy(scales).cuda())
+    value = np.tile(table, 2)[None, :] * np.exp2(bytes_[:, None] - 127.0)
+    assert np.array_equal(host(L.dequantize(torch.float32)), value.astype(np.float32).astype(np.float64))
+    dy = np.eye(N)
+    dx = host(dbf.mx4_backward(L, torch.tensor(dy).to(torch.bfloat16).cuda(), dx_dtype=torch.float32))
+    # products below the smallest normal fp32 may be flushed
+    ok = (np.abs(value) >= 2.0 ** -126) | (value == 0)
+    assert np.array_equal(dx[ok], value[ok]) and np.all(np.abs(dx[~ok]) <= np.abs(value[~ok]))
+
+
+# ---- how calls may be made
+def test_empty_batches(dbf):
+    L = layer_of(dbf, np.ones((64, 32)))
+    x = torch.empty(0, 32, device="cuda")
+    assert dbf.mx4_forward(L, x).shape == (0, 64)
+    assert dbf.mx4_backward(L, torch.empty(0, 64, device="cuda")).shape == (0, 32)
+    saved = dbf.Act8.empty(0, 64, "cuda"), dbf.Act8.empty(0, 64, "cuda")
+    assert dbf.mx4_gated_forward(L, L, x, save=saved).shape == (0, 64)
+    dx, dg, du = dbf.mx4_gated_backward(L, L, torch.empty(0, 64, device="cuda"), saved)
+    assert dx.shape == (0, 32) and dg.shape == du.shape == (0, 64)
+    assert dbf.act8_load(dbf.act8_save(x)).shape == (0, 32)
+
+
+def test_rows_behind_the_last_token_are_left(dbf):
+    rng = np.random.default_rng(3)
+    for T, M, N in ((5, 64, 72), (70, 64, 520), (230, 256, 264)):
+        L = layer_of(dbf, exact_operand(rng, N, M))
+        big = torch.full((T + 40, N), 7.0, device="cuda", dtype=torch.bfloat16)
+        x = torch.tensor(exact_operand(rng, T, M)).to(torch.bfloat16).cuda()
+        dbf.mx4_forward(L, x, y=big[:T])
+        assert (big[T:] == 7).all() and not (big[:T] == 7).all()
+        bx = torch.full((T + 40, M), 7.0, device="cuda", dtype=torch.bfloat16)
+        dbf.mx4_backward(L, torch.ones(T, N, device="cuda", dtype=torch.bfloat16), dx=bx[:T])
+        assert (bx[T:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [1, 24, 200])
+def test_graph_replays_on_new_inputs(dbf, T):
+    """Forward, gated forward and backward captured once and replayed on other inputs, two graphs on one workspace."""
+    M, N = 520, 1000
+    rng = np.random.default_rng(T)
+    wg, wu = exact_operand(rng, N, M), exact_operand(rng, N, M)
+    gl, ul = layer_of(dbf, wg), layer_of(dbf, wu)
+    x = torch.zeros(T, M, device="cuda", dtype=torch.bfloat16)
+    y = torch.zeros(T, N, device="cuda")
+    dx = torch.zeros(T, M, device="cuda")
+    ws = dbf.alloc_workspace(max(dbf.mx4_workspace_bytes(gl, T), dbf.mx4_gated_workspace_bytes(gl, ul, T),
+                                 dbf.mx4_backward_workspace_bytes(gl, T, torch.float32)), "cuda")
+    h = torch.zeros(T, N, device="cuda")
+    graphs = []
+    s = torch.cuda.Stream()
+    for f in (lambda: (dbf.mx4_forward(gl, x, y=y, ws=ws), dbf.mx4_backward(gl, y, dx=dx, ws=ws)),
+              lambda: dbf.mx4_gated_forward(gl, ul, x, h=h, ws=ws)):
+        with torch.cuda.stream(s):
+            f()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            f()
+        graphs.append(g)
+    for seed in (1, 2, 3):
+        xv = exact_operand(np.random.default_rng(seed), T, M)
+        x.copy_(torch.tensor(xv).to(torch.bfloat16))
+        graphs[1].replay()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        ref = xv @ wg.T
+        assert np.array_equal(host(y), ref)
+        eager = dbf.mx4_gated_forward(gl, ul, x, h_dtype=torch.float32)
+        assert torch.equal(h, eager)
+        assert torch.equal(dx, dbf.mx4_backward(gl, y, dx_dtype=torch.float32))
+    assert dbf.workspace_status(ws) == 0
+
+
+def test_calls_follow_what_was_enqueued_before(dbf):
+    """x, and without static_weights the weights too, may be written by the work just before the call; y may be read
+    by it. Long chains of launches on one stream, each depending on the last."""
+    M = N = 512
+    rng = np.random.default_rng(9)
+    ws_ = [exact_operand(rng, N, M) / 16 for _ in range(2)]
+    for T in (1, 20, 90):
+        src = [dbf.mx4_quantize(torch.tensor(w, dtype=torch.float32).cuda()) for w in ws_]
+        L = dbf.Mx4Layer(M, N, src[0][0].clone(), src[0][1].clone())
+        x = torch.tensor(exact_operand(rng, T, M)).to(torch.bfloat16).cuda()
+        want = []
+        for w in src:
+            want.append([dbf.mx4_forward(dbf.Mx4Layer(M, N, *w), x.clone(), y_dtype=torch.float32),
+                         dbf.mx4_backward(dbf.Mx4Layer(M, N, *w), x.clone(), dx_dtype=torch.float32)])
+        torch.cuda.synchronize()
+        y, dx, cur = torch.empty(T, N, device="cuda"), torch.empty(T, M, device="cuda"), torch.empty_like(x)
+        outs = []
+        for i in range(24):
+            L.codes.copy_(src[i % 2][0])
+            L.scales.copy_(src[i % 2][1])
+            cur.zero_()
+            cur.copy_(x)
+            dbf.mx4_forward(L, cur, y=y)
+            dbf.mx4_backward(L, cur, dx=dx)
+            outs.append((y.clone(), dx.clone()))
+            y.fill_(-1.0)
+        for i, (a, b) in enumerate(outs):
+            assert torch.equal(a, want[i % 2][0]) and torch.equal(b, want[i % 2][1])
+
+
+def test_two_streams_at_once(dbf):
+    """Calls on two streams with workspaces of their own give what they give alone."""
+    rng = np.random.default_rng(4)
+    jobs = []
+    for T, M, N in ((1, 2048, 4096), (33, 1000, 3000), (300, 1024, 2048), (2, 4096, 11008)):
+        L = layer_of(dbf, exact_operand(rng, N, M))
+        x = torch.tensor(exact_operand(rng, T, M)).to(torch.bfloat16).cuda()
+        jobs.append((L, x, dbf.mx4_forward(L, x, y_dtype=torch.float32), dbf.mx4_gated_forward(L, L, x)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [dbf.alloc_workspace(max(dbf.mx4_gated_workspace_bytes(j[0], j[0], j[1].shape[0]) for j in jobs), "cuda") for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for rep in range(6):
+        for k, st in enumerate(streams):
+            L, x, ref, href = jobs[(rep + k) % len(jobs)]
+            y, h = torch.empty_like(ref), torch.empty_like(href)
+            st.wait_stream(torch.cuda.current_stream())
+            dbf.mx4_forward(L, x, y=y, ws=wss[k], static_weights=True, stream=st)
+            dbf.mx4_gated_forward(L, L, x, h=h, ws=wss[k], static_weights=True, stream=st)
+            got.append((y, ref, h, href))
+    torch.cuda.synchronize()
+    for y, ref, h, href in got:
+        assert torch.equal(y, ref) and torch.equal(h, href)
+    assert all(dbf.workspace_status(w) == 0 for w in wss)
+
+
+def test_offsets_past_32_bits(dbf):
+    """y, x and an 8-bit activation of more than 2^31 elements (and more than 2^32 bytes)."""
+    T, M, N = 270_001, 32, 8192
+    rng = np.random.default_rng(2)
+    w, row = exact_operand(rng, N, M), exact_operand(rng, 5, M)
+    L = layer_of(dbf, w)
+    pick = [0, 1, 131_071, 262_143, 262_144, 265_000, 269_999, 270_000]
+    x = torch.tensor(row).to(torch.bfloat16).cuda()[torch.arange(T, device="cuda") % 5].contiguous()
+    y = dbf.mx4_forward(L, x)
+    ref = torch.tensor(row @ w.T).float().to(torch.bfloat16)
+    for t in pick:
+        assert torch.equal(y[t].cpu(), ref[t % 5])
+    a = dbf.act8_save(y)
+    codes, scales = dbf.mx4_quantize(y)
+    small = y[pick].contiguous()
+    back, want = dbf.act8_load(a), dbf.act8_load(dbf.act8_save(small))
+    assert torch.equal(back[pick], want)
+    del back
+    want4 = dbf.mx4_dequantize(*dbf.mx4_quantize(small), len(pick), N)
+    assert torch.equal(dbf.mx4_dequantize(codes, scales, T, N)[pick], want4)
+    del codes, scales, a
+    dx = dbf.mx4_backward(L, y, dx_dtype=torch.float32)
+    for t in pick:
+        assert torch.equal(dx[t], dx[t % 5])
+    # these sums pass 2^24 units (9.4e6 in units of 0.5 or less), so they are not exact
+    y5 = host(y[:5])
+    assert np.all(np.abs(host(dx[:5]) - y5 @ w) <= N * 2.0 ** -23 * (np.abs(y5) @ np.abs(w)))
+
+
+def test_refusals(dbf):
+    L = layer_of(dbf, np.ones((64, 96)))
+    x = torch.ones(4, 96, device="cuda")
+    for bad in (x[:, :64], x.t(), x.half(), x.double(), x.cpu(), torch.ones(4, 192, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError):
+            dbf.mx4_forward(L, bad)
+    with pytest.raises(ValueError):
+        dbf.mx4_forward(L, x, y=torch.empty(4, 65, device="cuda"))
+    with pytest.raises(ValueError):
+        dbf.mx4_forward(L, x, accumulate=True)
+    with pytest.raises(ValueError):
+        dbf.Mx4Layer(96, 64, L.codes[:, :32], L.scales)
+    with pytest.raises(ValueError):
+        dbf.Mx4Layer(96, 64, L.codes, L.scales.view(-1))
+    with pytest.raises(dbf.DbfError) as e:
+        dbf.mx4_forward(L, x, ws=torch.zeros(128, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == dbf.ERR_WORKSPACE
+    with pytest.raises(dbf.DbfError) as e:   # rows that start off a 16-byte boundary
+        dbf.mx4_forward(L, torch.ones(4 * 96 + 1, device="cuda")[1:].view(4, 96))
+    assert e.value.status == dbf.ERR_ALIGNMENT
+    with pytest.raises(ValueError):
+        dbf.mx4_gated_forward(L, L, x, g_add=torch.ones(4, 63, device="cuda"))
+    with pytest.raises(KeyError):
+        dbf.mx4_gated_forward(L, L, x, act="relu")
+    with pytest.raises(ValueError):
+        dbf.mx4_gated_forward(L, L, x, save=(dbf.Act8.empty(4, 64, "cuda"), dbf.Act8.empty(5, 64, "cuda")))
+    with pytest.raises(ValueError):
+        dbf.act8_save(x, out=dbf.Act8.empty(4, 95, "cuda"))
+
+
+# ---- together: an adapter on a 4-bit gated block, trained with 8-bit checkpoints
+def test_adapter_training_step_on_a_4bit_block(dbf):
+    """The step of one block: adapter branches from dbf_forward are added inside the gated kernel, x, g and u are kept
+    in 8 bits, dg and du feed dbf_backward of both adapters, dx collects the base's and the adapters' parts. Against
+    the same step in 64 bits."""
+    import dbf_synth as S
+    import oracle
+    from gpu_util import dev_layer, random_layer, rel_err
+    T, M, N, r = 200, 256, 384, 128
+    rng = np.random.default_rng(11)
+    wg, wu = (rng.standard_normal((N, M)) / np.sqrt(M) for _ in range(2))
+    gl, ul = layer_of(dbf, wg), layer_of(dbf, wu)
+    ad = [random_layer(rng, M, N, r, 1) for _ in range(2)]
+    for L in ad:   # a branch as large as the base's output
+        L.alpha[:] = S.to_f16_bits(np.full(N, 2.0 ** -7))
+    dev = [dev_layer(L) for L in ad]
+    x = torch.tensor(rng.standard_normal((T, M))).to(torch.bfloat16).cuda()
+    dh = torch.tensor(rng.standard_normal((T, N))).to(torch.bfloat16).cuda()
+    # forward
+    add = [dbf.forward(d, x) for d in dev]
+    saved = dbf.Act8.empty(T, N, "cuda"), dbf.Act8.empty(T, N, "cuda")
+    h = dbf.mx4_gated_forward(gl, ul, x, g_add=add[0], u_add=add[1], save=saved)
+    x8 = dbf.act8_save(x)
+    # backward
+    dx, dg, du = dbf.mx4_gated_backward(gl, ul, dh, saved, dx_dtype=torch.float32)
+    xr = dbf.act8_load(x8)
+    grads = [dbf.backward(d, xr, dd) for d, dd in zip(dev, (dg, du))]
+    total = dx + grads[0].dx + grads[1].dx
+    # 64 bits: every stored value rounded where the step rounds it
+    xq = R.mx4(host(x))[0]
+    g, u = (xq @ R.mx4(w.astype(np.float32))[0].T + host(a) for w, a in zip((wg, wu), add))
+    tol = 2.0 ** -8
+    assert np.all(np.abs(host(h) - R.gate("silu", g) * u) <= (tol + 2.0 ** -12) * np.abs(R.gate("silu", g) * u) + 1e-5)
+    # g and u may round to the neighbouring 8-bit code where fp32 and fp64 sums lie on two sides of a border
+    g8, u8 = (host(dbf.act8_load(a, dtype=torch.float32)) for a in saved)
+    for got, want in ((g8, g), (u8, u)):
+        val, _, byte = R.act8(want.astype(np.float32))
+        step = np.exp2(byte.repeat(32, axis=1)[:, :N] - 127.0) * 2.0 ** -9 + np.abs(want) / 8
+        assert np.all(np.abs(got - val) <= step) and np.mean(got != val) < 1e-3
+    h64 = host(dh)
+    rdg, rdu = h64 * u8 * R.gate_slope("silu", g8), h64 * R.gate("silu", g8)
+    for got, want in ((dg, rdg), (du, rdu)):
+        assert np.all(np.abs(host(got) - want) <= (tol + 2.0 ** -12) * np.abs(want) + 1e-6)
+    xr64 = R.act8(host(x))[0]
+    assert np.array_equal(host(xr), xr64)
+    base = host(dg) @ R.mx4(wg.astype(np.float32))[0] + host(du) @ R.mx4(wu.astype(np.float32))[0]
+    refs = [oracle.backward(L, xr64.astype(np.float32), host(d).astype(np.float32)) for L, d in zip(ad, (dg, du))]
+    assert rel_err(host(total), base + refs[0].dx + refs[1].dx) < 2e-3   # the adapters' tolerance
