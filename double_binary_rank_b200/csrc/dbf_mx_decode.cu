@@ -32,6 +32,7 @@ using namespace tc;
 constexpr int kMaxRing = 8;
 constexpr int kMaxColumns = 64;   // tokens of a call times its weights: beyond, dbf_mx_gemm.cu is faster
 constexpr int kInline = 48;       // rows of 256 columns of x up to which a CTA quantises its part itself
+constexpr int kSplit = 4;          // parts of the columns (2048 x 2048 at one token: 4.9 us in 4, 5.7 us in 8); 8 where x does not fit otherwise
 constexpr int kWorkers = 8;
 constexpr int kThreads = 32 * (2 + kWorkers);
 constexpr uint32_t kABytes = 128 * 128, kSfBytes = 1024;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
 }
 
 struct Shape {
-    int w, split, ring, nks, pre;
+    int w, split, ring, nks, pre, tmem_cols;
     size_t smem;
 };
 
@@ -247,13 +248,13 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
     const int64_t fixed = 1024 + sizeof(Smem);
     for (int per_sm = 2; per_sm >= 1; --per_sm) {
         const int64_t room = (per_sm == 2 ? 113 : 227) * 1024 - fixed;
-        int64_t split = std::max<int64_t>(1, std::min<int64_t>({8, nk, per_sm * sms / row_blocks}));
+        int64_t split = std::max<int64_t>(1, std::min<int64_t>({kSplit, nk, per_sm * sms / row_blocks}));
         // one CTA to an SM where that occupies four fifths of them and a CTA's
         // weights are all in flight at once (4096 x 4096 at one token: 6.2 us split
         // in 4, 7.0 us in 8; 8192 x 8192, whose CTAs would take 16 stages: 13.0 us
         // at one to an SM, 10.2 us at two)
         const int64_t one = sms / row_blocks;
-        if (one >= 1 && one <= 8 && one * row_blocks * 5 >= sms * 4 && (nk + one - 1) / one <= kMaxRing) split = std::min(one, nk);
+        if (one >= 1 && one <= kSplit && one * row_blocks * 5 >= sms * 4 && (nk + one - 1) / one <= kMaxRing) split = std::min(one, nk);
         for (; split <= std::min<int64_t>(8, nk); ++split) {
             p.split = static_cast<int>(split);
             p.nks = static_cast<int>((nk + split - 1) / split);
@@ -263,10 +264,14 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
             while (ring < fit && ring * stage + x_bytes < partials) ++ring;   // the partial sums take this place
             if (ring * stage + x_bytes < partials) continue;
             p.ring = static_cast<int>(ring);
-            // at least a third of an SM: with two CTAs to an SM at most, their tensor
-            // memory (256 columns each) is always there, so no CTA waits for it while
-            // another of its cluster waits at the exchange
-            p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + ring * stage, 77 * 1024));
+            // Shared memory in proportion to tensor memory: whatever CTAs share an SM,
+            // of this or another of these kernels, their columns are always there, so
+            // that no CTA waits for them while another of its cluster waits at the
+            // exchange.
+            const int cols = mats * p.w + 8 * mats + 8;
+            p.tmem_cols = 32;
+            while (p.tmem_cols < cols) p.tmem_cols *= 2;
+            p.smem = static_cast<size_t>(std::max<int64_t>(fixed + x_bytes + ring * stage, 227 * 1024 / 512 * p.tmem_cols));
             p.pre = T * p.nks > kInline ? 1 : 0;
             return true;
         }
@@ -289,7 +294,6 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
     const bool gated = c.mats == 2;
     CUtensorMap a[2], sa[2];
     for (int m = 0; m < 2; ++m) {
-        const int from = gated ? m : 0;
         const uint64_t dims[2] = {static_cast<uint64_t>(code_pitch(c.M)), static_cast<uint64_t>(c.N)};
         const uint64_t strides[1] = {dims[0]};
         const uint32_t box[2] = {128, 128};
@@ -297,8 +301,12 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
         const uint64_t sdims[3] = {128, tiles, static_cast<uint64_t>((c.N + 127) / 128)};
         const uint64_t sstrides[2] = {512, tiles * 512};
         const uint32_t sbox[3] = {128, 2, 1};
-        if (!tc_map(&a[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes[from], dims, strides, box, true) ||
-            !tc_map(&sa[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, c.scales[from], sdims, sstrides, sbox, false))
+        if (m > 0 && !gated) {
+            a[m] = a[0], sa[m] = sa[0];
+            break;
+        }
+        if (!tc_map(&a[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes[m], dims, strides, box, true) ||
+            !tc_map(&sa[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, c.scales[m], sdims, sstrides, sbox, false))
             return cudaErrorInvalidValue;
     }
     CUtensorMap xm = a[0], xs = sa[0];
@@ -328,9 +336,7 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
     g.xd = c.xd;
     g.vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
     g.early = p.pre || (c.flags & DBF_WEIGHTS_STATIC) ? 1 : 0;
-    const int cols = c.mats * p.w + 8 * c.mats + 8;
-    g.tmem_cols = 32;
-    while (static_cast<int>(g.tmem_cols) < cols) g.tmem_cols *= 2;
+    g.tmem_cols = static_cast<uint32_t>(p.tmem_cols);
     g.ep = c.ep;
     g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
 

@@ -518,10 +518,10 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
 
     CUtensorMap a[2], sa[2], b, sb;
     const bool gated = c.mats == 2;
-    for (int m = 0; m < 2; ++m)
-        if (!code_map(&a[m], c.codes[gated ? m : 0], c.M, c.N, 128) ||
-            !scale_map(&sa[m], c.scales[gated ? m : 0], c.M, (c.N + 127) / 128, 1))
+    for (int m = 0; m < c.mats; ++m)
+        if (!code_map(&a[m], c.codes[m], c.M, c.N, 128) || !scale_map(&sa[m], c.scales[m], c.M, (c.N + 127) / 128, 1))
             return cudaErrorInvalidValue;
+    if (!gated) a[1] = a[0], sa[1] = sa[0];
     if (!code_map(&b, codes, c.M, c.T, pl.w / 2) ||
         !scale_map(&sb, scales, c.M, (c.T + pl.w - 1) / pl.w * (pl.pad / 128), pl.pad / 128))
         return cudaErrorInvalidValue;

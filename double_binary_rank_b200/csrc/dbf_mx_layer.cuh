@@ -64,9 +64,9 @@ template <bool kGated>
 __device__ __forceinline__ void epilogue_reads(const Epilogue &e, int64_t t, int c, bool on, Raw8 (&x)[kGated ? 2 : 1])
 {
     const int64_t N = e.N;
-    if (kGated) {
+    if constexpr (kGated) {
         x[0] = load_raw8(e.g_add, e.add_dt, t * N, on && e.g_add ? c : N, N, epilogue_vec(e));
-        x[kGated] = load_raw8(e.u_add, e.add_dt, t * N, on && e.u_add ? c : N, N, epilogue_vec(e));
+        x[1] = load_raw8(e.u_add, e.add_dt, t * N, on && e.u_add ? c : N, N, epilogue_vec(e));
     } else {
         x[0] = load_raw8(e.y, e.yd, t * N, on && e.accumulate ? c : N, N, epilogue_vec(e));
     }
@@ -94,13 +94,13 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue &e, int64_t t, in
 {
     const int64_t N = e.N;
     const bool vec = epilogue_vec(e);
-    if (!kGated) {
+    if constexpr (!kGated) {
         if (e.accumulate) add_raw8(x[0], e.yd, vec, v[0]);
     } else {
         float(&g)[8] = v[0];
-        float(&u)[8] = v[kGated];
+        float(&u)[8] = v[1];
         if (e.g_add) add_raw8(x[0], e.add_dt, vec, g);
-        if (e.u_add) add_raw8(x[kGated], e.add_dt, vec, u);
+        if (e.u_add) add_raw8(x[1], e.add_dt, vec, u);
         if (e.g8) {
             if (c + 8 > N) {   // columns past the last may hold anything, a NaN too
 #pragma unroll
