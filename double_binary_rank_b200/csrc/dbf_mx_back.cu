@@ -39,17 +39,21 @@ namespace {
 using namespace mx;
 using namespace tc;
 
-constexpr int kStages = 4;
+constexpr int kMaxStages = 10;
 constexpr int kExpand = 8, kEpiWarps = 8;   // warps
 constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
 constexpr int kAhead = 4;                           // stages that the expansion's loads run ahead
 constexpr int kRowsK = 64;                          // rows of W per stage
-constexpr uint32_t kABytes = 128 * kRowsK * 2, kBBytes = 2 * 128 * kRowsK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kABytes = 128 * kRowsK * 2;
+// A stage is this CTA's half of W's columns and w / 2 token rows. From the last
+// MMA on a stage to the next one's data it takes about 2.2 us, so a ring of n
+// stages gives one every 2.2 / n us at best: as many as fit.
+__host__ __device__ constexpr uint32_t stage_bytes(int w) { return kABytes + w / 2 * kRowsK * 2; }
+constexpr int kMaxSmem = 227 * 1024;
 constexpr uint32_t kTmemCols = 512;
 
 struct Smem {
-    uint64_t full[kStages], empty[kStages], acc_full, acc_empty, drain, exit_bar;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, drain, exit_bar;
     uint32_t tmem_base;
     int abort;
 };
@@ -64,6 +68,7 @@ struct Args {
     int mats, planes;    // products summed: weights, pieces of the gradient
     int64_t plane_rows;  // rows from one piece to the next in the gradient's map
     int w;               // tokens per tile
+    int ring;            // stages in shared memory
     int n_p, n_c;        // tiles along the columns of W and along the tokens
     int splits;          // parts of the contraction; over 1, each writes fp32 sums [T][M] of its own
     int tiles;           // n_p * n_c * splits
@@ -128,7 +133,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
 {
     extern __shared__ uint8_t raw[];
     uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float *turn = reinterpret_cast<float *>(stage0 + kStages * kStageBytes);
+    const int stages = g.ring;
+    const uint32_t stage_size = stage_bytes(g.w);
+    float *turn = reinterpret_cast<float *>(stage0 + stages * stage_size);
     Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kTurnFloats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
     volatile int *abort = &sh->abort;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             bar_init(&sh->full[i], 1 + 2 * kExpand);
             bar_init(&sh->empty[i], 1);
         }
@@ -173,18 +180,18 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                     }
                     const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
                     const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
-                    uint8_t *st = stage0 + s * kStageBytes + kABytes;
+                    uint8_t *st = stage0 + s * stage_size + kABytes;
                     if (rank == 0) bar_expect_tx(&sh->full[s], 4 * quarter_w * kRowsK * 2);
                     tma_2d_pair(st, map, i * kRowsK, row, &sh->full[s]);
                     tma_2d_pair(st + quarter_w * kRowsK * 2, map, i * kRowsK, row + 2 * quarter_w, &sh->full[s]);
                     ++issued;
-                    if (++s == kStages) s = 0, ph ^= 1u;
+                    if (++s == stages) s = 0, ph ^= 1u;
                     if (++i == g.nn) i = 0, ++seg;
                 }
             }
             if (*abort && rank == 0)
-                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+                for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+                    drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(stage0) + s * kStageBytes;
+                    const uint32_t st = smem_u32(stage0) + s * stage_size;
                     // A: 64 columns of W to a 128-byte row; groups of 8 rows 1 KB apart, the second
                     // 64 columns 8 KB on
                     const uint64_t a = sw128_desc(st, 1024, 8192), b0 = sw128_desc(st + kABytes), b1 = sw128_desc(st + kABytes + second);
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                         mma_bf16_pair(tmem + 256, a + kk * (2048 >> 4), b1 + 2 * kk, id, acc);
                     }
                     commit_pair_both(&sh->empty[s]);
-                    if (++s == kStages) s = 0, ph ^= 1u;
+                    if (++s == stages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
                 commit_pair_both(&sh->acc_full);
@@ -296,12 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(dst + s * kStageBytes + (((chunk0 + j) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(dst + s * stage_size + (((chunk0 + j) ^ (r & 7)) << 4)) =
                         make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(&sh->full[s]);
-                if (++s == kStages) s = 0, ph ^= 1u;
+                if (++s == stages) s = 0, ph ^= 1u;
             }
         }
     } else {
@@ -554,9 +561,9 @@ int resident_pairs(cudaLaunchConfig_t cfg)
 
 // Tokens per tile (a multiple of 32 up to 512) and parts of the contraction.
 // Cost of the last pair to finish, in cycles: waves of tiles, each so many
-// stages, a stage taking its eight MMAs (2 w) or the expansion of W (the same
-// at every width), and an epilogue; the parts' sums are written and read once
-// more.
+// stages, a stage taking its eight MMAs (2 w), the expansion of W (the same at
+// every width) or its share of the ring's round trip, and an epilogue; the
+// parts' sums are written and read once more.
 constexpr int64_t kMaxSplits = 16;
 struct Plan {
     int w, splits;
@@ -573,7 +580,8 @@ Plan plan(int64_t M, int64_t T, int64_t nk)
             const double waves = static_cast<double>((tiles * splits + pairs - 1) / pairs);
             const double stages = static_cast<double>((nk + splits - 1) / splits);
             const double join = splits > 1 ? 4000.0 + 8.0 * T * M * (splits + 1) / 3500.0 : 0.0;   // a launch, and bytes at 3.5 KB a cycle
-            const double cost = waves * (stages * std::max(2.0 * w, 600.0) + 1500 + 12.0 * w) + join;
+            const double ring = std::min(10.0, 220.0 * 1024 / stage_bytes(w));
+            const double cost = waves * (stages * std::max({2.0 * w, 450.0, 4000.0 / ring}) + 3000 + 12.0 * w) + join;
             if (least < 0 || cost < least) least = cost, best = {w, splits};
         }
         if (w >= T) break;
@@ -642,7 +650,10 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     g.ep.N = static_cast<int32_t>(c.M), g.ep.T = c.T;
     g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
 
-    const int smem = 1024 + kStages * kStageBytes + kEpiWarps * kTurnFloats * 4 + sizeof(Smem);
+    const int fixed = 1024 + kEpiWarps * kTurnFloats * 4 + sizeof(Smem);
+    g.ring = std::min<int>(kMaxStages, (kMaxSmem - fixed) / stage_bytes(w));
+    // the largest a launch may ask for, so that no second CTA shares the SM: each allocates all of its tensor memory
+    const int smem = kMaxSmem;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(mx_back_kernel), smem);
     if (e != cudaSuccess) return e;
     PdlAttr attr;

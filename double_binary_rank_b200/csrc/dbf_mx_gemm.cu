@@ -40,21 +40,28 @@ namespace {
 using namespace mx;
 using namespace tc;
 
-constexpr int kStages = 4;
+constexpr int kMaxStages = 10, kMaxSfBufs = 4;
 constexpr int kMaxW = 224;
 constexpr int kScaleWarps = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kScaleWarps + kEpiWarps);
 constexpr uint32_t kABytes = 128 * 128;            // 128 rows x 256 codes
-constexpr uint32_t kBBytes = kMaxW / 2 * 128;      // this CTA's half of the tokens
-constexpr uint32_t kSfABytes = 1024, kSfBBytes = 2048;
-constexpr uint32_t kStageBytes = 2 * kABytes + kBBytes + 2 * kSfABytes + kSfBBytes;
-// tensor-memory columns: 2 w per set of accumulators, then buffers of scales: 8
-// per weight block (4 per K half), then 4 per K half and 128 tokens
+constexpr uint32_t kSfBytes = 1024;                // scales of 128 rows x 256 codes
+constexpr int kMaxSmem = 227 * 1024;
+// A stage: the codes of 'accs' blocks of 128 weight rows and of this CTA's half
+// of the tokens, then the scales of both (of all the tokens). From the last MMA
+// on a stage to the next one's data it takes about 2.2 us, so a ring of n
+// stages gives one every 2.2 / n us at best: as many as fit.
+__host__ __device__ constexpr uint32_t b_at(int accs) { return accs * kABytes; }
+__host__ __device__ constexpr uint32_t sf_at(int accs, int w) { return accs * kABytes + w / 2 * 128; }
+__host__ __device__ constexpr uint32_t stage_bytes(int accs, int w) { return sf_at(accs, w) + (accs + (w > 128 ? 2 : 1)) * kSfBytes; }
+// tensor-memory columns: accs w per set of accumulators, then buffers of
+// scales: 8 per weight block (4 per K half), 16 kept for them, then 4 per K half
+// and 128 tokens
 __host__ __device__ constexpr uint32_t sf_cols(int w) { return w > 128 ? 32u : 24u; }
 constexpr uint32_t kTmemCols = 512;
 
 struct Smem {
-    uint64_t full[kStages], sf_full[kStages], empty[kStages], sf_ready[kStages], acc_full[2], acc_empty[2], drain, exit_bar;
+    uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages], sf_ready[kMaxSfBufs], acc_full[2], acc_empty[2], drain, exit_bar;
     uint32_t tmem_base;
     int abort;
 };
@@ -62,11 +69,13 @@ struct Smem {
 struct Args {
     int nk;         // stages of 256 columns
     int w;          // tokens per tile
-    int sf_bufs;    // scale buffers, 2 to kStages
+    int accs;       // accumulators of a set: 2, or 1 (plain, where tiles are few)
+    int ring;       // stages in shared memory
+    int sf_bufs;    // scale buffers, 2 to kMaxSfBufs
     int bufs;       // 2: two sets of accumulators, so that an epilogue overlaps the next tile's products
     int n_p;        // row tiles
     int tiles;
-    int row_step;   // weight rows of a tile: 512 plain, 256 gated
+    int row_step;   // weight rows of a tile: 256 accs plain, 256 gated
     int row_off;    // rows from the first accumulator's to the second's: 256 plain, 0 gated
     Epilogue ep;
     int32_t *status;
@@ -132,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     constexpr int kMats = kGated ? 2 : 1;
     extern __shared__ uint8_t raw[];
     uint8_t *stage0 = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float *turn = reinterpret_cast<float *>(stage0 + kStages * kStageBytes);
+    const int accs = kGated ? 2 : g.accs, stages = g.ring;
+    const uint32_t stage_size = stage_bytes(accs, g.w), off_b = b_at(accs), off_sf = sf_at(accs, g.w);
+    float *turn = reinterpret_cast<float *>(stage0 + stages * stage_size);
     Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kMats * kTurnFloats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -140,12 +151,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     volatile int *abort = &sh->abort;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             bar_init(&sh->full[i], 1);
             bar_init(&sh->sf_full[i], 1);
-            bar_init(&sh->sf_ready[i], 2 * kScaleWarps);
             bar_init(&sh->empty[i], 1);
         }
+        for (int i = 0; i < kMaxSfBufs; ++i) bar_init(&sh->sf_ready[i], 2 * kScaleWarps);
         for (int i = 0; i < 2; ++i) {
             bar_init(&sh->acc_full[i], 1);
             bar_init(&sh->acc_empty[i], 2 * kEpiWarps);
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     if (warp == 0) {
         if (lane == 0) {
             const int half_w = g.w / 2, nrt = g.w > 128 ? 2 : 1;
-            const uint32_t bytes = 2 * (2 * kABytes + half_w * 128), sf_bytes = 2 * kSfABytes + nrt * 1024;
+            const uint32_t bytes = 2 * off_sf, sf_bytes = stage_size - off_sf;
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true, waited = false;
@@ -181,31 +192,31 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                         ok = false;
                         break;
                     }
-                    uint8_t *st = stage0 + s * kStageBytes;
+                    uint8_t *st = stage0 + s * stage_size, *sf = st + off_sf;
                     if (rank == 0) bar_expect_tx(&sh->full[s], bytes);
+                    bar_expect_tx(&sh->sf_full[s], sf_bytes);   // the scales are counted by each CTA for itself
                     tma_2d_pair(st, &mA0, ks * 128, row0, &sh->full[s]);
-                    tma_2d_pair(st + kABytes, &mA1, ks * 128, row1, &sh->full[s]);
-                    uint8_t *sf = st + 2 * kABytes + kBBytes;
-                    // the scales are counted by each CTA for itself
-                    bar_expect_tx(&sh->sf_full[s], sf_bytes);
                     tma_3d(sf, &mS0, 0, ks * 2, row0 >> 7, &sh->sf_full[s]);
-                    tma_3d(sf + kSfABytes, &mS1, 0, ks * 2, row1 >> 7, &sh->sf_full[s]);
+                    if (accs == 2) {
+                        tma_2d_pair(st + kABytes, &mA1, ks * 128, row1, &sh->full[s]);
+                        tma_3d(sf + kSfBytes, &mS1, 0, ks * 2, row1 >> 7, &sh->sf_full[s]);
+                    }
                     if (!waited) {
                         griddep_wait();
                         waited = true;
                     }
-                    tma_2d_pair(st + 2 * kABytes, &mB, ks * 128, tok, &sh->full[s]);
-                    tma_3d(sf + 2 * kSfABytes, &mSB, 0, ks * 2, c * nrt, &sh->sf_full[s]);
+                    tma_2d_pair(st + off_b, &mB, ks * 128, tok, &sh->full[s]);
+                    tma_3d(sf + accs * kSfBytes, &mSB, 0, ks * 2, c * nrt, &sh->sf_full[s]);
                     ++issued;
-                    if (++s == kStages) s = 0, ph ^= 1u;
+                    if (++s == stages) s = 0, ph ^= 1u;
                 }
             }
             // after a wait gave up, the loads in flight are still waited for
             // (CTA 0's barriers count both CTAs' bytes)
             if (*abort)
-                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
-                    drain_wait(&sh->sf_full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
-                    if (rank == 0) drain_wait(&sh->full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
+                for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
+                    drain_wait(&sh->sf_full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
+                    if (rank == 0) drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
                 }
         }
     } else if (warp == 1) {
@@ -213,28 +224,28 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             int s = 0;
             uint32_t ph = 0;
             Turn acc, sf_turn;
-            const uint32_t sf0 = tmem + 2 * g.w * g.bufs, b_half = g.w > 128 ? 8 : 4;
+            const uint32_t sf0 = tmem + accs * g.w * g.bufs, b_half = g.w > 128 ? 8 : 4;
             bool ok = true;
             const uint32_t id0 = mxf4_idesc(256, g.w, 0), id2 = mxf4_idesc(256, g.w, 2);
             for (int tile = unit; tile < g.tiles && ok; tile += units, acc.next(g.bufs)) {
                 ok = bar_wait(&sh->acc_empty[acc.buf], acc.phase ^ 1u, abort);
                 if (!ok) break;
-                const uint32_t d = tmem + acc.buf * 2 * g.w;
+                const uint32_t d = tmem + acc.buf * accs * g.w;
                 for (int ks = 0; ks < g.nk; ++ks, sf_turn.next(g.sf_bufs)) {
                     ok = bar_wait(&sh->full[s], ph, abort) && bar_wait(&sh->sf_ready[sf_turn.buf], sf_turn.phase, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(stage0) + s * kStageBytes, sf = sf0 + sf_turn.buf * sf_cols(g.w);
-                    const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + 2 * kABytes);
+                    const uint32_t st = smem_u32(stage0) + s * stage_size, sf = sf0 + sf_turn.buf * sf_cols(g.w);
+                    const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + off_b);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t id = kk & 1 ? id2 : id0, acc = ks > 0 || kk > 0 ? 1u : 0u;
                         const uint32_t sb = sf + 16 + b_half * (kk >> 1);
                         mma_mxf4<2>(d, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, acc);
-                        mma_mxf4<2>(d + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
+                        if (accs == 2) mma_mxf4<2>(d + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
                     }
                     commit_pair_both(&sh->empty[s]);
-                    if (++s == kStages) s = 0, ph ^= 1u;
+                    if (++s == stages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
                 commit_pair_both(&sh->acc_full[acc.buf]);
@@ -251,48 +262,51 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
         uint32_t ph = 0;
         Turn buf;
         for (int64_t k = 0; k < total; ++k, buf.next(g.sf_bufs)) {
-            // the buffer is free once the MMAs of stage k - sf_bufs are done (with as many
-            // buffers as stages that stage's place in shared memory is this one's, and its
-            // load has waited for them)
+            // the buffer is free once the MMAs of stage k - sf_bufs are done
             const int64_t before = k - g.sf_bufs;
-            if (before >= 0 && !bar_wait(&sh->empty[before % kStages], static_cast<uint32_t>(before / kStages) & 1u, abort)) break;
+            if (before >= 0 && !bar_wait(&sh->empty[before % stages], static_cast<uint32_t>(before / stages) & 1u, abort)) break;
             if (!bar_wait(&sh->sf_full[s], ph, abort)) break;
             tc_fence_after();
-            const uint4 *sf = reinterpret_cast<const uint4 *>(stage0 + s * kStageBytes + 2 * kABytes + kBBytes) + lane;
+            const uint4 *sf = reinterpret_cast<const uint4 *>(stage0 + s * stage_size + off_sf) + lane;
             // 512 bytes hold 128 rows x 4 blocks, a lane's 16 the rows lane, lane + 32, ...
-            const uint32_t to = lanes + 2 * g.w * g.bufs + buf.buf * sf_cols(g.w);
-            tmem_st16(to, sf[0], sf[32], sf[64], sf[96]);
-            if (g.w > 128)
-                tmem_st16(to + 16, sf[128], sf[192], sf[160], sf[224]);
+            const uint32_t to = lanes + accs * g.w * g.bufs + buf.buf * sf_cols(g.w);
+            const uint4 *sb = sf + accs * 64;
+            if (accs == 2)
+                tmem_st16(to, sf[0], sf[32], sf[64], sf[96]);
             else
-                tmem_st8(to + 16, sf[128], sf[160]);
+                tmem_st8(to, sf[0], sf[32]);
+            if (g.w > 128)
+                tmem_st16(to + 16, sb[0], sb[64], sb[32], sb[96]);
+            else
+                tmem_st8(to + 16, sb[0], sb[32]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive_leader(&sh->sf_ready[buf.buf]);
-            if (++s == kStages) s = 0, ph ^= 1u;
+            if (++s == stages) s = 0, ph ^= 1u;
         }
     } else {
         griddep_wait();   // y (and the addends) belong to earlier work until then
         const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;
-        const uint32_t lanes0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (kGated ? 0 : half * g.w);
+        const bool two = !kGated && accs == 2;
+        const uint32_t lanes0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (two ? half * g.w : 0);
         float *own = turn + (warp - 2 - kScaleWarps) * kMats * kTurnFloats;
-        // gated: the two warps of a lane quarter take turns by 8 tokens of both
-        // accumulators; plain: each takes one accumulator
-        const int j_first = kGated ? half * 8 : 0, j_step = kGated ? 16 : 8;
+        // two plain accumulators: each of a lane quarter's two warps takes one;
+        // else they take turns by 8 (16) tokens
+        const int j_first = two ? 0 : half * 8, j_step = two ? 8 : 16;
         const bool simple = epilogue_is_simple(g.ep), bf16 = epilogue_is_bf16(g.ep);
         Turn acc;
         for (int tile = unit; tile < g.tiles; tile += units, acc.next(g.bufs)) {
-            const uint32_t lanes = lanes0 + acc.buf * 2 * g.w;
+            const uint32_t lanes = lanes0 + acc.buf * accs * g.w;
             uint64_t *full = &sh->acc_full[acc.buf], *empty = &sh->acc_empty[acc.buf];
             const int p = tile % g.n_p, c = tile / g.n_p;
-            const int n = p * g.row_step + (kGated ? 0 : half * g.row_off) + static_cast<int>(rank) * 128 + quarter * 32 +
+            const int n = p * g.row_step + (two ? half * g.row_off : 0) + static_cast<int>(rank) * 128 + quarter * 32 +
                           (lane & 3) * 8;
             const int64_t t = static_cast<int64_t>(c) * g.w + (lane >> 2);
             if (simple) {
                 if (!bar_wait(full, acc.phase, abort)) break;
                 tc_fence_after();
-                for (int j = kGated ? half * 16 : 0; j < g.w; j += kGated ? 32 : 16) {
+                for (int j = 2 * j_first; j < g.w; j += 2 * j_step) {
                     float v[kMats][16];
                     load_chunk(lanes + j, g.w, v);
                     simple_finish<kMats>(g.ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v);
@@ -415,7 +429,7 @@ int resident_pairs(const void *kernel, cudaLaunchConfig_t cfg)
 // What an epilogue costs per token of a tile, in cycles: plain bf16 rows, the
 // gate, addends, 8-bit copies (from 6 waves of 4096 -> 11008 at 2048 tokens).
 enum Kind { kPlain, kGate, kGateAdd, kGateSave, kKinds };
-constexpr double kEpilogueCycles[kKinds] = {25, 29, 73, 98};
+constexpr double kEpilogueCycles[kKinds] = {25, 29, 73, 98};   // plain: of two accumulators
 
 Kind kind_of(const Product &c)
 {
@@ -424,33 +438,40 @@ Kind kind_of(const Product &c)
 }
 
 struct Plan {
-    int w, bufs, pad;   // pad: scale rows of a tile
+    int w, bufs, accs, ring, pad;   // pad: scale rows of a tile
 };
+int fixed_smem(int mats) { return 1024 + kEpiWarps * mats * kTurnFloats * 4 + static_cast<int>(sizeof(Smem)); }
 
-// Tokens per tile, and one or two sets of accumulators (up to 224 tokens, or
-// 112). Cost of the last pair to finish, in cycles: waves of tiles, each nk
-// stages and an epilogue, which two sets hide behind the next tile's stages. A
-// stage takes its eight MMAs (4 w cycles) or its operands' way from L2 (about
-// 45 bytes a cycle and SM, 40 beside a running epilogue), whichever is longer:
-// narrow tiles pay for their weights' way there, so two sets win only where the
-// epilogue is long against K. 2048 x 8192 at 4096 tokens with addends: 120 us on
-// one set, 101 us on two; 4096 x 11008 at 2048 tokens: 114 us and 126 us.
+// Tokens per tile, one or two sets of accumulators, and for a plain product one
+// or two accumulators in a set. Cost of the last pair to finish, in cycles:
+// waves of tiles, each nk stages and an epilogue, which two sets hide behind the
+// next tile's stages. A stage takes its MMAs (2 w cycles an accumulator), its
+// operands' way from L2 (about 45 bytes a cycle and SM, 40 beside a running
+// epilogue) or its share of the ring's round trip, whichever is longest. Wide
+// tiles pay least for their weights' way there: two sets win only where the
+// epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 120 us on
+// one set, 101 us on two; 4096 x 11008 at 2048 tokens: 114 us and 126 us), one
+// accumulator only where tiles are fewer than pairs.
 Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
 {
-    const int64_t n_p = (N + (mats == 2 ? 255 : 511)) / (mats == 2 ? 256 : 512);
     const int64_t nk = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
     Plan p = {};
     double least = -1;
-    for (int bufs = 1; bufs <= 2; ++bufs)
-        for (int w = 16; w <= kMaxW / bufs; w += 16) {
-            const int64_t waves = (n_p * ((T + w - 1) / w) + pairs - 1) / pairs;
-            const double bytes = 2 * (kABytes + 1024.0) + w / 2 * 128 + (w > 128 ? 2048 : 1024);
-            const double products = nk * std::max(4.0 * w, bytes / (bufs == 1 ? 45 : 40)), epilogue = 800 + kEpilogueCycles[kind] * w;
-            const double cost = bufs == 1 ? waves * (products + epilogue)
-                                          : (waves - 1) * std::max(products, epilogue) + products + epilogue;
-            if (least < 0 || cost < least) least = cost, p.w = w, p.bufs = bufs;
-            if (w >= T) break;
-        }
+    for (int accs = mats; accs <= 2; ++accs)
+        for (int bufs = 1; bufs <= 2; ++bufs)
+            for (int w = 16; w <= kMaxW; w += 16) {
+                if (accs * w * bufs > 2 * kMaxW) break;
+                const int64_t rows = mats == 2 ? 256 : 256 * accs;
+                const int64_t waves = ((N + rows - 1) / rows * ((T + w - 1) / w) + pairs - 1) / pairs;
+                const double bytes = stage_bytes(accs, w);
+                const int ring = std::min<int>(kMaxStages, (kMaxSmem - fixed_smem(mats)) / stage_bytes(accs, w));
+                const double stage = std::max({2.0 * accs * w, bytes / (bufs == 1 ? 45 : 40), 4000.0 / ring});
+                const double products = nk * stage, epilogue = 800 + kEpilogueCycles[kind] * w * accs / 2;
+                const double cost = bufs == 1 ? waves * (products + epilogue)
+                                              : (waves - 1) * std::max(products, epilogue) + products + epilogue;
+                if (least < 0 || cost < least) least = cost, p.w = w, p.bufs = bufs, p.accs = accs, p.ring = ring;
+                if (w >= T) break;
+            }
     p.pad = p.w > 128 ? 256 : 128;
     return p;
 }
@@ -537,15 +558,18 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
     if (e != cudaSuccess) return e;
 
     const auto kernel = gated ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
-    const int smem = 1024 + kStages * kStageBytes + kEpiWarps * c.mats * kTurnFloats * 4 + sizeof(Smem);
+    // the largest a launch may ask for, so that no second CTA shares the SM: each allocates all of its tensor memory
+    const int smem = kMaxSmem;
     e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     Args g = {};
     g.nk = static_cast<int>((c.M + 255) / 256);
     g.w = pl.w;
     g.bufs = pl.bufs;
-    g.sf_bufs = std::min<int>(kStages, (kTmemCols - 2 * pl.w * pl.bufs) / sf_cols(pl.w));
-    g.row_step = gated ? 256 : 512;
+    g.accs = pl.accs;
+    g.ring = pl.ring;
+    g.sf_bufs = std::min<int>({kMaxSfBufs, pl.ring, static_cast<int>((kTmemCols - pl.accs * pl.w * pl.bufs) / sf_cols(pl.w))});
+    g.row_step = gated ? 256 : 256 * pl.accs;
     g.row_off = gated ? 0 : 256;
     g.n_p = static_cast<int>((c.N + g.row_step - 1) / g.row_step);
     g.tiles = static_cast<int>(g.n_p * ((c.T + pl.w - 1) / pl.w));
