@@ -23,10 +23,12 @@ dbf_status check_matrix(const void *values, dbf_dtype d, const uint8_t *codes, c
 }
 
 bool layer_shape_ok(const dbf_mx4_layer *L) { return L && L->M > 0 && L->N > 0; }
-// tiles of at least 16 tokens and 256 rows are counted in 32 bits
+// tiles of at least 16 tokens and 256 rows are counted in 32 bits, and rows
+// past the last one of a tile still have 32-bit numbers
+constexpr int64_t kMost = (int64_t{1} << 31) - 4096;
 bool tokens_ok(const dbf_mx4_layer *L, int64_t T)
 {
-    return T >= 0 && T < (int64_t{1} << 31) - 4096 && ((L->N + 255) / 256) * ((T + 15) / 16) < (int64_t{1} << 31) &&
+    return T >= 0 && T < kMost && L->N < kMost && (int64_t{L->N} + 255) / 256 * ((T + 15) / 16) < (int64_t{1} << 31) &&
            mx_size_ok(L->N, L->M);
 }
 
@@ -34,7 +36,7 @@ bool tokens_ok(const dbf_mx4_layer *L, int64_t T)
 // columns, rows of W, are 65535 * 256 at most
 bool gradient_ok(const dbf_mx4_layer *L, int64_t T)
 {
-    return T >= 0 && 3 * T < (int64_t{1} << 31) - 4096 && ((L->M + 255) / 256) * ((T + 31) / 32) < (int64_t{1} << 31) &&
+    return T >= 0 && 3 * T < kMost && (int64_t{L->M} + 255) / 256 * ((T + 31) / 32) < (int64_t{1} << 31) &&
            mx_size_ok(L->N, L->M) && L->N <= 65535 * 256;
 }
 

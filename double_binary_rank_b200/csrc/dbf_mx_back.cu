@@ -27,8 +27,7 @@
 // Where the tiles are fewer than the pairs, the contraction is cut into parts
 // whose fp32 sums a second launch adds in order.
 #include <algorithm>
-#include <map>
-#include <mutex>
+#include <atomic>
 
 #include "dbf_mx_layer.cuh"
 #include "dbf_tc.cuh"
@@ -45,9 +44,7 @@ constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
 constexpr int kAhead = 4;                           // stages that the expansion's loads run ahead
 constexpr int kRowsK = 64;                          // rows of W per stage
 constexpr uint32_t kABytes = 128 * kRowsK * 2;
-// A stage is this CTA's half of W's columns and w / 2 token rows. From the last
-// MMA on a stage to the next one's data it takes about 2.2 us, so a ring of n
-// stages gives one every 2.2 / n us at best: as many as fit.
+// A stage is this CTA's half of W's columns and w / 2 token rows; as many as fit.
 __host__ __device__ constexpr uint32_t stage_bytes(int w) { return kABytes + w / 2 * kRowsK * 2; }
 constexpr int kMaxSmem = 227 * 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -540,30 +537,31 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
     }
 }
 
+// CTA pairs that can be resident at once (kept per device)
 int resident_pairs(cudaLaunchConfig_t cfg)
 {
-    static std::mutex lock;
-    static std::map<int, int> known;
+    static std::atomic<int> known[kMaxDevices];
     int dev = 0;
-    cudaGetDevice(&dev);
-    std::lock_guard<std::mutex> guard(lock);
-    auto it = known.find(dev);
-    if (it == known.end()) {
-        const int pairs = std::max(1, device_sms() / 2);
+    const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+    int pairs = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (pairs == 0) {
+        pairs = std::max(1, device_sms() / 2);
         cfg.gridDim = dim3(2 * pairs);
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, mx_back_kernel, &cfg);
+        if (cudaOccupancyMaxActiveClusters(&n, mx_back_kernel, &cfg) == cudaSuccess && n > 0) pairs = std::min(n, pairs);
         (void)cudaGetLastError();
-        it = known.emplace(dev, e == cudaSuccess && n > 0 ? std::min(n, pairs) : pairs).first;
+        if (keep) known[dev].store(pairs, std::memory_order_relaxed);
     }
-    return it->second;
+    return pairs;
 }
 
 // Tokens per tile (a multiple of 32 up to 512) and parts of the contraction.
 // Cost of the last pair to finish, in cycles: waves of tiles, each so many
-// stages, a stage taking its eight MMAs (2 w), the expansion of W (the same at
-// every width) or its share of the ring's round trip, and an epilogue; the
-// parts' sums are written and read once more.
+// stages, a stage taking its eight MMAs (2 w) or, as measured for narrow tiles,
+// 1050 (the expansion's instructions and the hand-over between the roles, the
+// same at every width), and an epilogue; the parts' sums are written and read
+// once more. 4096 -> 11008 at 1024 tokens: 102 us in tiles of 256, 72 us in two
+// parts of tiles of 512.
 constexpr int64_t kMaxSplits = 16;
 struct Plan {
     int w, splits;
@@ -580,8 +578,7 @@ Plan plan(int64_t M, int64_t T, int64_t nk)
             const double waves = static_cast<double>((tiles * splits + pairs - 1) / pairs);
             const double stages = static_cast<double>((nk + splits - 1) / splits);
             const double join = splits > 1 ? 4000.0 + 8.0 * T * M * (splits + 1) / 3500.0 : 0.0;   // a launch, and bytes at 3.5 KB a cycle
-            const double ring = std::min(10.0, 220.0 * 1024 / stage_bytes(w));
-            const double cost = waves * (stages * std::max({2.0 * w, 450.0, 4000.0 / ring}) + 3000 + 12.0 * w) + join;
+            const double cost = waves * (stages * std::max(2.0 * w, 1050.0) + 3000 + 12.0 * w) + join;
             if (least < 0 || cost < least) least = cost, best = {w, splits};
         }
         if (w >= T) break;

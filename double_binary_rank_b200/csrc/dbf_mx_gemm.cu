@@ -28,8 +28,7 @@
 // than scales need to get there, have up to four buffers. Every wait is bounded; on expiry the status
 // word is set.
 #include <algorithm>
-#include <map>
-#include <mutex>
+#include <atomic>
 
 #include "dbf_mx_layer.cuh"
 #include "dbf_tc.cuh"
@@ -407,23 +406,24 @@ __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict_
     griddep_launch();
 }
 
-int resident_pairs(const void *kernel, cudaLaunchConfig_t cfg)
+// CTA pairs that can be resident at once (the query is slow next to a launch:
+// kept per device).
+template <bool kGated>
+int resident_pairs(cudaLaunchConfig_t cfg)
 {
-    static std::mutex lock;
-    static std::map<std::pair<int, const void *>, int> known;
+    static std::atomic<int> known[kMaxDevices];
     int dev = 0;
-    cudaGetDevice(&dev);
-    std::lock_guard<std::mutex> guard(lock);
-    auto it = known.find({dev, kernel});
-    if (it == known.end()) {
-        const int pairs = std::max(1, device_sms() / 2);
+    const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+    int pairs = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (pairs == 0) {
+        pairs = std::max(1, device_sms() / 2);
         cfg.gridDim = dim3(2 * pairs);
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<kGated>, &cfg) == cudaSuccess && n > 0) pairs = std::min(n, pairs);
         (void)cudaGetLastError();
-        it = known.emplace(std::make_pair(dev, kernel), e == cudaSuccess && n > 0 ? std::min(n, pairs) : pairs).first;
+        if (keep) known[dev].store(pairs, std::memory_order_relaxed);
     }
-    return it->second;
+    return pairs;
 }
 
 // What an epilogue costs per token of a tile, in cycles: plain bf16 rows, the
@@ -581,7 +581,7 @@ cudaError_t mx_gemm(const Product &c, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr + 1;
     cfg.numAttrs = 1;
-    const int pairs = std::min(resident_pairs(reinterpret_cast<const void *>(kernel), cfg), g.tiles);
+    const int pairs = std::min(gated ? resident_pairs<true>(cfg) : resident_pairs<false>(cfg), g.tiles);
     cfg.gridDim = dim3(2 * pairs);
     cfg.attrs = attr;
     cfg.numAttrs = 2;

@@ -7,6 +7,8 @@
 namespace dbf {
 namespace mx {
 
+constexpr int kMaxDevices = 64;
+
 // Outputs of one product call. Plain: y = [acc] y + W q(x). Gated: g and u
 // are the two products plus the optional addends, y = act(g) u, and g and u
 // are kept in 8 bits where g8 is set.

@@ -133,3 +133,15 @@ def test_python_refuses_host_tensors(dbf):
         dbf.mx4_forward(layer, x)
     with pytest.raises(ValueError):   # codes of another width
         dbf.Mx4Layer(128, 64, codes, scales)
+
+
+def test_sizes_that_32_bits_cannot_count(dbf, lib):
+    by = ctypes.byref
+    big = 2 ** 31 - 1
+    L = dbf.DbfMx4LayerC(32, big, P, P)
+    assert lib.dbf_mx4_workspace_bytes(by(L), 1) == 0
+    assert lib.dbf_mx4_forward(by(L), P, dbf.F32, P, dbf.F32, 1, 0, P, 1 << 40, None) == dbf.ERR_UNSUPPORTED
+    assert lib.dbf_mx4_backward(by(L), P, dbf.F32, P, dbf.F32, 1, 0, P, 1 << 40, None) == dbf.ERR_UNSUPPORTED
+    L = dbf.DbfMx4LayerC(32, 64, P, P)
+    assert lib.dbf_mx4_forward(by(L), P, dbf.F32, P, dbf.F32, big, 0, P, 1 << 62, None) == dbf.ERR_UNSUPPORTED
+    assert lib.dbf_mx4_backward(by(L), P, dbf.F32, P, dbf.F32, big // 3, 0, P, 1 << 62, None) == dbf.ERR_UNSUPPORTED
