@@ -324,9 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                         tc_fence_after();
                         return ok;
                     };
-                    const bool ok = add ? (save ? gated_tile<true, true>(g, own, lanes, t, n, half * 16, ready)
-                                                : gated_tile<true, false>(g, own, lanes, t, n, half * 16, ready))
-                                        : gated_tile<false, true>(g, own, lanes, t, n, half * 16, ready);
+                    const int64_t t16 = t - (lane >> 2) + (lane >> 1);
+                    const int n16 = n - (lane & 3) * 8 + (lane & 1) * 16;
+                    const bool ok = add ? (save ? gated_tile<true, true>(g, own, lanes, t16, n16, half * 16, ready)
+                                                : gated_tile<true, false>(g, own, lanes, t16, n16, half * 16, ready))
+                                        : gated_tile<false, true>(g, own, lanes, t16, n16, half * 16, ready);
                     if (!ok) break;
                     tc_fence_before();
                     __syncwarp();
@@ -429,7 +431,7 @@ int resident_pairs(cudaLaunchConfig_t cfg)
 // What an epilogue costs per token of a tile, in cycles: plain bf16 rows, the
 // gate, addends, 8-bit copies (from 6 waves of 4096 -> 11008 at 2048 tokens).
 enum Kind { kPlain, kGate, kGateAdd, kGateSave, kKinds };
-constexpr double kEpilogueCycles[kKinds] = {25, 29, 73, 98};   // plain: of two accumulators
+constexpr double kEpilogueCycles[kKinds] = {25, 29, 75, 78};   // plain: of two accumulators
 
 Kind kind_of(const Product &c)
 {
@@ -446,11 +448,11 @@ int fixed_smem(int mats) { return 1024 + kEpiWarps * mats * kTurnFloats * 4 + st
 // or two accumulators in a set. Cost of the last pair to finish, in cycles:
 // waves of tiles, each nk stages and an epilogue, which two sets hide behind the
 // next tile's stages. A stage takes its MMAs (2 w cycles an accumulator), its
-// operands' way from L2 (about 45 bytes a cycle and SM, 40 beside a running
+// operands' way from L2 (about 45 bytes a cycle and SM, 38 beside a running
 // epilogue) or its share of the ring's round trip, whichever is longest. Wide
 // tiles pay least for their weights' way there: two sets win only where the
-// epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 120 us on
-// one set, 101 us on two; 4096 x 11008 at 2048 tokens: 114 us and 126 us), one
+// epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 124 us on
+// one set, 107 us on two; 4096 x 11008 at 2048 tokens: 117 us and 131 us), one
 // accumulator only where tiles are fewer than pairs.
 Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
 {
@@ -465,7 +467,7 @@ Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
                 const int64_t waves = ((N + rows - 1) / rows * ((T + w - 1) / w) + pairs - 1) / pairs;
                 const double bytes = stage_bytes(accs, w);
                 const int ring = std::min<int>(kMaxStages, (kMaxSmem - fixed_smem(mats)) / stage_bytes(accs, w));
-                const double stage = std::max({2.0 * accs * w, bytes / (bufs == 1 ? 45 : 40), 4000.0 / ring});
+                const double stage = std::max({2.0 * accs * w, bytes / (bufs == 1 ? 45 : 38), 4000.0 / ring});
                 const double products = nk * stage, epilogue = 800 + kEpilogueCycles[kind] * w * accs / 2;
                 const double cost = bufs == 1 ? waves * (products + epilogue)
                                               : (waves - 1) * std::max(products, epilogue) + products + epilogue;

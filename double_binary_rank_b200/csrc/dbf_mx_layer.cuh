@@ -184,54 +184,99 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
 }
 
 // The same rows for the gated block with bf16 addends and 8-bit copies of g and
-// u, 16 tokens at once as two turns of 8.
+// u, 16 tokens at once, a lane sixteen columns of one token: two lanes hold a
+// block, so its scale is found once for sixteen values and the codes are one
+// 16-byte store.
 __device__ __forceinline__ bool epilogue_is_bf16(const Epilogue &e)
 {
     return epilogue_vec(e) && e.yd == DBF_BF16 && !e.g_add == !e.u_add && (!e.g_add || e.add_dt == DBF_BF16);
 }
+// t: the lane's token; c: its first column (rows hold whole vectors of eight)
 template <bool kAdd>
 __device__ __forceinline__ void gated_reads(const Epilogue &e, int64_t t, int c, bool on, uint4 (&x)[2][2])
 {
     if (!kAdd) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const bool in = on && c < e.N && t + 8 * i < e.T;
-        const int64_t at = (t + 8 * i) * e.N + c;
-        x[i][0] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.g_add) + at) : make_uint4(0u, 0u, 0u, 0u);
-        x[i][1] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.u_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+        const bool in = on && t < e.T && c + 8 * i < e.N;
+        const int64_t at = t * e.N + c + 8 * i;
+        x[0][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.g_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+        x[1][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.u_add) + at) : make_uint4(0u, 0u, 0u, 0u);
     }
+}
+// 16 tokens x 32 columns, a column per lane, to 16 columns of token lane / 2
+__device__ __forceinline__ void turn16(float *own, const float (&col)[16], float (&row)[16])
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) own[j * 36 + lane] = col[j];
+    __syncwarp();
+    const float4 *p = reinterpret_cast<const float4 *>(own + (lane >> 1) * 36 + (lane & 1) * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 a = p[j];
+        row[4 * j] = a.x, row[4 * j + 1] = a.y, row[4 * j + 2] = a.z, row[4 * j + 3] = a.w;
+    }
+}
+__device__ __forceinline__ void keep8(uint8_t *codes, uint8_t *scales, int64_t pitch, int64_t T, int64_t t, int c, bool on,
+                                      const float (&v)[16])
+{
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(v[i]));
+    uint32_t bits = __float_as_uint(m) & 0x7FFFFFFFu;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, bits, 1);
+    bits = other > bits ? other : bits;
+    const uint32_t byte = scale_byte8(bits);
+    const float inv = inv_scale(byte);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        if (byte == 255u) w[i] = 0u;
+    }
+    if (!on || c >= pitch) return;
+    *reinterpret_cast<uint4 *>(codes + t * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if ((c & 31) == 0) scales[static_cast<int64_t>(c / kBlock) * T + t] = static_cast<uint8_t>(byte);
 }
 template <bool kAdd, bool kSave>
 __device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int64_t t, int c, const float (&v)[2][16],
                                              const uint4 (&x)[2][2])
 {
+    float r[2][16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float col[2][8], row[2][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) col[0][j] = v[0][8 * i + j], col[1][j] = v[1][8 * i + j];
-        turn8<2>(own, col, row);
-        const bool on = t + 8 * i < e.T;
+    for (int m = 0; m < 2; ++m) {
+        turn16(own, v[m], r[m]);
         if (kAdd) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const Raw8 r = {x[i][m], make_uint4(0u, 0u, 0u, 0u)};
-                add_raw8(r, DBF_BF16, true, row[m]);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t a[4] = {x[m][i].x, x[m][i].y, x[m][i].z, x[m][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[m][8 * i + 2 * j] += __uint_as_float(a[j] << 16);
+                    r[m][8 * i + 2 * j + 1] += __uint_as_float(a[j] & 0xFFFF0000u);
+                }
             }
         }
-        if (kSave) {
-            if (c >= e.N) {   // rows past the last may have given anything, a NaN too
+    }
+    const bool on = t < e.T;
+    if (kSave) {
+        if (c + 16 > e.N) {   // rows past the last may have given anything, a NaN too
 #pragma unroll
-                for (int j = 0; j < 8; ++j) row[0][j] = row[1][j] = 0.0f;
-            }
-            keep8(e.g8, e.gs, e.pitch8, e.T, t + 8 * i, c, on, row[0]);
-            keep8(e.u8, e.us, e.pitch8, e.T, t + 8 * i, c, on, row[1]);
+            for (int j = 0; j < 16; ++j)
+                if (c + j >= e.N) r[0][j] = r[1][j] = 0.0f;
         }
-        if (on) {
+        keep8(e.g8, e.gs, e.pitch8, e.T, t, c, on, r[0]);
+        keep8(e.u8, e.us, e.pitch8, e.T, t, c, on, r[1]);
+    }
+    if (!on) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) row[0][j] = gate_value(e.act, row[0][j]) * row[1][j];
-            store8(e.y, DBF_BF16, (t + 8 * i) * e.N, c, e.N, true, row[0]);
-        }
+    for (int i = 0; i < 2; ++i) {
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = gate_value(e.act, r[0][8 * i + j]) * r[1][8 * i + j];
+        store8(e.y, DBF_BF16, t * e.N, c + 8 * i, e.N, true, h);
     }
 }
 
