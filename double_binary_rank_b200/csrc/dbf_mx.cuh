@@ -278,54 +278,126 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t m)
     return b > m ? b : m;
 }
 
-// fp32 bits of the largest magnitude of the block that this lane and its three
-// neighbours hold. 16-bit values are compared two at a time, as integers.
-__device__ __forceinline__ uint32_t block_amax_raw(const Raw8 &r, dbf_dtype dt, bool vec)
+// How many values of one row a lane takes: sixteen of a 16-bit type in aligned
+// vectors, else eight. The quantisers run out of integer instructions before
+// anything else, and with sixteen the block's scale and its exchange between
+// lanes cost half as many per value.
+template <dbf_dtype DT, bool kVec>
+constexpr int lane_cols() { return DT != DBF_F32 && kVec ? 16 : 8; }
+
+// Columns c .. c + kCols - 1 of a row as loaded.
+template <dbf_dtype DT, bool kVec, int kCols>
+__device__ __forceinline__ void load_cols(const void *src, int64_t row_start, int64_t c, int64_t k, Raw8 (&r)[kCols / 8])
 {
-    if (dt == DBF_F32 || !vec) {
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i) r[i] = load_raw8(src, DT, row_start, c + 8 * i, k, kVec);
+}
+
+// Larger magnitudes of two pairs of 16-bit values; NaN wins.
+template <dbf_dtype DT>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if (DT == DBF_BF16)
+        asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// fp32 bits of the largest magnitude of the block that this lane and its
+// neighbours (32 / kCols lanes) hold.
+template <dbf_dtype DT, bool kVec, int kCols>
+__device__ __forceinline__ uint32_t block_amax_bits(const Raw8 (&r)[kCols / 8])
+{
+    if (DT == DBF_F32 || !kVec) {
         float v[8];
-        raw8_values(r, DBF_F32, true, v);
+        raw8_values(r[0], DBF_F32, true, v);
         return block_amax(amax_bits8(v));
     }
-    uint32_t m = __vmaxu2(__vmaxu2(r.lo.x & 0x7FFF7FFFu, r.lo.y & 0x7FFF7FFFu), __vmaxu2(r.lo.z & 0x7FFF7FFFu, r.lo.w & 0x7FFF7FFFu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t hi = m >> 16, lo = m & 0xFFFFu;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i) {
+        const uint32_t a = max_abs2<DT>(max_abs2<DT>(r[i].lo.x, r[i].lo.y), max_abs2<DT>(r[i].lo.z, r[i].lo.w));
+        m = i ? max_abs2<DT>(m, a) : a;
+    }
+#pragma unroll
+    for (int d = 1; d < 32 / kCols; d *= 2) m = max_abs2<DT>(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const uint32_t hi = m >> 16, lo = m & 0xFFFFu;   // as integers, NaN > infinity > finite
     const uint32_t top = hi > lo ? hi : lo;
-    return dt == DBF_BF16 ? top << 16 : __float_as_uint(h2f(static_cast<uint16_t>(top)));
+    return DT == DBF_BF16 ? top << 16 : __float_as_uint(h2f(static_cast<uint16_t>(top)));
 }
 
-// A lane's eight values to codes; four neighbouring lanes hold one block.
-// Returns the code word and the block's scale byte.
-__device__ __forceinline__ uint32_t quantize8_e2m1(const Raw8 &r, dbf_dtype dt, bool vec, uint32_t &byte)
+// Eight values times 2^-s of a scale byte, exact (bf16 in pairs: results below
+// its normal range round to the code 0 in any case).
+template <dbf_dtype DT, bool kVec>
+__device__ __forceinline__ void scaled_values(const Raw8 &r, uint32_t byte, float (&v)[8])
 {
-    byte = scale_byte4(block_amax_raw(r, dt, vec));
+    if (DT == DBF_BF16 && kVec) {
+        const uint32_t f = byte == 255u ? 0u : (254u - byte) << 7, f2 = f | f << 16;
+        const uint32_t a[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(a[i]), "r"(f2));
+            v[2 * i] = __uint_as_float(p << 16);
+            v[2 * i + 1] = __uint_as_float(p & 0xFFFF0000u);
+        }
+        return;
+    }
     const float inv = inv_scale(byte);
-    float v[8];
-    raw8_values(r, dt, vec, v);
+    raw8_values(r, DT, kVec, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
-    const uint32_t w = e2m1x8(v);
-    return byte == 255u ? 0u : w;
-}
-__device__ __forceinline__ uint2 quantize8_e4m3(const Raw8 &r, dbf_dtype dt, bool vec, uint32_t &byte)
-{
-    byte = scale_byte8(block_amax_raw(r, dt, vec));
-    const float inv = inv_scale(byte);
-    float v[8];
-    raw8_values(r, dt, vec, v);
-    const uint2 w = make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                               e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    return byte == 255u ? make_uint2(0u, 0u) : w;
 }
 
-// The scale bytes of the four blocks that a half-warp holds, as one word
-// (the same in every lane of the half).
-__device__ __forceinline__ uint32_t half_warp_scales(uint32_t byte, int lane)
+// A lane's values to codes (eight to a word, or four); its neighbours hold the
+// rest of the block. Sets the block's scale byte.
+template <dbf_dtype DT, bool kVec, int kCols>
+__device__ __forceinline__ void quantize_e2m1(const Raw8 (&r)[kCols / 8], uint32_t &byte, uint32_t (&w)[kCols / 8])
 {
-    uint32_t w = byte << (lane * 2 & 24);   // 8 * (lane / 4 % 4)
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
-    return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
+    byte = scale_byte4(block_amax_bits<DT, kVec, kCols>(r));
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i) {
+        float v[8];
+        scaled_values<DT, kVec>(r[i], byte, v);
+        w[i] = byte == 255u ? 0u : e2m1x8(v);
+    }
+}
+template <dbf_dtype DT, bool kVec, int kCols>
+__device__ __forceinline__ void quantize_e4m3(const Raw8 (&r)[kCols / 8], uint32_t &byte, uint32_t (&w)[kCols / 4])
+{
+    byte = scale_byte8(block_amax_bits<DT, kVec, kCols>(r));
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i) {
+        float v[8];
+        scaled_values<DT, kVec>(r[i], byte, v);
+        w[2 * i] = byte == 255u ? 0u : e4m3x4(v[0], v[1], v[2], v[3]);
+        w[2 * i + 1] = byte == 255u ? 0u : e4m3x4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// kWords neighbouring words, aligned
+template <int kWords>
+__device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&w)[kWords])
+{
+    if constexpr (kWords == 1)
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+    else if constexpr (kWords == 2)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The scale bytes of the four blocks of 128 columns as one word, the same in
+// every one of the 128 / kCols lanes that hold them.
+template <int kCols>
+__device__ __forceinline__ uint32_t tile_scales(uint32_t byte, int lane)
+{
+    constexpr int kLanes = 32 / kCols;
+    uint32_t w = byte << (lane / kLanes * 8 & 24);
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, kLanes);
+    return w | __shfl_xor_sync(0xFFFFFFFFu, w, 2 * kLanes);
 }
 
 }  // namespace mx

@@ -174,11 +174,15 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
                 const int u = u0 + i * kWorkers;
                 if (u >= g.T * nks) break;
                 const int t = u / nks, ks = u - t * nks;
-                uint32_t byte;
-                const uint32_t q = quantize8_e2m1(in[i], g.xd, g.vec, byte);
-                const uint32_t word = half_warp_scales(byte, lane);
+                uint32_t byte, q[1];
+                const Raw8 r[1] = {in[i]};
+                if (g.xd == DBF_BF16 && g.vec)
+                    quantize_e2m1<DBF_BF16, true, 8>(r, byte, q);
+                else   // fp32 values, loaded as they are or one by one
+                    quantize_e2m1<DBF_F32, true, 8>(r, byte, q);
+                const uint32_t word = tile_scales<8>(byte, lane);
                 uint8_t *xs = xq + ks * x_stage;
-                *reinterpret_cast<uint32_t *>(xs + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = q;
+                *reinterpret_cast<uint32_t *>(xs + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = q[0];
                 if ((lane & 15) == 0)
                     *reinterpret_cast<uint32_t *>(xs + g.w * 128 + (lane >> 4) * 512 + (t & 31) * 16 + (t >> 5) * 4) = word;
             }

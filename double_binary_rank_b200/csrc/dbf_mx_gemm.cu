@@ -383,23 +383,24 @@ __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict_
 {
     griddep_wait();   // the workspace may still be read by the call before
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+    constexpr int kCols = lane_cols<DT, kVec>();
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kCols;
     const int64_t nb = blocks(M), pitch = nb * 16, tiles = scale_tiles(M);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + warp;
     const int left = static_cast<int>(T - row < 32 ? T - row : 32);   // row + 8 i exists where 8 i < left
-    Raw8 in[4];
+    Raw8 in[4][kCols / 8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = load_raw8(x, DT, (row + 8 * i) * M, 8 * i < left ? c : M, M, kVec);
+    for (int i = 0; i < 4; ++i) load_cols<DT, kVec, kCols>(x, (row + 8 * i) * M, 8 * i < left ? c : M, M, in[i]);
     uint8_t *out = codes + row * pitch + c / 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i, out += 8 * pitch) {
         const int r = static_cast<int>(row) + 8 * i;
-        uint32_t byte;
-        const uint32_t q = quantize8_e2m1(in[i], DT, kVec, byte);
-        const uint32_t word = half_warp_scales(byte, lane);
+        uint32_t byte, q[kCols / 8];
+        quantize_e2m1<DT, kVec, kCols>(in[i], byte, q);
+        const uint32_t word = tile_scales<kCols>(byte, lane);
         if (8 * i >= left) continue;
-        if (c < nb * kBlock) *reinterpret_cast<uint32_t *>(out) = q;
-        if ((lane & 15) == 0 && (c >> 7) < tiles)
+        if (c < nb * kBlock) store_words(out, q);
+        if (lane % (128 / kCols) == 0 && (c >> 7) < tiles)
             *reinterpret_cast<uint32_t *>(scales + scale_at(r / w * pad + r % w, c >> 5, tiles)) = word;
     }
     // Only now: the product's CTAs would take the registers of this kernel's
@@ -523,12 +524,13 @@ cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + 255) / 256));
+    const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+    const int cols = 32 * (vec && c.xd == DBF_BF16 ? lane_cols<DBF_BF16, true>() : lane_cols<DBF_F32, true>());
+    cfg.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + cols - 1) / cols));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
     const auto kernel = c.xd == DBF_F32 ? (vec ? quantize_x_kernel<DBF_F32, true> : quantize_x_kernel<DBF_F32, false>)
                                         : (vec ? quantize_x_kernel<DBF_BF16, true> : quantize_x_kernel<DBF_BF16, false>);
     return cudaLaunchKernelEx(&cfg, kernel, c.x, c.T, c.M, w, pad, codes, scales);

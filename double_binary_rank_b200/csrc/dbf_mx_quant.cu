@@ -2,10 +2,9 @@
 // activation to 8-bit codes and scales and back (dbf_mx.cuh has the formats).
 //
 // Each kernel reads every input and writes every output once and computes
-// little, so device memory bounds it. A warp takes 256 columns (a lane eight
-// of them: one 16-byte load of 16-bit values; four lanes a block, whose
-// largest magnitude two shuffles find) of four rows, whose loads are all in
-// flight before the first is used. The four rows of a 4-bit warp are 32
+// little, so device memory should bound it. A warp takes 256 columns (a lane
+// eight of them, four lanes a block) of four rows, whose loads are all in flight
+// before the first is used; the quantisers of 16-bit types 512, a lane sixteen. The four rows of a 4-bit warp are 32
 // apart: their scales are neighbours in the tiled layout, so a warp writes
 // them as 16-byte vectors. The 8-bit scales lie block by block ([block][row]),
 // the order in which the gated block's epilogue produces them; a CTA gathers
@@ -23,10 +22,11 @@ constexpr int kRowsPerWarp = 4;
 constexpr int kWarps = 8;
 constexpr int kSegment = 256;   // columns of a warp
 
-// kVec: rows are whole aligned vectors of eight values. Instruction issue is
-// what these kernels run into first (11008 x 4096 bf16: 447 instructions a warp
-// and 30 us, against 17 us for the bytes), hence the packed comparisons, the
-// compile-time types and the running pointers.
+// kVec: rows are whole aligned vectors of eight values. Integer instructions are
+// what the quantisers run into first (11008 x 4096 bf16, 17 us for the bytes: 30
+// us with eight values to a lane, run-time types and a conversion each; 25 us
+// with packed comparisons and compile-time types, the ALU pipe 82 % busy; 23 us
+// as it stands).
 template <dbf_dtype DT, bool kVec>
 __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__restrict__ src, int64_t rows, int64_t k,
                                                                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
@@ -37,26 +37,28 @@ __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__re
     // four groups of 32
     const int64_t tile = blockIdx.x / (32 / kWarps);
     const int r32 = static_cast<int>(blockIdx.x % (32 / kWarps)) * kWarps + warp;
-    const int64_t row = tile * 128 + r32, c = static_cast<int64_t>(blockIdx.y) * kSegment + lane * 8;
+    constexpr int kCols = lane_cols<DT, kVec>();
+    const int64_t row = tile * 128 + r32, c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kCols;
     const int64_t nb = blocks(k), pitch = nb * 16, tiles = scale_tiles(k);
     const int left = static_cast<int>(rows - row < 128 ? rows - row : 128);   // row + 32 g exists where 32 g < left
-    Raw8 x[kRowsPerWarp];
+    Raw8 x[kRowsPerWarp][kCols / 8];
 #pragma unroll
-    for (int g = 0; g < kRowsPerWarp; ++g) x[g] = load_raw8(src, DT, (row + 32 * g) * k, 32 * g < left ? c : k, k, kVec);
+    for (int g = 0; g < kRowsPerWarp; ++g)
+        load_cols<DT, kVec, kCols>(src, (row + 32 * g) * k, 32 * g < left ? c : k, k, x[g]);
     uint32_t words[kRowsPerWarp];
     bool bad = false;
     uint8_t *out = codes + row * pitch + c / 2;
     const bool in = c < nb * kBlock;
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g, out += 32 * pitch) {
-        uint32_t byte;
-        const uint32_t w = quantize8_e2m1(x[g], DT, kVec, byte);
+        uint32_t byte, w[kCols / 8];
+        quantize_e2m1<DT, kVec, kCols>(x[g], byte, w);
         bad |= byte == 255u;
-        if (in && 32 * g < left) *reinterpret_cast<uint32_t *>(out) = w;
-        words[g] = half_warp_scales(byte, lane);
+        if (in && 32 * g < left) store_words(out, w);
+        words[g] = tile_scales<kCols>(byte, lane);
     }
-    const int64_t ct = c >> 7;   // scale tile of this half-warp; blocks and rows past the end hold scale 0
-    if ((lane & 15) == 0 && ct < tiles)
+    const int64_t ct = c >> 7;   // scale tile of these lanes; blocks and rows past the end hold scale 0
+    if (lane % (128 / kCols) == 0 && ct < tiles)
         *reinterpret_cast<uint4 *>(scales + (tile * tiles + ct) * 512 + r32 * 16) =
             make_uint4(words[0], words[1], words[2], words[3]);
     if (status && bad) atomicExch(status, static_cast<int32_t>(DBF_ERR_INVALID_ARG));
@@ -98,29 +100,34 @@ __global__ void __launch_bounds__(32 * kWarps) act8_save_kernel(const void *__re
                                                                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                                 int32_t *status)
 {
-    __shared__ uint8_t gather[kSegment / kBlock][32];
+    constexpr int kCols = lane_cols<DT, kVec>();
+    __shared__ uint8_t gather[kCols][32];   // kCols blocks: a warp's columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32, row = r0 + warp;
-    const int64_t c = static_cast<int64_t>(blockIdx.y) * kSegment + lane * 8;
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kCols;
     const int64_t nb = blocks(k), pitch = nb * kBlock;
     const int left = static_cast<int>(rows - row < 32 ? rows - row : 32);   // row + 8 g exists where 8 g < left
-    Raw8 x[kRowsPerWarp];
+    Raw8 x[kRowsPerWarp][kCols / 8];
 #pragma unroll
-    for (int g = 0; g < kRowsPerWarp; ++g) x[g] = load_raw8(src, DT, (row + kWarps * g) * k, kWarps * g < left ? c : k, k, kVec);
+    for (int g = 0; g < kRowsPerWarp; ++g)
+        load_cols<DT, kVec, kCols>(src, (row + kWarps * g) * k, kWarps * g < left ? c : k, k, x[g]);
     bool bad = false;
     uint8_t *out = codes + row * pitch + c;
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g, out += kWarps * pitch) {
-        uint32_t byte;
-        const uint2 w = quantize8_e4m3(x[g], DT, kVec, byte);
+        uint32_t byte, w[kCols / 4];
+        quantize_e4m3<DT, kVec, kCols>(x[g], byte, w);
         bad |= byte == 255u;
-        if (kWarps * g < left && c < pitch) *reinterpret_cast<uint2 *>(out) = w;
-        if ((lane & 3) == 0) gather[lane >> 2][g * kWarps + warp] = static_cast<uint8_t>(byte);
+        if (kWarps * g < left && c < pitch) store_words(out, w);
+        if (lane % (32 / kCols) == 0) gather[lane * kCols / 32][g * kWarps + warp] = static_cast<uint8_t>(byte);
     }
     __syncthreads();
-    // a warp writes one block's scales of the CTA's 32 rows
-    const int64_t b = static_cast<int64_t>(blockIdx.y) * (kSegment / kBlock) + warp;
-    if (b < nb && r0 + lane < rows) scales[b * rows + r0 + lane] = gather[warp][lane];
+    // a warp writes a block's scales of the CTA's 32 rows
+#pragma unroll
+    for (int i = 0; i < kCols / kWarps; ++i) {
+        const int64_t b = static_cast<int64_t>(blockIdx.y) * kCols + i * kWarps + warp;
+        if (b < nb && r0 + lane < rows) scales[b * rows + r0 + lane] = gather[i * kWarps + warp][lane];
+    }
     if (status && bad) atomicExch(status, static_cast<int32_t>(DBF_ERR_INVALID_ARG));
 }
 
@@ -156,13 +163,14 @@ __global__ void __launch_bounds__(32 * kWarps) act8_load_kernel(const uint8_t *_
     }
 }
 
-dim3 grid4(int64_t rows, int64_t k)
+// cols: columns of a warp
+dim3 grid4(int64_t rows, int64_t k, int cols)
 {
-    return dim3(static_cast<unsigned>((rows + 127) / 128 * (32 / kWarps)), static_cast<unsigned>((k + kSegment - 1) / kSegment));
+    return dim3(static_cast<unsigned>((rows + 127) / 128 * (32 / kWarps)), static_cast<unsigned>((k + cols - 1) / cols));
 }
-dim3 grid8(int64_t rows, int64_t k)
+dim3 grid8(int64_t rows, int64_t k, int cols)
 {
-    return dim3(static_cast<unsigned>((rows + 31) / 32), static_cast<unsigned>((k + kSegment - 1) / kSegment));
+    return dim3(static_cast<unsigned>((rows + 31) / 32), static_cast<unsigned>((k + cols - 1) / cols));
 }
 
 template <class F>
@@ -192,9 +200,9 @@ bool mx_size_ok(int64_t rows, int64_t k)
 cudaError_t launch_quantize4(const void *src, dbf_dtype dt, int64_t rows, int64_t k, uint8_t *codes, uint8_t *scales,
                              int32_t *status, cudaStream_t s)
 {
-    const dim3 g = grid4(rows, k);
     by_type(dt, vectors(src, k), [&](auto type, auto vec) {
-        quantize4_kernel<decltype(type)::value, decltype(vec)::value><<<g, 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
+        quantize4_kernel<decltype(type)::value, decltype(vec)::value>
+            <<<grid4(rows, k, 32 * lane_cols<decltype(type)::value, decltype(vec)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
     });
     return cudaGetLastError();
 }
@@ -202,7 +210,7 @@ cudaError_t launch_quantize4(const void *src, dbf_dtype dt, int64_t rows, int64_
 cudaError_t launch_dequantize4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
                                dbf_dtype dt, cudaStream_t s)
 {
-    const dim3 g = grid4(rows, k);
+    const dim3 g = grid4(rows, k, kSegment);
     by_type(dt, vectors(dst, k), [&](auto type, auto vec) {
         dequantize4_kernel<decltype(type)::value, decltype(vec)::value><<<g, 32 * kWarps, 0, s>>>(codes, scales, rows, k, dst);
     });
@@ -212,9 +220,9 @@ cudaError_t launch_dequantize4(const uint8_t *codes, const uint8_t *scales, int6
 cudaError_t launch_act8_save(const void *src, dbf_dtype dt, int64_t rows, int64_t k, uint8_t *codes, uint8_t *scales,
                              int32_t *status, cudaStream_t s)
 {
-    const dim3 g = grid8(rows, k);
     by_type(dt, vectors(src, k), [&](auto type, auto vec) {
-        act8_save_kernel<decltype(type)::value, decltype(vec)::value><<<g, 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
+        act8_save_kernel<decltype(type)::value, decltype(vec)::value>
+            <<<grid8(rows, k, 32 * lane_cols<decltype(type)::value, decltype(vec)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
     });
     return cudaGetLastError();
 }
@@ -222,7 +230,7 @@ cudaError_t launch_act8_save(const void *src, dbf_dtype dt, int64_t rows, int64_
 cudaError_t launch_act8_load(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, void *dst,
                              dbf_dtype dt, cudaStream_t s)
 {
-    const dim3 g = grid8(rows, k);
+    const dim3 g = grid8(rows, k, kSegment);
     by_type(dt, vectors(dst, k), [&](auto type, auto vec) {
         act8_load_kernel<decltype(type)::value, decltype(vec)::value><<<g, 32 * kWarps, 0, s>>>(codes, scales, rows, k, dst);
     });
