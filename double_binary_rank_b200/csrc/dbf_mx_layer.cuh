@@ -144,20 +144,30 @@ __device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], 
     }
 }
 
-// The epilogue where nothing but the products is read and the output is bf16
-// with rows of whole 16-byte vectors: 16 tokens at once are finished as they
-// come, a column of 16 tokens per lane, and turned as pairs of tokens in one
-// word: a third of the instructions of the general one, whose issue bounds the
-// prefill kernel's epilogue.
+// The epilogue where nothing but the products is read and the output is fp32, or
+// bf16 with rows of whole 16-byte vectors: 16 tokens at once are finished as they
+// come, a column of 16 tokens per lane. fp32 is stored so (a warp's lanes are 128
+// bytes of a row); bf16 is turned as pairs of tokens in one word: a third of the
+// instructions of the general one, whose issue bounds the prefill kernel's
+// epilogue.
 __device__ __forceinline__ bool epilogue_is_simple(const Epilogue &e)
 {
-    return epilogue_vec(e) && e.yd == DBF_BF16 && !e.accumulate && !e.g_add && !e.u_add && !e.g8;
+    return (e.yd == DBF_F32 || epilogue_vec(e)) && !e.accumulate && !e.g_add && !e.u_add && !e.g8;
 }
 // n0: the warp's first column; own: kTurnFloats words
 template <int kMats>
 __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, int64_t t0, int n0, const float (&v)[kMats][16])
 {
     const int lane = threadIdx.x & 31;
+    if (e.yd == DBF_F32) {
+        const int n = n0 + lane;
+        const int left = static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16);
+        float *y = static_cast<float *>(e.y) + t0 * e.N + n;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < left && n < e.N) y[j * static_cast<int64_t>(e.N)] = kMats == 2 ? gate_value(e.act, v[0][j]) * v[kMats - 1][j] : v[0][j];
+        return;
+    }
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
