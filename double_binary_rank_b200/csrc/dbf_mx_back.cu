@@ -12,9 +12,9 @@
 // operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
 // each (v = p0 + p1 + p2 exactly), three times the products.
 //
-// A CTA pair owns 256 columns of W x w <= 512 tokens of dx as two accumulators
-// (an expanded stage feeds two MMAs a step), contraction over the rows of W in
-// stages of 64:
+// A CTA pair owns 256 columns of W x w <= 512 tokens of dx, over 256 tokens as
+// two accumulators (an expanded stage feeds two MMAs a step), contraction over
+// the rows of W in stages of 64:
 //   warp 0       TMA: w / 2 token rows of the gradient, 64 columns each;
 //   warps 2..9   expansion: a thread takes 32 codes of one row of W (16 bytes
 //                and a scale, loaded four stages ahead) and writes them as 64
@@ -22,7 +22,7 @@
 //                the A operand in its M-major form, so nothing is transposed;
 //                a warp's lanes hold 32 different rows, whose swizzled chunks
 //                lie in different banks;
-//   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N = w / 2, K = 16);
+//   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N up to 256, K = 16);
 //   warps 10..17 epilogue.
 // Where the tiles are fewer than the pairs, the contraction is cut into parts
 // whose fp32 sums a second launch adds in order.
@@ -66,6 +66,7 @@ struct Args {
     int64_t plane_rows;  // rows from one piece to the next in the gradient's map
     int w;               // tokens per tile
     int ring;            // stages in shared memory
+    int halves;          // accumulators: 1 up to 256 tokens, else 2
     int n_p, n_c;        // tiles along the columns of W and along the tokens
     int splits;          // parts of the contraction; over 1, each writes fp32 sums [T][M] of its own
     int tiles;           // n_p * n_c * splits
@@ -89,16 +90,20 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 
-// Two codes of a word (nibbles 2i and 2i + 1) as bf16 bit patterns: sign to
-// bit 15, the three magnitude bits to the lowest exponent bits and the highest
-// mantissa bit. That pattern is the code's value times 2^-126 (0.5 becomes a
-// bf16 subnormal), so one multiplication by 2^(126 + s) gives value * 2^s.
-__device__ __forceinline__ uint32_t bf16_pattern(uint32_t w, uint32_t w_hi, int i)
+// Codes i and i + 4 of a word of eight as bf16 bit patterns: sign to bit 15, the
+// three magnitude bits to the lowest exponent bits and the highest mantissa
+// bit. That pattern is the code's value times 2^-126 (0.5 becomes a bf16
+// subnormal), so one multiplication by 2^(126 + s) gives value * 2^s. Codes four
+// apart lie 16 bits apart, so two shifts serve both; a group of eight columns
+// thus comes out in the order 0 4 1 5 2 6 3 7, which column_slot() undoes where
+// dx leaves tensor memory.
+template <int i>
+__device__ __forceinline__ uint32_t bf16_pattern(uint32_t w)
 {
-    // bytes 0 and 2: byte i of the word and of the word shifted by a nibble (the others are masked off below)
-    const uint32_t x = __byte_perm(w, w_hi, ((4u + i) << 8) | i);
-    return ((x << 6) & 0x01C001C0u) | ((x << 12) & 0x80008000u);
+    const uint32_t mag = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
+    return (mag & 0x01C001C0u) | ((w << (12 - 4 * i)) & 0x80008000u);
 }
+__device__ __forceinline__ int column_slot(int lane) { return (lane & 24) | (lane & 1) << 2 | (lane & 7) >> 1; }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
     const uint32_t stage_size = stage_bytes(g.w);
     float *turn = reinterpret_cast<float *>(stage0 + stages * stage_size);
     Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kTurnFloats);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
     const int nseg = g.mats * g.planes, nk = nseg * g.nn;
@@ -157,129 +162,139 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before either is reached from the other
     tc_fence_after();
-    const uint32_t tmem = sh->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh->tmem_base, 0);
 
     if (warp == 0) {
-        if (lane == 0) {
-            griddep_wait();   // the gradient belongs to earlier work until then
-            const int quarter_w = g.w / 4;
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int tile = unit; tile < g.tiles && ok; tile += units) {
-                const Tile c = tile_of(g, tile, nk);
-                const int tok = c.c * g.w + static_cast<int>(rank) * quarter_w;
-                int seg = c.k0 / g.nn, i = c.k0 - seg * g.nn;
-                for (int k = c.k0; k < c.k1; ++k) {
-                    if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
-                    const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
-                    uint8_t *st = stage0 + s * stage_size + kABytes;
-                    if (rank == 0) bar_expect_tx(&sh->full[s], 4 * quarter_w * kRowsK * 2);
+        griddep_wait();   // the gradient belongs to earlier work until then
+        const int rows = g.w / g.halves / 2;   // of this CTA, per accumulator
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = unit; tile < g.tiles && ok; tile += units) {
+            const Tile c = tile_of(g, tile, nk);
+            const int tok = c.c * g.w + static_cast<int>(rank) * rows;
+            int seg = c.k0 / g.nn, i = c.k0 - seg * g.nn;
+            for (int k = c.k0; k < c.k1; ++k) {
+                ok = warp_wait(&sh->empty[s], ph ^ 1u, abort);
+                if (!ok) break;
+                const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
+                const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
+                uint8_t *st = stage0 + s * stage_size + kABytes;
+                if (elect_one()) {
+                    if (rank == 0) bar_expect_tx(&sh->full[s], g.w * kRowsK * 2);
                     tma_2d_pair(st, map, i * kRowsK, row, &sh->full[s]);
-                    tma_2d_pair(st + quarter_w * kRowsK * 2, map, i * kRowsK, row + 2 * quarter_w, &sh->full[s]);
-                    ++issued;
-                    if (++s == stages) s = 0, ph ^= 1u;
-                    if (++i == g.nn) i = 0, ++seg;
+                    if (g.halves == 2) tma_2d_pair(st + rows * kRowsK * 2, map, i * kRowsK, row + 2 * rows, &sh->full[s]);
                 }
+                __syncwarp();
+                ++issued;
+                if (++s == stages) s = 0, ph ^= 1u;
+                if (++i == g.nn) i = 0, ++seg;
             }
-            if (*abort && rank == 0)
-                for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-                    drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
         }
+        if (*abort && rank == 0)
+            for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+                drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int s = 0;
             uint32_t ph = 0, acc_ph = 0;
             bool ok = true;
-            const uint32_t id = bf16_idesc(g.w / 2), second = g.w / 4 * kRowsK * 2;
+            const uint32_t id = bf16_idesc(g.w / g.halves), second = g.w / 4 * kRowsK * 2;
             for (int tile = unit; tile < g.tiles && ok; tile += units) {
                 const Tile c = tile_of(g, tile, nk);
-                ok = bar_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
+                ok = warp_wait(&sh->acc_empty, acc_ph ^ 1u, abort);
                 if (!ok) break;
-                tc_fence_after();
                 for (int k = c.k0; k < c.k1; ++k) {
-                    if (!bar_wait(&sh->full[s], ph, abort)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(&sh->full[s], ph, abort);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(stage0) + s * stage_size;
                     // A: 64 columns of W to a 128-byte row; groups of 8 rows 1 KB apart, the second
                     // 64 columns 8 KB on
                     const uint64_t a = sw128_desc(st, 1024, 8192), b0 = sw128_desc(st + kABytes), b1 = sw128_desc(st + kABytes + second);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t acc = k > c.k0 || kk > 0 ? 1u : 0u;
-                        mma_bf16_pair(tmem, a + kk * (2048 >> 4), b0 + 2 * kk, id, acc);
-                        mma_bf16_pair(tmem + 256, a + kk * (2048 >> 4), b1 + 2 * kk, id, acc);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t acc = k > c.k0 || kk > 0 ? 1u : 0u;
+                            mma_bf16_pair(tmem, a + kk * (2048 >> 4), b0 + 2 * kk, id, acc);
+                            if (g.halves == 2) mma_bf16_pair(tmem + 256, a + kk * (2048 >> 4), b1 + 2 * kk, id, acc);
+                        }
+                        commit_pair_both(&sh->empty[s]);
                     }
-                    commit_pair_both(&sh->empty[s]);
+                    __syncwarp();
                     if (++s == stages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
-                commit_pair_both(&sh->acc_full);
+                if (elect_one()) commit_pair_both(&sh->acc_full);
+                __syncwarp();
                 acc_ph ^= 1u;
             }
             if (*abort) {
-                commit_pair_own(&sh->drain);
+                if (elect_one()) commit_pair_own(&sh->drain);
+                __syncwarp();
                 drain_wait(&sh->drain, 0);
             }
         }
     } else if (warp < 2 + kExpand) {
         if (!g.early) griddep_wait();
         const int e = warp - 2, q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
-        uint8_t *dst = stage0 + (q >> 1) * 8192 + r * 128;
-        const int chunk0 = (q & 1) * 4;
-        // A cursor over (tile, stage) runs kAhead stages ahead of the expansion;
-        // its loads land in slots with fixed names, so that nothing waits for a
-        // load before the stage that uses it.
-        const uint8_t *code_at = nullptr, *scale_base = nullptr;
-        int tile = unit, k = 0, k1 = 0, i = 0, block = 0, left = 0;   // left: rows of W from this thread's on
-        auto load = [&](uint4 &codes, uint32_t &scale) {
-            if (k == k1 || i == g.nn) {
-                if (k == k1) {   // the next tile (the first: k and k1 are 0 and tile is this pair's)
-                    if (k1 > 0) tile += units;
-                    const Tile c = tile_of(g, tile < g.tiles ? tile : unit, nk);
-                    k = c.k0, k1 = c.k1, block = c.p * 8 + static_cast<int>(rank) * 4 + q;
-                }
-                const int seg = k / g.nn, m = seg < g.planes ? 0 : 1;
-                i = k - seg * g.nn;
-                const int r0 = i * kRowsK + r;
-                // columns past the last stay zero (rows of dx that are not stored)
-                left = tile < g.tiles && block < g.nb ? g.N - r0 : 0;
-                code_at = g.codes[m] + r0 * g.pitch + block * 16;
-                scale_base = g.scales[m];
+        uint32_t to[4];   // where the four 16-byte pieces of the row go
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = smem_u32(stage0) + (q >> 1) * 8192 + r * 128 + ((((q & 1) * 4 + j) ^ (r & 7)) << 4);
+        // A cursor over (tile, product, stage) runs kAhead stages ahead of the
+        // expansion; its loads land in slots with fixed names, so that nothing
+        // waits for a load before the stage that uses it. Its pointers move by 64
+        // rows; 'steps' counts down to the next product or tile.
+        const uint8_t *code_at = nullptr, *scale_from = nullptr;
+        const int64_t code_step = kRowsK * g.pitch, scale_tile = g.sf_tiles * 512;
+        int tile = unit, k = 0, k1 = 0, steps = 0, left = 0;   // left: rows of W from this thread's on
+        bool odd = false;                                      // the row's number modulo 128 is 64 or more
+        auto place = [&] {
+            if (k == k1) {   // the next tile (the first: k and k1 are 0 and tile is this pair's)
+                if (k1 > 0) tile += units;
+                const Tile c = tile_of(g, tile < g.tiles ? tile : unit, nk);
+                k = c.k0, k1 = c.k1;
             }
+            const int seg = k / g.nn, m = seg < g.planes ? 0 : 1, i = k - seg * g.nn, n = i * kRowsK + r;
+            const int block = tile % g.n_p * 8 + static_cast<int>(rank) * 4 + q;
+            steps = min(g.nn - i, k1 - k);
+            k += steps;
+            // columns past the last stay zero (rows of dx that are not stored)
+            left = tile < g.tiles && block < g.nb ? g.N - n : 0;
+            odd = n & 64;
+            code_at = g.codes[m] + n * g.pitch + block * 16;
+            scale_from = g.scales[m] + scale_at(n, block, g.sf_tiles);
+        };
+        auto load = [&](uint4 &codes, uint32_t &scale) {
+            if (steps == 0) place();
             codes = make_uint4(0u, 0u, 0u, 0u);
             scale = 0;
             if (left > 0) {   // rows past the last stay zero (they meet zeros of the gradient)
                 codes = *reinterpret_cast<const uint4 *>(code_at);
-                scale = scale_base[scale_at(i * kRowsK + r, block, g.sf_tiles)];
+                scale = *scale_from;
             }
-            ++i, ++k;
+            --steps;
             left -= kRowsK;
-            code_at += kRowsK * g.pitch;
+            code_at += code_step;
+            scale_from += odd ? scale_tile - 8 : 8;   // rows 64 apart: two words on, or the next tile's
+            odd = !odd;
         };
         uint4 codes[kAhead];
         uint32_t scale[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) load(codes[a], scale[a]);
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
         int64_t total = 0;   // stages of this pair
         for (int t = unit; t < g.tiles; t += units) {
             const Tile c = tile_of(g, t, nk);
             total += c.k1 - c.k0;
         }
-        for (int64_t done = 0; done < total && ok; done += kAhead) {
+        int s = 0;
+        uint32_t ph = 0, at = 0;   // at: the stage's place in the ring
+        bool ok = true;
+        for (; total > 0 && ok; total -= kAhead) {
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (done + a >= total) break;
+                if (a >= total) break;
                 // exponent field of 2^(126 + s); what passes 254 is a second factor
                 const uint32_t field = scale[a] + 126u;
                 const uint32_t f1 = scale[a] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
@@ -287,9 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 const uint32_t words[4] = {codes[a].x, codes[a].y, codes[a].z, codes[a].w};
                 uint32_t v[16];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) v[4 * j + b] = mul_bf16x2(bf16_pattern(words[j], words[j] >> 4, b), f1x2);
+                for (int j = 0; j < 4; ++j) {
+                    v[4 * j] = mul_bf16x2(bf16_pattern<0>(words[j]), f1x2);
+                    v[4 * j + 1] = mul_bf16x2(bf16_pattern<1>(words[j]), f1x2);
+                    v[4 * j + 2] = mul_bf16x2(bf16_pattern<2>(words[j]), f1x2);
+                    v[4 * j + 3] = mul_bf16x2(bf16_pattern<3>(words[j]), f1x2);
+                }
                 if (field > 254u && scale[a] != 255u) {
                     const uint32_t f2 = (127u + field - 254u) << 7, f2x2 = f2 | f2 << 16;
 #pragma unroll
@@ -300,22 +318,27 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(dst + s * stage_size + (((chunk0 + j) ^ (r & 7)) << 4)) =
-                        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[j] + at), "r"(v[4 * j]), "r"(v[4 * j + 1]),
+                                 "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
+                                 : "memory");
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(&sh->full[s]);
-                if (++s == stages) s = 0, ph ^= 1u;
+                at += stage_size;
+                if (++s == stages) s = 0, at = 0, ph ^= 1u;
             }
         }
     } else {
         griddep_wait();
         griddep_launch();   // all earlier work is done
-        const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2;
+        const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2, slot = column_slot(lane);
         float *own = turn + (warp - 2 - kExpand) * kTurnFloats;
-        // one warp of a lane quarter takes the first w / 2 tokens, the other the rest
-        const int first = half * (g.w / 2);
-        const uint32_t from = tmem + half * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+        // two accumulators: each of a lane quarter's two warps takes one; one: they
+        // take turns by 8 (16) tokens
+        const bool two = g.halves == 2;
+        const int wide = g.w / g.halves, first = two ? half * wide : 0;
+        const int j_first = two ? 0 : half * 8, j_step = two ? 8 : 16;
+        const uint32_t from = tmem + (two ? half * 256 : 0) + (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t acc_ph = 0;
         for (int tile = unit; tile < g.tiles; tile += units) {
             const Tile c = tile_of(g, tile, nk);
@@ -331,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
                 acc_ph ^= 1u;
                 tc_fence_after();
-                for (int j = 0; j < g.w / 2; j += 16) {
+                for (int j = 2 * j_first; j < wide; j += 2 * j_step) {
                     float v[1][16];
                     tmem_ld16(from + j, v);
-                    simple_finish<1>(ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v);
+                    simple_finish<1>(ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v, slot);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -342,18 +365,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 continue;
             }
             Raw8 x[2][1];   // what a chunk of 8 tokens reads is asked for a chunk ahead
-            epilogue_reads<false>(ep, t, n, t < ep.T, x[0]);
+            epilogue_reads<false>(ep, t + j_first, n, t + j_first < ep.T, x[0]);
             if (!bar_wait(&sh->acc_full, acc_ph, abort)) break;
             acc_ph ^= 1u;
             tc_fence_after();
-            for (int j0 = 0; j0 < g.w / 2; j0 += 16) {
+            for (int j0 = j_first; j0 < wide; j0 += 2 * j_step) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int j = j0 + i * 8, next = j + 8;
-                    epilogue_reads<false>(ep, t + next, n, next < g.w / 2 && t + next < ep.T, x[i ^ 1]);
+                    const int j = j0 + i * j_step, next = j + j_step;
+                    if (j >= wide) break;
+                    epilogue_reads<false>(ep, t + next, n, next < wide && t + next < ep.T, x[i ^ 1]);
                     float col[1][8], row[1][8];
                     tmem_ld8(from + j, col);
-                    turn8<1>(own, col, row);
+                    turn8<1>(own, col, row, slot);
                     epilogue_finish<false>(ep, t + j, n, t + j < ep.T, x[i], row);
                 }
             }
@@ -555,7 +579,7 @@ int resident_pairs(cudaLaunchConfig_t cfg)
     return pairs;
 }
 
-// Tokens per tile (a multiple of 32 up to 512) and parts of the contraction.
+// Tokens per tile (a multiple of 16, over 256 of 32, up to 512) and parts of the contraction.
 // Cost of the last pair to finish, in cycles: waves of tiles, each so many
 // stages, a stage taking its eight MMAs (2 w) or, as measured for narrow tiles,
 // 1050 (the expansion's instructions and the hand-over between the roles, the
@@ -569,9 +593,9 @@ struct Plan {
 Plan plan(int64_t M, int64_t T, int64_t nk)
 {
     const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
-    Plan best = {32, 1};
+    Plan best = {16, 1};
     double least = -1;
-    for (int w = 32; w <= 512; w += 32) {
+    for (int w = 16; w <= 512; w += w < 256 ? 16 : 32) {
         const int64_t tiles = n_p * ((T + w - 1) / w);
         for (int splits = 1; splits <= kMaxSplits && splits <= nk; ++splits) {
             if (splits > 1 && tiles * splits > pairs) break;
@@ -617,12 +641,12 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
 {
     const int mats = c.codes[1] ? 2 : 1;
     const Plan pl = plan(c.M, c.T, stages(c.N, mats, planes));
-    const int w = pl.w;
+    const int w = pl.w, halves = w > 256 ? 2 : 1;
     CUtensorMap map[2];
     for (int m = 0; m < 2; ++m) {
         const uint64_t dims[2] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.T * planes)};
         const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
-        const uint32_t box[2] = {kRowsK, static_cast<uint32_t>(w / 4)};
+        const uint32_t box[2] = {kRowsK, static_cast<uint32_t>(w / halves / 2)};
         if (!tc_map(&map[m], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, operand[m < mats ? m : 0], dims, strides, box, true))
             return cudaErrorInvalidValue;
     }
@@ -637,6 +661,7 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     g.planes = planes;
     g.plane_rows = c.T;
     g.w = w;
+    g.halves = halves;
     g.n_p = static_cast<int>((c.M + 255) / 256);
     g.n_c = static_cast<int>((c.T + w - 1) / w);
     g.splits = pl.splits;

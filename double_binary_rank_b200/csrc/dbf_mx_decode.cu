@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
     const uint32_t x_stage = g.w * 128 + 1024;
     Smem *sh = reinterpret_cast<Smem *>(xq + g.nks * x_stage);
     float *part = reinterpret_cast<float *>(ring);   // [mat][token][128 rows], once the ring is done with
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int S = gridDim.x, rank = blockIdx.x;
     const int row0 = blockIdx.y * 128;
     const int k0 = g.nk * rank / S, nks = g.nk * (rank + 1) / S - k0;
@@ -94,54 +94,59 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh->tmem_base, 0);
     const uint32_t sf_col = kMats * g.w;   // scales: 8 columns per weight, then 8 of x
 
     if (warp == 0) {
-        if (lane == 0) {
-            if (!g.early) griddep_wait();
-            int i = 0;
-            for (; i < nks; ++i) {
-                if (g.pre && i == min(nks, g.ring) - 1) {   // after the first weights, before a wait for a free stage
-                    griddep_wait();
+        if (!g.early) griddep_wait();
+        const int first = min(nks, g.ring) - 1;
+        int i = 0;
+        for (; i < nks; ++i) {
+            if (g.pre && i == first) {   // after the first weights, before a wait for a free stage
+                griddep_wait();
+                if (elect_one()) {
                     bar_expect_tx(&sh->x_ready, nks * x_stage);
                     for (int k = 0; k < nks; ++k) {
                         tma_2d(xq + k * x_stage, &mX, (k0 + k) * 128, 0, &sh->x_ready);
                         tma_3d(xq + k * x_stage + g.w * 128, &mXS, 0, (k0 + k) * 2, 0, &sh->x_ready);
                     }
                 }
-                const int s = i % g.ring;
-                if (!bar_wait(&sh->empty[s], (static_cast<uint32_t>(i / g.ring) & 1u) ^ 1u, abort)) break;
-                uint8_t *st = ring + s * kStage;
+                __syncwarp();
+            }
+            const int s = i % g.ring;
+            if (!warp_wait(&sh->empty[s], (static_cast<uint32_t>(i / g.ring) & 1u) ^ 1u, abort)) break;
+            uint8_t *st = ring + s * kStage;
+            if (elect_one()) {
                 bar_expect_tx(&sh->full[s], kStage);
                 tma_2d(st, &mA0, (k0 + i) * 128, row0, &sh->full[s]);
                 if (kGated) tma_2d(st + kABytes, &mA1, (k0 + i) * 128, row0, &sh->full[s]);
                 tma_3d(st + kMats * kABytes, &mS0, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
                 if (kGated) tma_3d(st + kMats * kABytes + kSfBytes, &mS1, 0, (k0 + i) * 2, blockIdx.y, &sh->full[s]);
             }
-            if (*abort && g.pre && i >= min(nks, g.ring) - 1) drain_wait(&sh->x_ready, 0);
-            if (*abort)
-                for (int j = i > g.ring ? i - g.ring : 0; j < i; ++j)
-                    drain_wait(&sh->full[j % g.ring], static_cast<uint32_t>(j / g.ring) & 1u);
+            __syncwarp();
         }
+        if (*abort && g.pre && i >= first) drain_wait(&sh->x_ready, 0);
+        if (*abort)
+            for (int j = i > g.ring ? i - g.ring : 0; j < i; ++j)
+                drain_wait(&sh->full[j % g.ring], static_cast<uint32_t>(j / g.ring) & 1u);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id0 = mxf4_idesc(128, g.w, 0), id2 = mxf4_idesc(128, g.w, 2);
-            bool ok = bar_wait(&sh->x_ready, 0, abort);
-            for (int i = 0; i < nks && ok; ++i) {
-                const int s = i % g.ring;
-                ok = bar_wait(&sh->full[s], static_cast<uint32_t>(i / g.ring) & 1u, abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(ring) + s * kStage, sf = st + kMats * kABytes;
-                const uint32_t xs = smem_u32(xq) + i * x_stage;
+        const uint32_t id0 = mxf4_idesc(128, g.w, 0), id2 = mxf4_idesc(128, g.w, 2);
+        bool ok = warp_wait(&sh->x_ready, 0, abort);
+        for (int i = 0; i < nks && ok; ++i) {
+            const int s = i % g.ring;
+            ok = warp_wait(&sh->full[s], static_cast<uint32_t>(i / g.ring) & 1u, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(ring) + s * kStage, sf = st + kMats * kABytes;
+            const uint32_t xs = smem_u32(xq) + i * x_stage;
+            const uint64_t b = sw128_desc(xs);
+            if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     scale_copy<1>(tmem + sf_col + 4 * c, scale_desc(sf + c * 512));
                     if (kGated) scale_copy<1>(tmem + sf_col + 8 + 4 * c, scale_desc(sf + kSfBytes + c * 512));
                     scale_copy<1>(tmem + sf_col + 8 * kMats + 4 * c, scale_desc(xs + g.w * 128 + c * 512));
                 }
-                const uint64_t b = sw128_desc(xs);
 #pragma unroll
                 for (int m = 0; m < kMats; ++m) {
                     const uint64_t a = sw128_desc(st + m * kABytes);
@@ -153,9 +158,11 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
                 }
                 commit_own(&sh->empty[s]);
             }
-            commit_own(&sh->done);
-            drain_wait(&sh->done, 0);
+            __syncwarp();
         }
+        if (elect_one()) commit_own(&sh->done);
+        __syncwarp();
+        drain_wait(&sh->done, 0);
     } else {
         const int worker = warp - 2;
         griddep_wait();     // x, y and the addends belong to earlier work until then

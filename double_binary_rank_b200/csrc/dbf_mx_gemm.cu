@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     const uint32_t stage_size = stage_bytes(accs, g.w), off_b = b_at(accs), off_sf = sf_at(accs, g.w);
     float *turn = reinterpret_cast<float *>(stage0 + stages * stage_size);
     Smem *sh = reinterpret_cast<Smem *>(turn + kEpiWarps * kMats * kTurnFloats);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
     volatile int *abort = &sh->abort;
@@ -170,28 +170,27 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before either is reached from the other
     tc_fence_after();
-    const uint32_t tmem = sh->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh->tmem_base, 0);
     // the pre-pass before this launch has waited for all earlier work, so
     // weights may be read at once; x's codes, and y, only after it is done
     griddep_launch();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const int half_w = g.w / 2, nrt = g.w > 128 ? 2 : 1;
-            const uint32_t bytes = 2 * off_sf, sf_bytes = stage_size - off_sf;
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true, waited = false;
-            for (int tile = unit; tile < g.tiles && ok; tile += units) {
-                const int p = tile % g.n_p, c = tile / g.n_p;
-                const int row0 = p * g.row_step + static_cast<int>(rank) * 128, row1 = row0 + g.row_off;
-                const int tok = c * g.w + static_cast<int>(rank) * half_w;
-                for (int ks = 0; ks < g.nk; ++ks) {
-                    if (!bar_wait(&sh->empty[s], ph ^ 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = stage0 + s * stage_size, *sf = st + off_sf;
+        const int half_w = g.w / 2, nrt = g.w > 128 ? 2 : 1;
+        const uint32_t bytes = 2 * off_sf, sf_bytes = stage_size - off_sf;
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true, waited = false;
+        for (int tile = unit; tile < g.tiles && ok; tile += units) {
+            const int p = tile % g.n_p, c = tile / g.n_p;
+            const int row0 = p * g.row_step + static_cast<int>(rank) * 128, row1 = row0 + g.row_off;
+            const int tok = c * g.w + static_cast<int>(rank) * half_w;
+            for (int ks = 0; ks < g.nk; ++ks) {
+                ok = warp_wait(&sh->empty[s], ph ^ 1u, abort);
+                if (!ok) break;
+                uint8_t *st = stage0 + s * stage_size, *sf = st + off_sf;
+                const bool one = elect_one();
+                if (one) {
                     if (rank == 0) bar_expect_tx(&sh->full[s], bytes);
                     bar_expect_tx(&sh->sf_full[s], sf_bytes);   // the scales are counted by each CTA for itself
                     tma_2d_pair(st, &mA0, ks * 128, row0, &sh->full[s]);
@@ -200,26 +199,30 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                         tma_2d_pair(st + kABytes, &mA1, ks * 128, row1, &sh->full[s]);
                         tma_3d(sf + kSfBytes, &mS1, 0, ks * 2, row1 >> 7, &sh->sf_full[s]);
                     }
-                    if (!waited) {
-                        griddep_wait();
-                        waited = true;
-                    }
+                }
+                __syncwarp();
+                if (!waited) {
+                    griddep_wait();
+                    waited = true;
+                }
+                if (one) {
                     tma_2d_pair(st + off_b, &mB, ks * 128, tok, &sh->full[s]);
                     tma_3d(sf + accs * kSfBytes, &mSB, 0, ks * 2, c * nrt, &sh->sf_full[s]);
-                    ++issued;
-                    if (++s == stages) s = 0, ph ^= 1u;
                 }
+                __syncwarp();
+                ++issued;
+                if (++s == stages) s = 0, ph ^= 1u;
             }
-            // after a wait gave up, the loads in flight are still waited for
-            // (CTA 0's barriers count both CTAs' bytes)
-            if (*abort)
-                for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
-                    drain_wait(&sh->sf_full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
-                    if (rank == 0) drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
-                }
         }
+        // after a wait gave up, the loads in flight are still waited for
+        // (CTA 0's barriers count both CTAs' bytes)
+        if (*abort)
+            for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
+                drain_wait(&sh->sf_full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
+                if (rank == 0) drain_wait(&sh->full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
+            }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int s = 0;
             uint32_t ph = 0;
             Turn acc, sf_turn;
@@ -227,30 +230,35 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             bool ok = true;
             const uint32_t id0 = mxf4_idesc(256, g.w, 0), id2 = mxf4_idesc(256, g.w, 2);
             for (int tile = unit; tile < g.tiles && ok; tile += units, acc.next(g.bufs)) {
-                ok = bar_wait(&sh->acc_empty[acc.buf], acc.phase ^ 1u, abort);
+                ok = warp_wait(&sh->acc_empty[acc.buf], acc.phase ^ 1u, abort);
                 if (!ok) break;
                 const uint32_t d = tmem + acc.buf * accs * g.w;
                 for (int ks = 0; ks < g.nk; ++ks, sf_turn.next(g.sf_bufs)) {
-                    ok = bar_wait(&sh->full[s], ph, abort) && bar_wait(&sh->sf_ready[sf_turn.buf], sf_turn.phase, abort);
+                    ok = warp_wait(&sh->full[s], ph, abort) && warp_wait(&sh->sf_ready[sf_turn.buf], sf_turn.phase, abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(stage0) + s * stage_size, sf = sf0 + sf_turn.buf * sf_cols(g.w);
                     const uint64_t a0 = sw128_desc(st), a1 = sw128_desc(st + kABytes), b = sw128_desc(st + off_b);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t id = kk & 1 ? id2 : id0, acc = ks > 0 || kk > 0 ? 1u : 0u;
-                        const uint32_t sb = sf + 16 + b_half * (kk >> 1);
-                        mma_mxf4<2>(d, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, acc);
-                        if (accs == 2) mma_mxf4<2>(d + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, acc);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t id = kk & 1 ? id2 : id0, more = ks > 0 || kk > 0 ? 1u : 0u;
+                            const uint32_t sb = sf + 16 + b_half * (kk >> 1);
+                            mma_mxf4<2>(d, a0 + 2 * kk, b + 2 * kk, id, sf + 4 * (kk >> 1), sb, more);
+                            if (accs == 2) mma_mxf4<2>(d + g.w, a1 + 2 * kk, b + 2 * kk, id, sf + 8 + 4 * (kk >> 1), sb, more);
+                        }
+                        commit_pair_both(&sh->empty[s]);
                     }
-                    commit_pair_both(&sh->empty[s]);
+                    __syncwarp();
                     if (++s == stages) s = 0, ph ^= 1u;
                 }
                 if (!ok) break;
-                commit_pair_both(&sh->acc_full[acc.buf]);
+                if (elect_one()) commit_pair_both(&sh->acc_full[acc.buf]);
+                __syncwarp();
             }
             if (*abort) {
-                commit_pair_own(&sh->drain);
+                if (elect_one()) commit_pair_own(&sh->drain);
+                __syncwarp();
                 drain_wait(&sh->drain, 0);
             }
         }
@@ -308,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                 for (int j = 2 * j_first; j < g.w; j += 2 * j_step) {
                     float v[kMats][16];
                     load_chunk(lanes + j, g.w, v);
-                    simple_finish<kMats>(g.ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v);
+                    simple_finish<kMats>(g.ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v, lane);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
                     epilogue_reads<kGated>(g.ep, t + next, n, next < g.w && t + next < g.ep.T, x[i ^ 1]);
                     float col[kMats][8], row[kMats][8];
                     load_chunk(lanes + j, g.w, col);
-                    turn8<kMats>(own, col, row);
+                    turn8<kMats>(own, col, row, lane);
                     epilogue_finish<kGated>(g.ep, t + j, n, t + j < g.ep.T, x[i], row);
                 }
             }

@@ -125,15 +125,16 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue &e, int64_t t, in
 // different banks.
 constexpr int kTurnFloats = 8 * 36;   // per accumulator
 
+// slot: which of the 32 columns the lane holds.
 template <int kMats>
-__device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], float (&row)[kMats][8])
+__device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], float (&row)[kMats][8], int slot)
 {
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) own[m * kTurnFloats + j * 36 + lane] = col[m][j];
+        for (int j = 0; j < 8; ++j) own[m * kTurnFloats + j * 36 + slot] = col[m][j];
     __syncwarp();
 #pragma unroll
     for (int m = 0; m < kMats; ++m) {
@@ -154,13 +155,15 @@ __device__ __forceinline__ bool epilogue_is_simple(const Epilogue &e)
 {
     return (e.yd == DBF_F32 || epilogue_vec(e)) && !e.accumulate && !e.g_add && !e.u_add && !e.g8;
 }
-// n0: the warp's first column; own: kTurnFloats words
+// n0: the warp's first column; own: kTurnFloats words; slot: which column the
+// lane holds
 template <int kMats>
-__device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, int64_t t0, int n0, const float (&v)[kMats][16])
+__device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, int64_t t0, int n0, const float (&v)[kMats][16],
+                                              int slot)
 {
     const int lane = threadIdx.x & 31;
     if (e.yd == DBF_F32) {
-        const int n = n0 + lane;
+        const int n = n0 + slot;
         const int left = static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16);
         float *y = static_cast<float *>(e.y) + t0 * e.N + n;
 #pragma unroll
@@ -177,7 +180,7 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
             b = gate_value(e.act, b) * v[kMats - 1][2 * p + 1];
         }
         const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
-        own[p * 36 + lane] = *reinterpret_cast<const uint32_t *>(&w);
+        own[p * 36 + slot] = *reinterpret_cast<const uint32_t *>(&w);
     }
     __syncwarp();
     const int p = lane >> 2, c = n0 + (lane & 3) * 8;

@@ -60,6 +60,28 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
         }
     }
 }
+// The whole warp's wait, with one answer: control flow that depends on it stays
+// uniform, and what the issuing lane of a role needs stays in uniform registers
+// (in a branch of one lane alone an MMA took about 130 cycles to issue, and the
+// loop around it 700).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort));
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one)::"memory");
+    return one != 0;
+}
+// This thread's warp number, known to be the same in the whole warp
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
 // Wait (bounded) whatever the abort flag says: before a CTA ends, nothing
 // that it issued may still be in flight.
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
