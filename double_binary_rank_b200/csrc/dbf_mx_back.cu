@@ -16,14 +16,15 @@
 // two accumulators (an expanded stage feeds two MMAs a step), contraction over
 // the rows of W in stages of 64:
 //   warp 0       TMA: w / 2 token rows of the gradient, 64 columns each;
-//   warps 2..9   expansion: a thread takes 32 codes of one row of W (16 bytes
-//                and a scale, loaded four stages ahead) and writes them as 64
+//   warps 2..17  expansion, two groups taking turns by stages: a thread takes
+//                32 codes of one row of W (16 bytes and a scale, loaded four
+//                stages ahead) and writes them as 64
 //                bytes of a 128-byte-swizzled tile whose rows are rows of W:
 //                the A operand in its M-major form, so nothing is transposed;
 //                a warp's lanes hold 32 different rows, whose swizzled chunks
 //                lie in different banks;
 //   warp 1       one thread of CTA 0 issues the MMAs (M = 256, N up to 256, K = 16);
-//   warps 10..17 epilogue.
+//   warps 18..25 epilogue.
 // Where the tiles are fewer than the pairs, the contraction is cut into parts
 // whose fp32 sums a second launch adds in order.
 #include <algorithm>
@@ -39,9 +40,9 @@ using namespace mx;
 using namespace tc;
 
 constexpr int kMaxStages = 10;
-constexpr int kExpand = 8, kEpiWarps = 8;   // warps
-constexpr int kThreads = 32 * (2 + kExpand + kEpiWarps);
-constexpr int kAhead = 4;                           // stages that the expansion's loads run ahead
+constexpr int kGroups = 2, kExpand = 8, kEpiWarps = 8;   // groups of kExpand warps, taking turns by stages
+constexpr int kThreads = 32 * (2 + kGroups * kExpand + kEpiWarps);
+constexpr int kAhead = 2;                           // a group's stages that its loads run ahead
 constexpr int kRowsK = 64;                          // rows of W per stage
 constexpr uint32_t kABytes = 128 * kRowsK * 2;
 // A stage is this CTA's half of W's columns and w / 2 token rows; as many as fit.
@@ -235,38 +236,42 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 drain_wait(&sh->drain, 0);
             }
         }
-    } else if (warp < 2 + kExpand) {
+    } else if (warp < 2 + kGroups * kExpand) {
         if (!g.early) griddep_wait();
-        const int e = warp - 2, q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
+        const int group = (warp - 2) / kExpand, e = (warp - 2) % kExpand;
+        const int q = e >> 1, r = (e & 1) * 32 + lane;   // block of 32 columns, row of the stage
         uint32_t to[4];   // where the four 16-byte pieces of the row go
 #pragma unroll
         for (int j = 0; j < 4; ++j) to[j] = smem_u32(stage0) + (q >> 1) * 8192 + r * 128 + ((((q & 1) * 4 + j) ^ (r & 7)) << 4);
-        // A cursor over (tile, product, stage) runs kAhead stages ahead of the
-        // expansion; its loads land in slots with fixed names, so that nothing
-        // waits for a load before the stage that uses it. Its pointers move by 64
-        // rows; 'steps' counts down to the next product or tile.
+        // A cursor over (tile, product, stage) runs kAhead of the group's stages
+        // ahead of the expansion; its loads land in slots with fixed names, so that
+        // nothing waits for a load before the stage that uses it. Its pointers move
+        // by 128 rows, the scales' to the next tile of them; 'steps' counts down to
+        // the next product or tile.
+        static_assert(kGroups * kRowsK == 128, "a group's step is a row tile of scales");
         const uint8_t *code_at = nullptr, *scale_from = nullptr;
-        const int64_t code_step = kRowsK * g.pitch, scale_tile = g.sf_tiles * 512;
-        int tile = unit, k = 0, k1 = 0, steps = 0, left = 0;   // left: rows of W from this thread's on
-        bool odd = false;                                      // the row's number modulo 128 is 64 or more
+        const int64_t code_step = kGroups * kRowsK * g.pitch, scale_step = g.sf_tiles * 512;
+        int tile = unit, steps = 0, left = 0;   // left: rows of W from this thread's on
+        Tile c = tile_of(g, unit, nk);
+        int k = c.k0 + group;
         auto place = [&] {
-            if (k == k1) {   // the next tile (the first: k and k1 are 0 and tile is this pair's)
-                if (k1 > 0) tile += units;
-                const Tile c = tile_of(g, tile < g.tiles ? tile : unit, nk);
-                k = c.k0, k1 = c.k1;
+            while (k >= c.k1 && tile < g.tiles) {
+                k -= c.k1;
+                tile += units;
+                c = tile_of(g, tile < g.tiles ? tile : unit, nk);
+                k += c.k0;
             }
-            const int seg = k / g.nn, m = seg < g.planes ? 0 : 1, i = k - seg * g.nn, n = i * kRowsK + r;
-            const int block = tile % g.n_p * 8 + static_cast<int>(rank) * 4 + q;
-            steps = min(g.nn - i, k1 - k);
-            k += steps;
+            const int at = min(k, nk - 1), seg = at / g.nn, m = seg < g.planes ? 0 : 1, i = at - seg * g.nn, n = i * kRowsK + r;
+            const int block = c.p * 8 + static_cast<int>(rank) * 4 + q;
+            steps = (min(g.nn - i, c.k1 - at) + kGroups - 1) / kGroups;
+            k += steps * kGroups;
             // columns past the last stay zero (rows of dx that are not stored)
             left = tile < g.tiles && block < g.nb ? g.N - n : 0;
-            odd = n & 64;
             code_at = g.codes[m] + n * g.pitch + block * 16;
             scale_from = g.scales[m] + scale_at(n, block, g.sf_tiles);
         };
         auto load = [&](uint4 &codes, uint32_t &scale) {
-            if (steps == 0) place();
+            if (steps <= 0) place();
             codes = make_uint4(0u, 0u, 0u, 0u);
             scale = 0;
             if (left > 0) {   // rows past the last stay zero (they meet zeros of the gradient)
@@ -274,10 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 scale = *scale_from;
             }
             --steps;
-            left -= kRowsK;
+            left -= kGroups * kRowsK;
             code_at += code_step;
-            scale_from += odd ? scale_tile - 8 : 8;   // rows 64 apart: two words on, or the next tile's
-            odd = !odd;
+            scale_from += scale_step;
         };
         uint4 codes[kAhead];
         uint32_t scale[kAhead];
@@ -288,13 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
             const Tile c = tile_of(g, t, nk);
             total += c.k1 - c.k0;
         }
-        int s = 0;
-        uint32_t ph = 0, at = 0;   // at: the stage's place in the ring
+        int s = group;                                     // the ring is longer than the groups are many
+        uint32_t ph = 0, at = group * stage_size;          // at: the stage's place in the ring
         bool ok = true;
-        for (; total > 0 && ok; total -= kAhead) {
+        for (total -= group; total > 0 && ok; total -= kAhead * kGroups) {
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (a >= total) break;
+                if (a * kGroups >= total) break;
                 // exponent field of 2^(126 + s); what passes 254 is a second factor
                 const uint32_t field = scale[a] + 126u;
                 const uint32_t f1 = scale[a] == 255u ? 0x7FC0u : (field > 254u ? 254u : field) << 7;
@@ -324,15 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(&sh->full[s]);
-                at += stage_size;
-                if (++s == stages) s = 0, at = 0, ph ^= 1u;
+                s += kGroups, at += kGroups * stage_size;
+                if (s >= stages) s -= stages, at -= stages * stage_size, ph ^= 1u;
             }
         }
     } else {
         griddep_wait();
         griddep_launch();   // all earlier work is done
-        const int quarter = warp & 3, half = (warp - 2 - kExpand) >> 2, slot = column_slot(lane);
-        float *own = turn + (warp - 2 - kExpand) * kTurnFloats;
+        const int quarter = warp & 3, half = (warp - 2 - kGroups * kExpand) >> 2, slot = column_slot(lane);
+        float *own = turn + (warp - 2 - kGroups * kExpand) * kTurnFloats;
         // two accumulators: each of a lane quarter's two warps takes one; one: they
         // take turns by 8 (16) tokens
         const bool two = g.halves == 2;
