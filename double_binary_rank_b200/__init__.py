@@ -777,6 +777,15 @@ class Act8:
         return Act8(rows, cols, torch.empty((rows, nb * 32), dtype=torch.uint8, device=device),
                     torch.empty((nb, rows), dtype=torch.uint8, device=device))
 
+    @staticmethod
+    def _like(rows: int, cols: int, t: torch.Tensor) -> "Act8":
+        """empty() on t's device, of what needs no check."""
+        nb = -(-cols // 32)
+        codes, scales = t.new_empty((rows, nb * 32), dtype=torch.uint8), t.new_empty((nb, rows), dtype=torch.uint8)
+        a = object.__new__(Act8)
+        a.__dict__.update(rows=rows, cols=cols, codes=codes, scales=scales, _c=DbfAct8C(codes.data_ptr(), scales.data_ptr()))
+        return a
+
     def descriptor(self) -> DbfAct8C:
         return self._c
 
@@ -795,7 +804,7 @@ def act8_save(src: torch.Tensor, out: Optional[Act8] = None, status: Optional[to
     _need(status, "status", (1,), _I32, src)
     s, back = _enter(src, stream)
     try:
-        out = Act8.empty(rows, cols, src.device) if out is None else out
+        out = Act8._like(rows, cols, src) if out is None else out
         _check(_lib.dbf_act8_save(_ptr(src), _DT[src.dtype], rows, cols, _act8(out, rows, cols, src), _ptr(status), s),
                "dbf_act8_save")
     finally:

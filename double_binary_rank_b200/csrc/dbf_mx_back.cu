@@ -585,11 +585,11 @@ int resident_pairs(cudaLaunchConfig_t cfg)
 
 // Tokens per tile (a multiple of 16, over 256 of 32, up to 512) and parts of the contraction.
 // Cost of the last pair to finish, in cycles: waves of tiles, each so many
-// stages, a stage taking its eight MMAs (2 w) or, as measured for narrow tiles,
-// 1050 (the expansion's instructions and the hand-over between the roles, the
-// same at every width), and an epilogue; the parts' sums are written and read
-// once more. 4096 -> 11008 at 1024 tokens: 102 us in tiles of 256, 72 us in two
-// parts of tiles of 512.
+// stages, a stage taking its MMAs (2 w and the hand-over) or the expansion of W
+// (the same at every width), and an epilogue; a second launch for the parts,
+// whose sums are written and read once more. 4096 -> 11008: 256 tokens 32 us in
+// four parts of one tile, 46 us in one; 2048 x 2048 at 600 tokens 15.8 us in
+// tiles of 96, 16.9 us in three parts of tiles of 208.
 constexpr int64_t kMaxSplits = 16;
 struct Plan {
     int w, splits;
@@ -605,8 +605,8 @@ Plan plan(int64_t M, int64_t T, int64_t nk)
             if (splits > 1 && tiles * splits > pairs) break;
             const double waves = static_cast<double>((tiles * splits + pairs - 1) / pairs);
             const double stages = static_cast<double>((nk + splits - 1) / splits);
-            const double join = splits > 1 ? 4000.0 + 8.0 * T * M * (splits + 1) / 3500.0 : 0.0;   // a launch, and bytes at 3.5 KB a cycle
-            const double cost = waves * (stages * std::max(2.0 * w, 1050.0) + 3000 + 12.0 * w) + join;
+            const double join = splits > 1 ? 4000.0 + 800.0 * splits + 8.0 * T * M * (splits + 1) / 3500.0 : 0.0;   // a launch, and bytes at 3.5 KB a cycle
+            const double cost = waves * (stages * std::max(2.0 * w + 120, 560.0) + 3000 + 12.0 * w) + join;
             if (least < 0 || cost < least) least = cost, best = {w, splits};
         }
         if (w >= T) break;

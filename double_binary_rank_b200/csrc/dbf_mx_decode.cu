@@ -30,7 +30,8 @@ using namespace mx;
 using namespace tc;
 
 constexpr int kMaxRing = 8;
-constexpr int kMaxColumns = 64;   // tokens of a call times its weights: beyond, dbf_mx_gemm.cu is faster
+constexpr int kMaxColumns = 32;   // tokens of a call times its weights: beyond, dbf_mx_gemm.cu is as fast or faster
+                                  // (4096 -> 11008 at 64 tokens 14.9 us here, 11.6 us there; at 16 10.3 us and 10.8 us)
 constexpr int kInline = 48;       // rows of 256 columns of x up to which a CTA quantises its part itself
 constexpr int kSplit = 4;          // parts of the columns (2048 x 2048 at one token: 4.9 us in 4, 5.7 us in 8); 8 where x does not fit otherwise
 constexpr int kWorkers = 8;
