@@ -9,8 +9,9 @@
 // so the block-scaled MMA cannot take them: the codes are expanded on chip to
 // bf16, exactly (E2M1 times a power of two has two significant bits), and the
 // product runs at the bf16 rate with fp32 accumulators. bf16 gradients are
-// operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
-// each (v = p0 + p1 + p2 exactly), three times the products.
+// operands as they are; fp32 ones are cut into bf16 pieces, each a product more:
+// three of eight bits for an fp32 dx (v = p0 + p1 + p2 exactly), two for a bf16
+// one (off by at most 2^-16 of v, against the 2^-8 of rounding dx).
 //
 // A CTA pair owns 256 columns of W x w <= 512 tokens of dx, over 256 tokens as
 // two accumulators (an expanded stage feeds two MMAs a step), contraction over
@@ -409,8 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
 
 // fp32 to three bf16 pieces by truncation: p0 the upper half of the word, then
 // the same of what is left (each difference is exact); the last has at most
-// eight bits left. A NaN or an infinity stays whole in p0.
-__device__ __forceinline__ void split3(float v, uint16_t (&p)[3])
+// eight bits left. Of two pieces the second is rounded instead: what is left of
+// v after p0 is below 2^-7 |v|, its eight bits leave at most 2^-9 of that. A NaN
+// or an infinity stays whole in p0.
+__device__ __forceinline__ void split(float v, int planes, uint16_t (&p)[3])
 {
     const uint32_t b = __float_as_uint(v);
     if ((b & 0x7F800000u) == 0x7F800000u) {
@@ -420,6 +423,10 @@ __device__ __forceinline__ void split3(float v, uint16_t (&p)[3])
     }
     p[0] = static_cast<uint16_t>(b >> 16);
     const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
+    if (planes == 2) {
+        p[1] = __bfloat16_as_ushort(__float2bfloat16_rn(r1));
+        return;
+    }
     p[1] = static_cast<uint16_t>(__float_as_uint(r1) >> 16);
     const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
     p[2] = static_cast<uint16_t>(__float_as_uint(r2) >> 16);
@@ -432,8 +439,8 @@ __device__ __forceinline__ void store_planes(uint16_t *op, int64_t ld, int64_t p
     uint16_t p[8][3];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (planes == 3)
-            split3(v[i], p[i]);
+        if (planes > 1)
+            split(v[i], planes, p[i]);
         else
             p[i][0] = static_cast<uint16_t>(__float_as_uint(v[i]) >> 16);   // a bf16 value already
     }
@@ -622,6 +629,8 @@ size_t plane_bytes(int64_t N, int64_t T, dbf_dtype d)
     return align_up(static_cast<size_t>(T * operand_ld(N)) * 2 * (d == DBF_F32 ? 3 : 1), 256);
 }
 
+int pieces(const Gradient &c) { return c.dyd != DBF_F32 ? 1 : c.dxd == DBF_F32 ? 3 : 2; }
+
 struct PdlAttr {
     cudaLaunchAttribute attr[2];
     PdlAttr()
@@ -717,7 +726,7 @@ size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int
 cudaError_t mx_backward(const Gradient &c, cudaStream_t s)
 {
     const void *operand[2] = {c.dy, nullptr};
-    const int planes = c.dyd == DBF_F32 ? 3 : 1;
+    const int planes = pieces(c);
     if (direct_operand(c.N, c.dyd)) return product(c, operand, c.N, 1, false, kWsHeaderBytes, s);
     uint16_t *op = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
     const int64_t ld = operand_ld(c.N);
@@ -741,7 +750,7 @@ cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, co
     a.g8 = sg.codes, a.gs = sg.scales, a.u8 = su.codes, a.us = su.scales;
     a.dh = c.dy, a.dg = dg, a.du = du;
     a.T = c.T, a.N = c.N, a.pitch8 = blocks(c.N) * kBlock, a.ld = operand_ld(c.N);
-    a.planes = c.dyd == DBF_F32 ? 3 : 1;
+    a.planes = pieces(c);
     const void *operand[2] = {dg, du};
     if (want && !direct) {
         a.op_g = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);

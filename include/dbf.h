@@ -522,9 +522,10 @@ dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dt
 
 /* Gradient of dbf_mx4_forward for the values it multiplies: dx = [acc] dx +
  * dy W. The rounding of x to q(x) is passed straight through. W is expanded
- * exactly and bf16 gradients are used as they are; fp32 ones are cut into three
- * bf16 pieces that add up to them (parts below 2^-133 are lost), so products
- * are exact and sums fp32.
+ * exactly and bf16 gradients are used as they are. fp32 ones are cut into bf16
+ * pieces: three that add up to them (parts below 2^-133 are lost) for an fp32
+ * dx, two (off by at most 2^-16 of a value) for a bf16 dx. Products are exact
+ * and sums fp32.
  * dy: T x N and dx: T x M, DBF_F32 or DBF_BF16, 16-byte aligned, not
  *    overlapping. flags: DBF_ACCUMULATE | DBF_WEIGHTS_STATIC.
  * ws: dbf_mx4_backward_workspace_bytes(L, T, dy_dtype) bytes, 256-byte

@@ -199,7 +199,8 @@ def test_gated_forward(dbf, T, M, N, act, add):
                                    (65, 512, 512), (77, 1000, 2200), (130, 288, 640), (257, 520, 64), (300, 95, 511), (1000, 768, 1536)])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_backward_is_exact(dbf, T, M, N, kind):
-    """Whole-number gradients (up to 100, or up to 2^15 + 1 in fp32, which needs three pieces) and exact weights."""
+    """Whole-number gradients (up to 100, or up to 2^15 + 1 in fp32, which needs three pieces) and exact weights; a bf16
+    dx of an fp32 gradient within its tolerance."""
     rng = np.random.default_rng(T * 7 + M * 3 + N)
     w = exact_operand(rng, N, M)
     dy = rng.integers(-100, 101, (T, N)).astype(np.float64)
@@ -214,7 +215,11 @@ def test_backward_is_exact(dbf, T, M, N, kind):
     acc = dbf.mx4_backward(L, t, dx=torch.full((T, M), -3.0, device="cuda"), accumulate=True)
     assert np.array_equal(host(acc), ref - 3)
     b = dbf.mx4_backward(L, t, dx_dtype=torch.bfloat16)
-    assert torch.equal(b.cpu(), torch.tensor(ref).float().to(torch.bfloat16))
+    if kind == "bf16":
+        assert torch.equal(b.cpu(), torch.tensor(ref).float().to(torch.bfloat16))
+    else:   # two pieces of an fp32 gradient: each value off by at most 2^-16 of itself
+        tol = (2.0 ** -16 + N * 2.0 ** -23) * (np.abs(dy) @ np.abs(w))
+        assert np.all(np.abs(host(b) - ref) <= tol + STEP["bf16"] * (np.abs(ref) + tol))
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -242,6 +247,9 @@ def test_gated_backward(dbf, T, M, N, act, kind):
     ref, S = gg @ wgq + gu @ wuq, np.abs(gg) @ np.abs(wgq) + np.abs(gu) @ np.abs(wuq)
     pieces = 3 if kind == "f32" else 1
     assert np.all(np.abs(host(dx) - ref) <= 2 * pieces * N * 2.0 ** -23 * S + 1e-37)
+    low = host(dbf.mx4_gated_backward(gl, ul, t, saved, act=act, dx_dtype=torch.bfloat16)[0])
+    tol = (2.0 ** -16 + 4 * N * 2.0 ** -23) * S + 1e-37
+    assert np.all(np.abs(low - ref) <= tol + STEP["bf16"] * (np.abs(ref) + tol))
     none, g2, u2 = dbf.mx4_gated_backward(gl, ul, t, saved, act=act, want_dx=False)
     assert none is None and np.array_equal(host(g2), gg) and np.array_equal(host(u2), gu)
 
