@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
             if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    scale_copy<1>(tmem + sf_col + 4 * c, scale_desc(sf + c * 512));
-                    if (kGated) scale_copy<1>(tmem + sf_col + 8 + 4 * c, scale_desc(sf + kSfBytes + c * 512));
-                    scale_copy<1>(tmem + sf_col + 8 * kMats + 4 * c, scale_desc(xs + g.w * 128 + c * 512));
+                    scale_copy(tmem + sf_col + 4 * c, scale_desc(sf + c * 512));
+                    if (kGated) scale_copy(tmem + sf_col + 8 + 4 * c, scale_desc(sf + kSfBytes + c * 512));
+                    scale_copy(tmem + sf_col + 8 * kMats + 4 * c, scale_desc(xs + g.w * 128 + c * 512));
                 }
 #pragma unroll
                 for (int m = 0; m < kMats; ++m) {

@@ -109,26 +109,42 @@ __device__ __forceinline__ void prefetch_addends(const Epilogue &e, int64_t t0, 
 }
 
 // A warp's share of a gated tile: 16 tokens of both accumulators at a time,
-// every second 16 from j0; addends asked for a chunk ahead, the first before
-// the products are there. False when the wait for them gave up.
-template <bool kAdd, bool kSave, class Ready>
+// every second 16 from j0. The next 16 tokens' addends are asked for as soon as
+// these have left their registers, the first before the products are there.
+// False when the wait for them gave up.
+template <bool kAdd, bool kSave, int kAct, class Ready>
 __device__ __forceinline__ bool gated_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, Ready ready)
 {
-    uint4 x[2][2][2];
-    gated_reads<kAdd>(g.ep, t + j0, n, j0 < g.w, x[0]);
+    uint4 x[2][2];
+    gated_reads<kAdd>(g.ep, t + j0, n, j0 < g.w, x);
     if (!ready()) return false;
-    for (; j0 < g.w; j0 += 64) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = j0 + 32 * i, next = j + 32;
-            if (j >= g.w) break;
-            gated_reads<kAdd>(g.ep, t + next, n, next < g.w, x[i ^ 1]);
-            float v[2][16];
-            load_chunk(lanes + j, g.w, v);
-            gated_finish<kAdd, kSave>(g.ep, own, t + j, n, v, x[i]);
-        }
+#pragma unroll 1
+    for (int j = j0; j < g.w; j += 32) {
+        float v[2][16], r[2][16];
+        load_chunk(lanes + j, g.w, v);
+        gated_turn<kAdd>(own, v, x, r);
+        gated_reads<kAdd>(g.ep, t + j + 32, n, j + 32 < g.w, x);
+        gated_finish<kSave, kAct>(g.ep, t + j, n, r);
     }
     return true;
+}
+template <int kAct, class Ready>
+__device__ __forceinline__ bool gated_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, Ready ready)
+{
+    const bool add = g.ep.g_add != nullptr, save = g.ep.g8 != nullptr;
+    return add ? (save ? gated_tile<true, true, kAct>(g, own, lanes, t, n, j0, ready)
+                       : gated_tile<true, false, kAct>(g, own, lanes, t, n, j0, ready))
+               : gated_tile<false, true, kAct>(g, own, lanes, t, n, j0, ready);
+}
+// The same where the finish is simple.
+template <int kMats, int kAct>
+__device__ __forceinline__ void simple_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, int step)
+{
+    for (int j = j0; j < g.w; j += step) {
+        float v[kMats][16];
+        load_chunk(lanes + j, g.w, v);
+        simple_finish<kMats, kAct>(g.ep, reinterpret_cast<uint32_t *>(own), t + j, n, v, threadIdx.x & 31);
+    }
 }
 
 template <bool kGated>
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
         // two plain accumulators: each of a lane quarter's two warps takes one;
         // else they take turns by 8 (16) tokens
         const int j_first = two ? 0 : half * 8, j_step = two ? 8 : 16;
-        const bool simple = epilogue_is_simple(g.ep), bf16 = epilogue_is_bf16(g.ep);
+        const bool simple = epilogue_is_simple(g.ep), bf16 = epilogue_is_bf16(g.ep), silu = g.ep.act == DBF_GATE_SILU;
         Turn acc;
         for (int tile = unit; tile < g.tiles; tile += units, acc.next(g.bufs)) {
             const uint32_t lanes = lanes0 + acc.buf * accs * g.w;
@@ -313,11 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             if (simple) {
                 if (!bar_wait(full, acc.phase, abort)) break;
                 tc_fence_after();
-                for (int j = 2 * j_first; j < g.w; j += 2 * j_step) {
-                    float v[kMats][16];
-                    load_chunk(lanes + j, g.w, v);
-                    simple_finish<kMats>(g.ep, reinterpret_cast<uint32_t *>(own), t - (lane >> 2) + j, n - (lane & 3) * 8, v, lane);
-                }
+                if (!kGated || silu)
+                    simple_tile<kMats, DBF_GATE_SILU>(g, own, lanes, t - (lane >> 2), n - (lane & 3) * 8, 2 * j_first, 2 * j_step);
+                else
+                    simple_tile<kMats, DBF_GATE_GELU>(g, own, lanes, t - (lane >> 2), n - (lane & 3) * 8, 2 * j_first, 2 * j_step);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(empty);
@@ -325,18 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             }
             if constexpr (kGated) {
                 if (bf16) {
-                    const bool add = g.ep.g_add != nullptr, save = g.ep.g8 != nullptr;
-                    if (add) prefetch_addends(g.ep, t - (lane >> 2), g.w, n - (lane & 3) * 8 - quarter * 32, warp - 2 - kScaleWarps);
+                    if (g.ep.g_add) prefetch_addends(g.ep, t - (lane >> 2), g.w, n - (lane & 3) * 8 - quarter * 32, warp - 2 - kScaleWarps);
                     auto ready = [&] {
                         const bool ok = bar_wait(full, acc.phase, abort);
                         tc_fence_after();
                         return ok;
                     };
                     const int64_t t16 = t - (lane >> 2) + (lane >> 1);
-                    const int n16 = n - (lane & 3) * 8 + (lane & 1) * 16;
-                    const bool ok = add ? (save ? gated_tile<true, true>(g, own, lanes, t16, n16, half * 16, ready)
-                                                : gated_tile<true, false>(g, own, lanes, t16, n16, half * 16, ready))
-                                        : gated_tile<false, true>(g, own, lanes, t16, n16, half * 16, ready);
+                    const int n16 = n - (lane & 3) * 8 + (lane & 1) * 8;
+                    const bool ok = silu ? gated_tile<DBF_GATE_SILU>(g, own, lanes, t16, n16, half * 16, ready)
+                                         : gated_tile<DBF_GATE_GELU>(g, own, lanes, t16, n16, half * 16, ready);
                     if (!ok) break;
                     tc_fence_before();
                     __syncwarp();

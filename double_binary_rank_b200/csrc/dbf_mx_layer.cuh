@@ -157,7 +157,7 @@ __device__ __forceinline__ bool epilogue_is_simple(const Epilogue &e)
 }
 // n0: the warp's first column; own: kTurnFloats words; slot: which column the
 // lane holds
-template <int kMats>
+template <int kMats, int kAct = DBF_GATE_SILU>
 __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, int64_t t0, int n0, const float (&v)[kMats][16],
                                               int slot)
 {
@@ -168,7 +168,7 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
         float *y = static_cast<float *>(e.y) + t0 * e.N + n;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (j < left && n < e.N) y[j * static_cast<int64_t>(e.N)] = kMats == 2 ? gate_value(e.act, v[0][j]) * v[kMats - 1][j] : v[0][j];
+            if (j < left && n < e.N) y[j * static_cast<int64_t>(e.N)] = kMats == 2 ? gate_value(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
         return;
     }
     __syncwarp();
@@ -176,8 +176,8 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
     for (int p = 0; p < 8; ++p) {
         float a = v[0][2 * p], b = v[0][2 * p + 1];
         if (kMats == 2) {
-            a = gate_value(e.act, a) * v[kMats - 1][2 * p];
-            b = gate_value(e.act, b) * v[kMats - 1][2 * p + 1];
+            a = gate_value(kAct, a) * v[kMats - 1][2 * p];
+            b = gate_value(kAct, b) * v[kMats - 1][2 * p + 1];
         }
         const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
         own[p * 36 + slot] = *reinterpret_cast<const uint32_t *>(&w);
@@ -198,8 +198,9 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
 
 // The same rows for the gated block with bf16 addends and 8-bit copies of g and
 // u, 16 tokens at once, a lane sixteen columns of one token: two lanes hold a
-// block, so its scale is found once for sixteen values and the codes are one
-// 16-byte store.
+// block, so its scale is found once for sixteen values. They are columns 8 s ..
+// 8 s + 7 and 16 more than these, s the lane's parity, so that the two lanes'
+// 16-byte accesses meet in whole 32-byte sectors.
 __device__ __forceinline__ bool epilogue_is_bf16(const Epilogue &e)
 {
     return epilogue_vec(e) && e.yd == DBF_BF16 && !e.g_add == !e.u_add && (!e.g_add || e.add_dt == DBF_BF16);
@@ -208,22 +209,24 @@ __device__ __forceinline__ bool epilogue_is_bf16(const Epilogue &e)
 template <bool kAdd>
 __device__ __forceinline__ void gated_reads(const Epilogue &e, int64_t t, int c, bool on, uint4 (&x)[2][2])
 {
-    if (!kAdd) return;
+    if constexpr (kAdd) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool in = on && t < e.T && c + 8 * i < e.N;
-        const int64_t at = t * e.N + c + 8 * i;
-        x[0][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.g_add) + at) : make_uint4(0u, 0u, 0u, 0u);
-        x[1][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.u_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i) {
+            const bool in = on && t < e.T && c + 16 * i < e.N;
+            const int64_t at = t * e.N + c + 16 * i;
+            x[0][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.g_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+            x[1][i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.u_add) + at) : make_uint4(0u, 0u, 0u, 0u);
+        }
     }
 }
-// 16 tokens x 32 columns, a column per lane, to 16 columns of token lane / 2
+// 16 tokens x 32 columns, a column per lane, to 16 columns of token lane / 2;
+// those of an even lane are put in front
 __device__ __forceinline__ void turn16(float *own, const float (&col)[16], float (&row)[16])
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, slot = (lane & 7) | (lane & 8) << 1 | (lane & 16) >> 1;
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) own[j * 36 + lane] = col[j];
+    for (int j = 0; j < 16; ++j) own[j * 36 + slot] = col[j];
     __syncwarp();
     const float4 *p = reinterpret_cast<const float4 *>(own + (lane >> 1) * 36 + (lane & 1) * 16);
 #pragma unroll
@@ -249,15 +252,18 @@ __device__ __forceinline__ void keep8(uint8_t *codes, uint8_t *scales, int64_t p
         w[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
         if (byte == 255u) w[i] = 0u;
     }
-    if (!on || c >= pitch) return;
-    *reinterpret_cast<uint4 *>(codes + t * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    if ((c & 31) == 0) scales[static_cast<int64_t>(c / kBlock) * T + t] = static_cast<uint8_t>(byte);
+    // the lanes swap halves: sixteen neighbouring codes each
+    const bool odd = (threadIdx.x & 1) != 0;
+    const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[0] : w[2], 1), b = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[1] : w[3], 1);
+    const uint4 all = odd ? make_uint4(a, b, w[2], w[3]) : make_uint4(w[0], w[1], a, b);
+    if (!on || (c & ~31) >= pitch) return;
+    *reinterpret_cast<uint4 *>(codes + t * pitch + (c & ~31) + (odd ? 16 : 0)) = all;
+    if (!odd) scales[static_cast<int64_t>(c / kBlock) * T + t] = static_cast<uint8_t>(byte);
 }
-template <bool kAdd, bool kSave>
-__device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int64_t t, int c, const float (&v)[2][16],
-                                             const uint4 (&x)[2][2])
+// The lane's columns of both products, turned, plus what was read for them.
+template <bool kAdd>
+__device__ __forceinline__ void gated_turn(float *own, const float (&v)[2][16], const uint4 (&x)[2][2], float (&r)[2][16])
 {
-    float r[2][16];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         turn16(own, v[m], r[m]);
@@ -273,12 +279,16 @@ __device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int6
             }
         }
     }
+}
+template <bool kSave, int kAct>
+__device__ __forceinline__ void gated_finish(const Epilogue &e, int64_t t, int c, float (&r)[2][16])
+{
     const bool on = t < e.T;
     if (kSave) {
-        if (c + 16 > e.N) {   // rows past the last may have given anything, a NaN too
+        if (c + 24 > e.N) {   // rows past the last may have given anything, a NaN too
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (c + j >= e.N) r[0][j] = r[1][j] = 0.0f;
+                if (c + j + (j & 8) >= e.N) r[0][j] = r[1][j] = 0.0f;
         }
         keep8(e.g8, e.gs, e.pitch8, e.T, t, c, on, r[0]);
         keep8(e.u8, e.us, e.pitch8, e.T, t, c, on, r[1]);
@@ -288,8 +298,8 @@ __device__ __forceinline__ void gated_finish(const Epilogue &e, float *own, int6
     for (int i = 0; i < 2; ++i) {
         float h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = gate_value(e.act, r[0][8 * i + j]) * r[1][8 * i + j];
-        store8(e.y, DBF_BF16, t * e.N, c + 8 * i, e.N, true, h);
+        for (int j = 0; j < 8; ++j) h[j] = gate_value(kAct, r[0][8 * i + j]) * r[1][8 * i + j];
+        store8(e.y, DBF_BF16, t * e.N, c + 16 * i, e.N, true, h);
     }
 }
 

@@ -159,14 +159,6 @@ __device__ __forceinline__ void tma_2d_pair(void *dst, const CUtensorMap *map, i
         "l"(map), "r"(c0), "r"(c1), "r"(leader_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_3d_pair(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(leader_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -187,13 +179,9 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
            static_cast<uint64_t>(1u) << 46;
 }
 
-template <int kCtas>
 __device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc)
 {
-    if (kCtas == 2)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
 // kind::mxf4 (both E2M1, E8M0 scale per 32): K = 64, so two scales a row and
@@ -260,11 +248,13 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols)
 }
 
 // 8 or 16 columns of this warp's 32 tensor-memory lanes, of one or two
-// accumulators (each waits for its loads: the outputs must not be
-// touched before)
+// accumulators (each waits for its loads: the outputs must not be touched
+// before). The whole warp loads: it is brought together first, since lanes
+// without a token may have left the chunk before early.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[1][8])
 {
     uint32_t r[8];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
@@ -277,6 +267,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[1][8])
 __device__ __forceinline__ void tmem_ld8(uint32_t t0, uint32_t t1, float (&v)[2][8])
 {
     uint32_t r[16];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
@@ -291,6 +282,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t t0, uint32_t t1, float (&v)[2]
 __device__ __forceinline__ void tmem_ld16(uint32_t t0, uint32_t t1, float (&v)[2][16])
 {
     uint32_t r[32];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%32];\n\t"
@@ -309,6 +301,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t0, uint32_t t1, float (&v)[2
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[1][16])
 {
     uint32_t r[16];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%16];\n\t"
