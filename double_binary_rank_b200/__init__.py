@@ -575,7 +575,10 @@ def forward_segmented(table: AdapterTable, seg_offsets: torch.Tensor, seg_adapte
 
 # ---- 4-bit base layer, gated block, 8-bit activations -------------------------
 # These take the device from their tensors: the call runs with that device
-# current and, without an explicit stream, on its current stream.
+# current and, without an explicit stream, on its current stream. An explicit
+# stream is the current one for as long as the call, so that what the binding
+# does around the kernel (a contiguous copy, a new output, the workspace) is
+# ordered with it.
 
 _GATES = {"silu": 0, "gelu": 1}
 _ACT = (torch.float32, torch.bfloat16)
@@ -591,21 +594,31 @@ except ImportError:
         return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _enter(t: torch.Tensor, stream) -> Tuple[int, Optional[int]]:
-    """(stream handle, device to go back to after the call or None); makes the
-    tensor's device current."""
+def _enter(t: torch.Tensor, stream) -> Tuple[int, object]:
+    """(stream handle, what _leave restores); makes the tensor's device, and an
+    explicit stream, current."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("expected a CUDA tensor")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream: expected one of cuda:{dev}, got one of {stream.device}")
     cur = torch.cuda.current_device()
+    if stream is not None:
+        before = torch.cuda.current_stream(dev)
+        torch.cuda.set_stream(stream)   # makes its device current too
+        return stream.cuda_stream, (cur, before)
     if cur != dev:
         torch.cuda.set_device(dev)
-    return _raw_stream(dev) if stream is None else stream.cuda_stream, None if cur == dev else cur
+    return _raw_stream(dev), None if cur == dev else (cur, None)
 
 
-def _leave(back: Optional[int]) -> None:
-    if back is not None:
-        torch.cuda.set_device(back)
+def _leave(back) -> None:
+    if back is None:
+        return
+    cur, before = back
+    if before is not None:
+        torch.cuda.set_stream(before)
+    torch.cuda.set_device(cur)
 
 
 def _need(t: Optional[torch.Tensor], name: str, shape, dtypes, like: torch.Tensor) -> None:
@@ -641,12 +654,12 @@ def mx4_quantize(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales
 
     Returns (codes [rows, ceil(k/32) * 16], scales [row tiles, block tiles, 32, 4, 4]), uint8."""
     rows, k = src.shape
-    src = src.contiguous()
     cs, ss = _mx4_shapes(rows, k)
-    _need(src, "src", (rows, k), _FLOATS, src)
     _need(status, "status", (1,), _I32, src)
     s, back = _enter(src, stream)
     try:
+        src = src.contiguous()
+        _need(src, "src", (rows, k), _FLOATS, src)
         codes = src.new_empty(cs, dtype=torch.uint8) if codes is None else codes
         scales = src.new_empty(ss, dtype=torch.uint8) if scales is None else scales
         _need(codes, "codes", cs, _U8, src)
@@ -799,11 +812,11 @@ def _act8(a: Act8, rows: int, cols: int, like: torch.Tensor) -> DbfAct8C:
 def act8_save(src: torch.Tensor, out: Optional[Act8] = None, status: Optional[torch.Tensor] = None, stream=None) -> Act8:
     """Keep a rows x cols float tensor in 8 bits (dbf_act8_save)."""
     rows, cols = src.shape
-    src = src.contiguous()
-    _need(src, "src", (rows, cols), _FLOATS, src)
     _need(status, "status", (1,), _I32, src)
     s, back = _enter(src, stream)
     try:
+        src = src.contiguous()
+        _need(src, "src", (rows, cols), _FLOATS, src)
         out = Act8._like(rows, cols, src) if out is None else out
         _check(_lib.dbf_act8_save(_ptr(src), _DT[src.dtype], rows, cols, _act8(out, rows, cols, src), _ptr(status), s),
                "dbf_act8_save")

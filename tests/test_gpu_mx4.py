@@ -431,6 +431,32 @@ def test_two_streams_at_once(dbf):
     assert all(dbf.workspace_status(w) == 0 for w in wss)
 
 
+def test_an_explicit_stream_orders_the_copies_and_workspaces_too(dbf):
+    """The input is written late on the stream that is passed: the contiguous copy of a
+    strided input, the new outputs and the workspace's header belong on it as well."""
+    rng = np.random.default_rng(6)
+    T, M, N = 37, 96, 160
+    L = layer_of(dbf, exact_operand(rng, N, M))
+    late = torch.tensor(exact_operand(rng, T, M)).float().cuda()
+    want = dbf.mx4_quantize(late), dbf.act8_save(late), dbf.mx4_forward(L, late), dbf.mx4_gated_forward(L, L, late)
+    x, wide = torch.zeros(T, M, device="cuda"), torch.zeros(T, 2 * M, device="cuda")
+    busy = torch.ones(1 << 27, device="cuda")
+    st, own = torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(40):   # several milliseconds
+            busy.mul_(1.0)
+        x.copy_(late)
+        wide[:, ::2].copy_(late)
+    got = (dbf.mx4_quantize(wide[:, ::2], stream=st), dbf.act8_save(wide[:, ::2], stream=st), dbf.mx4_forward(L, x, stream=st),
+           dbf.mx4_gated_forward(L, L, x, stream=st))
+    assert torch.cuda.current_stream() == own
+    st.synchronize()
+    assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1], want[0][1])
+    assert torch.equal(got[1].codes, want[1].codes) and torch.equal(got[1].scales, want[1].scales)
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+
+
 def test_offsets_past_32_bits(dbf):
     """y, x and an 8-bit activation of more than 2^31 elements (and more than 2^32 bytes)."""
     T, M, N = 270_001, 32, 8192

@@ -145,3 +145,12 @@ def test_sizes_that_32_bits_cannot_count(dbf, lib):
     L = dbf.DbfMx4LayerC(32, 64, P, P)
     assert lib.dbf_mx4_forward(by(L), P, dbf.F32, P, dbf.F32, big, 0, P, 1 << 62, None) == dbf.ERR_UNSUPPORTED
     assert lib.dbf_mx4_backward(by(L), P, dbf.F32, P, dbf.F32, big // 3, 0, P, 1 << 62, None) == dbf.ERR_UNSUPPORTED
+
+
+def test_a_stream_of_another_device_is_refused(dbf):
+    from types import SimpleNamespace
+    on0 = SimpleNamespace(get_device=lambda: 0)
+    with pytest.raises(ValueError, match="stream"):
+        dbf._enter(on0, SimpleNamespace(device=torch.device("cuda", 1)))
+    with pytest.raises(ValueError, match="CUDA"):
+        dbf._enter(SimpleNamespace(get_device=lambda: -1), None)
