@@ -279,7 +279,8 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
             // Shared memory in proportion to tensor memory: whatever CTAs share an SM,
             // of this or another of these kernels, their columns are always there, so
             // that no CTA waits for them while another of its cluster waits at the
-            // exchange.
+            // exchange. (The other kernels with tensor memory take 192 KB at least:
+            // what is left beside them holds no CTA of this one, two stages and more.)
             const int cols = mats * p.w + 8 * mats + 8;
             p.tmem_cols = 32;
             while (p.tmem_cols < cols) p.tmem_cols *= 2;

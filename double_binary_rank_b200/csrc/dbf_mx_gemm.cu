@@ -11,11 +11,11 @@
 // accumulators of 256 x w: two row blocks of W, or 256 rows of Wg and the same
 // rows of Wu, so the gated block finds g and u of one element in one place. At
 // four times the bf16 rate the operands' way into the SM bounds the tile, not
-// the MMA: 512 x 240 takes 50 KB per 960 cycles of MMA and SM; a double-buffered
-// 256 x 240 would take 34 KB per 480.
+// the MMA: 512 x 224 takes 50 KB per 896 cycles of MMA and SM; a double-buffered
+// 256 x 224 would take 32 KB per 448.
 //   warp 0      TMA: per stage of 256 columns, 2 x 128 rows of codes (128-byte
 //               swizzle), w/2 token rows, and their scale tiles;
-//   warp 1      tensor memory; in CTA 0 one thread issues eight MMAs a stage;
+//   warp 1      tensor memory; in CTA 0 one elected thread issues eight MMAs a stage;
 //   warps 2..5  bring the stage's scales into tensor memory, each into its own
 //               32 lanes, through registers. tcgen05.cp would do it too, but
 //               runs in the MMAs' own queue: at about 70 cycles a copy, eight
@@ -25,8 +25,9 @@
 // The token width w is chosen per call (a multiple of 16 up to 224, what 512
 // tensor-memory columns hold beside two buffers of 32 of scales) so that the
 // tiles fill whole waves of pairs; narrower tiles, whose stages take less time
-// than scales need to get there, have up to four buffers. Every wait is bounded; on expiry the status
-// word is set.
+// than scales need to get there, have up to four buffers. 8192^3 takes 216 us: 31
+// of the pre-pass, 156 of the products and 26 of epilogues. Every wait is bounded;
+// on expiry the status word is set.
 #include <algorithm>
 #include <atomic>
 
@@ -473,8 +474,8 @@ int fixed_smem(int mats) { return 1024 + kEpiWarps * mats * kTurnFloats * 4 + st
 // operands' way from L2 (about 45 bytes a cycle and SM, 38 beside a running
 // epilogue) or its share of the ring's round trip, whichever is longest. Wide
 // tiles pay least for their weights' way there: two sets win only where the
-// epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 124 us on
-// one set, 107 us on two; 4096 x 11008 at 2048 tokens: 117 us and 131 us), one
+// epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 112 us on
+// one set, 102 us on two; 4096 x 11008 at 2048 tokens: 109 us and 121 us), one
 // accumulator only where tiles are fewer than pairs.
 Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
 {
