@@ -660,10 +660,10 @@ def mx4_quantize(src: torch.Tensor, codes: Optional[torch.Tensor] = None, scales
     try:
         src = src.contiguous()
         _need(src, "src", (rows, k), _FLOATS, src)
-        codes = src.new_empty(cs, dtype=torch.uint8) if codes is None else codes
-        scales = src.new_empty(ss, dtype=torch.uint8) if scales is None else scales
         _need(codes, "codes", cs, _U8, src)
         _need(scales, "scales", ss, _U8, src)
+        codes = src.new_empty(cs, dtype=torch.uint8) if codes is None else codes
+        scales = src.new_empty(ss, dtype=torch.uint8) if scales is None else scales
         _check(_lib.dbf_mx4_quantize(_ptr(src), _DT[src.dtype], rows, k, _ptr(codes), codes.numel(), _ptr(scales),
                                      scales.numel(), _ptr(status), s), "dbf_mx4_quantize")
     finally:
@@ -890,10 +890,10 @@ def mx4_gated_backward(gate: Mx4Layer, up: Mx4Layer, dh: torch.Tensor, saved: Tu
     sg, su = _act8(saved[0], T, N, dh), _act8(saved[1], T, N, dh)
     s, back = _enter(dh, stream)
     try:
-        dg = torch.empty_like(dh) if dg is None else dg
-        du = torch.empty_like(dh) if du is None else du
         _need(dg, "dg", (T, N), (dh.dtype,), dh)
         _need(du, "du", (T, N), (dh.dtype,), dh)
+        dg = torch.empty_like(dh) if dg is None else dg
+        du = torch.empty_like(dh) if du is None else du
         if want_dx and dx is None:
             if accumulate:
                 raise ValueError("accumulate needs dx")

@@ -431,6 +431,36 @@ def test_two_streams_at_once(dbf):
     assert all(dbf.workspace_status(w) == 0 for w in wss)
 
 
+def test_base_and_adapter_kernels_on_two_streams(dbf):
+    """The base's kernels on one stream while the adapter's run on another (both kinds hold tensor memory, in
+    clusters): the same results as alone. The adapter's fp32 sums may meet in another order: a bf16 step."""
+    from gpu_util import dev_layer, random_layer
+    rng = np.random.default_rng(12)
+    T, M, N, r = 600, 1024, 2048, 512
+    L = layer_of(dbf, exact_operand(rng, N, M))
+    ad = dev_layer(random_layer(rng, M, N, r, 1))
+    x = torch.tensor(exact_operand(rng, T, M)).to(torch.bfloat16).cuda()
+    dy = torch.tensor(rng.integers(-3, 4, (T, N)).astype(np.float64)).to(torch.bfloat16).cuda()
+    wss = [dbf.alloc_workspace(n, "cuda") for n in (max(dbf.mx4_gated_workspace_bytes(L, L, T),
+                                                        dbf.mx4_backward_workspace_bytes(L, T, torch.bfloat16)),
+                                                    max(dbf.workspace_bytes(ad, t) for t in (1, T)))]
+    base = (lambda st: dbf.mx4_forward(L, x[:1], ws=wss[0], stream=st), lambda st: dbf.mx4_gated_forward(L, L, x, ws=wss[0], stream=st),
+            lambda st: dbf.mx4_backward(L, dy, ws=wss[0], stream=st), lambda st: dbf.mx4_forward(L, x[:20], ws=wss[0], stream=st))
+    other = (lambda st: dbf.forward(ad, x, ws=wss[1], stream=st), lambda st: dbf.forward(ad, x[:1], ws=wss[1], stream=st))
+    own = torch.cuda.current_stream()
+    want = [[f(own) for f in fs] for fs in (base, other)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        got.append([[f(st) for f in fs] for fs, st in zip((base, other), streams)])
+    torch.cuda.synchronize()
+    for b, o in got:
+        assert all(torch.equal(a, w) for a, w in zip(b, want[0]))
+        assert all(((a.float() - w.float()).norm() <= 2.0 ** -7 * w.float().norm()).item() for a, w in zip(o, want[1]))
+    assert all(dbf.workspace_status(w) == 0 for w in wss)
+
+
 def test_an_explicit_stream_orders_the_copies_and_workspaces_too(dbf):
     """The input is written late on the stream that is passed: the contiguous copy of a
     strided input, the new outputs and the workspace's header belong on it as well."""
