@@ -293,15 +293,16 @@ __device__ __forceinline__ void load_cols(const void *src, int64_t row_start, in
     for (int i = 0; i < kCols / 8; ++i) r[i] = load_raw8(src, DT, row_start, c + 8 * i, k, kVec);
 }
 
-// Larger magnitudes of two pairs of 16-bit values; NaN wins.
+// Larger magnitudes of two pairs of 16-bit values, in all but the sign bits; NaN
+// wins.
 template <dbf_dtype DT>
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
 {
     uint32_t r;
     if (DT == DBF_BF16)
-        asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     else
-        asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -323,6 +324,7 @@ __device__ __forceinline__ uint32_t block_amax_bits(const Raw8 (&r)[kCols / 8])
     }
 #pragma unroll
     for (int d = 1; d < 32 / kCols; d *= 2) m = max_abs2<DT>(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    m &= 0x7FFF7FFFu;
     const uint32_t hi = m >> 16, lo = m & 0xFFFFu;   // as integers, NaN > infinity > finite
     const uint32_t top = hi > lo ? hi : lo;
     return DT == DBF_BF16 ? top << 16 : __float_as_uint(h2f(static_cast<uint16_t>(top)));

@@ -4,9 +4,9 @@
 // Each kernel reads every input and writes every output once and computes
 // little, so device memory should bound it. A warp takes 256 columns (a lane
 // eight of them, four lanes a block) of four rows, whose loads are all in flight
-// before the first is used; the quantisers of 16-bit types 512, a lane sixteen. The four rows of a 4-bit warp are 32
-// apart: their scales are neighbours in the tiled layout, so a warp writes
-// them as 16-byte vectors. The 8-bit scales lie block by block ([block][row]),
+// before the first is used; the quantisers of 16-bit types 512, a lane sixteen.
+// The four rows of a 4-bit warp are 32 apart: their scales are neighbours in the
+// tiled layout, so a warp writes them as 16-byte vectors. The 8-bit scales lie block by block ([block][row]),
 // the order in which the gated block's epilogue produces them; a CTA gathers
 // them for 32 rows in shared memory and writes 32 bytes at a time.
 #include <type_traits>
@@ -23,10 +23,11 @@ constexpr int kWarps = 8;
 constexpr int kSegment = 256;   // columns of a warp
 
 // kVec: rows are whole aligned vectors of eight values. Integer instructions are
-// what the quantisers run into first (11008 x 4096 bf16, 17 us for the bytes: 30
-// us with eight values to a lane, run-time types and a conversion each; 25 us
-// with packed comparisons and compile-time types, the ALU pipe 82 % busy; 23 us
-// as it stands).
+// what the quantisers run into first (11008 x 4096 bf16, 17.4 us for the bytes:
+// 30 us with eight values to a lane, run-time types and a conversion each; 25 us
+// with packed comparisons and compile-time types, the ALU pipe 82 % busy; 20.3 us
+// with sixteen values to a lane, 19.5 us with comparisons that take the
+// magnitudes themselves).
 template <dbf_dtype DT, bool kVec>
 __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__restrict__ src, int64_t rows, int64_t k,
                                                                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
