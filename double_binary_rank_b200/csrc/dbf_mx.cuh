@@ -278,19 +278,155 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t m)
     return b > m ? b : m;
 }
 
-// How many values of one row a lane takes: sixteen of a 16-bit type in aligned
-// vectors, else eight. The quantisers run out of integer instructions before
-// anything else, and with sixteen the block's scale and its exchange between
-// lanes cost half as many per value.
-template <dbf_dtype DT, bool kVec>
-constexpr int lane_cols() { return DT != DBF_F32 && kVec ? 16 : 8; }
+// How many values of one row a lane takes: sixteen of a 16-bit type, else eight.
+// The quantisers run out of integer instructions before anything else, and with
+// sixteen the block's scale and its exchange between lanes cost half as many per
+// value.
+template <dbf_dtype DT>
+constexpr int lane_cols() { return DT != DBF_F32 ? 16 : 8; }
 
-// Columns c .. c + kCols - 1 of a row as loaded.
+// Words first .. first + kOut - 1 of w, 'first' 0 to 3 at run time.
+template <int kIn, int kOut>
+__device__ __forceinline__ void pick_words(uint32_t (&w)[kIn], uint32_t first, uint32_t (&out)[kOut])
+{
+    static_assert(kIn >= kOut + 3, "enough words");
+#pragma unroll
+    for (int i = 0; i < kOut + 1; ++i) w[i] = first & 2u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) out[i] = first & 1u ? w[i + 1] : w[i];
+}
+
+// load_raw8 in the form of 'vec' where rows start anywhere: the aligned vectors
+// around the eight values, shifted. Single values (each instruction over all
+// lanes' vectors again) only where a vector would leave the tensor, which ends
+// at element 'total'. A 5003 x 6895 bf16 matrix to 4 bits took 65 us in single
+// values, 16 us with rows of whole vectors.
+template <dbf_dtype DT>
+__device__ __forceinline__ Raw8 load_shifted8(const void *src, int64_t row_start, int64_t c, int64_t k, int64_t total)
+{
+    constexpr int kSize = DT == DBF_F32 ? 4 : 2, kVecs = DT == DBF_F32 ? 3 : 2, kWords = 2 * kSize;
+    Raw8 r;
+    r.lo = r.hi = make_uint4(0u, 0u, 0u, 0u);
+    if (c >= k) return r;
+    const uintptr_t base = reinterpret_cast<uintptr_t>(src), at = base + static_cast<uintptr_t>(row_start + c) * kSize;
+    const uint32_t off = static_cast<uint32_t>(at & 15u);
+    const uintptr_t from = at - off;
+    const int vecs = off ? kVecs : kVecs - 1;
+    uint32_t out[8] = {};
+    if (from >= base && from + 16u * vecs <= base + static_cast<uintptr_t>(total) * kSize) {
+        uint32_t w[kWords + 4];   // one more than the eight values take
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint4 q = i < vecs ? reinterpret_cast<const uint4 *>(from)[i] : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        }
+        if constexpr (kSize == 4) {
+            pick_words(w, off >> 2, out);
+        } else {
+            uint32_t p[5];
+            pick_words(w, off >> 2, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = __funnelshift_r(p[i], p[i + 1], (off & 2u) * 8u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c + i >= k) break;
+            if constexpr (kSize == 4)
+                out[i] = reinterpret_cast<const uint32_t *>(at)[i];
+            else
+                out[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[i]) << (i & 1) * 16;
+        }
+    }
+    if (c + 8 > k) {   // the next row's values
+        const int left = static_cast<int>(k - c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= left) {
+                if constexpr (kSize == 4)
+                    out[i] = 0u;
+                else
+                    out[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+            }
+    }
+    r.lo = make_uint4(out[0], out[1], out[2], out[3]);
+    r.hi = make_uint4(out[4], out[5], out[6], out[7]);
+    return r;
+}
+
+// The reverse, a whole warp's call: lane i has columns c = c0 + 8 i of a row that
+// starts anywhere. Each lane stores the aligned vectors that begin in its
+// neighbour's columns and end in its own; single values only at both ends.
+template <dbf_dtype DT>
+__device__ __forceinline__ void store_shifted8(void *dst, int64_t row_start, int64_t c, int64_t k, const float (&v)[8])
+{
+    constexpr int kSize = DT == DBF_F32 ? 4 : 2, kWords = 2 * kSize;
+    const int lane = threadIdx.x & 31;
+    uint32_t own[kWords], out[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if (DT == DBF_F32) {
+            own[i] = __float_as_uint(v[i]);
+        } else if (DT == DBF_BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            own[i] = *reinterpret_cast<const uint32_t *>(&p);
+        } else {
+            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            own[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(dst) + static_cast<uintptr_t>(row_start + c) * kSize;
+    const uint32_t off = static_cast<uint32_t>(at & 15u);   // the same in all lanes
+    const int shift = static_cast<int>(off) / kSize;        // columns of the neighbour in front
+    if constexpr (kSize == 4) {
+        uint32_t w[11];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[3 + i] = own[i];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) w[i] = __shfl_up_sync(0xFFFFFFFFu, own[5 + i], 1);
+        pick_words(w, 3u - (off >> 2), out);
+    } else {
+        uint32_t w[8], p[5];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 + i] = own[i], w[i] = __shfl_up_sync(0xFFFFFFFFu, own[i], 1);
+        const uint32_t first = 16u - off;   // byte; 16: nothing of the neighbour's
+        pick_words(w, first >> 2 & 3u, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = off ? __funnelshift_r(p[i], p[i + 1], (first & 2u) * 8u) : own[i];
+    }
+    auto one = [&](const uint32_t (&w)[kWords], int i, int64_t column) {
+        const uintptr_t to = reinterpret_cast<uintptr_t>(dst) + static_cast<uintptr_t>(row_start + column) * kSize;
+        if constexpr (kSize == 4)
+            *reinterpret_cast<uint32_t *>(to) = w[i];
+        else
+            *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(w[i >> 1] >> (i & 1) * 16);
+    };
+    const int64_t from = c - shift;
+    const int low = lane == 0 ? shift : 0;
+    if (low == 0 && from + 8 <= k) {
+        uint4 *to = reinterpret_cast<uint4 *>(at - off);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) to[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= low && from + i < k) one(out, i, from + i);
+    }
+    if (lane == 31) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i >= 8 - shift && c + i < k) one(own, i, c + i);
+    }
+}
+
+// Columns c .. c + kCols - 1 of a row as loaded. kVec: rows are whole aligned
+// vectors of eight values.
 template <dbf_dtype DT, bool kVec, int kCols>
-__device__ __forceinline__ void load_cols(const void *src, int64_t row_start, int64_t c, int64_t k, Raw8 (&r)[kCols / 8])
+__device__ __forceinline__ void load_cols(const void *src, int64_t row_start, int64_t c, int64_t k, int64_t total, Raw8 (&r)[kCols / 8])
 {
 #pragma unroll
-    for (int i = 0; i < kCols / 8; ++i) r[i] = load_raw8(src, DT, row_start, c + 8 * i, k, kVec);
+    for (int i = 0; i < kCols / 8; ++i)
+        r[i] = kVec ? load_raw8(src, DT, row_start, c + 8 * i, k, true) : load_shifted8<DT>(src, row_start, c + 8 * i, k, total);
 }
 
 // Larger magnitudes of two pairs of 16-bit values, in all but the sign bits; NaN
@@ -308,10 +444,10 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
 
 // fp32 bits of the largest magnitude of the block that this lane and its
 // neighbours (32 / kCols lanes) hold.
-template <dbf_dtype DT, bool kVec, int kCols>
+template <dbf_dtype DT, int kCols>
 __device__ __forceinline__ uint32_t block_amax_bits(const Raw8 (&r)[kCols / 8])
 {
-    if (DT == DBF_F32 || !kVec) {
+    if (DT == DBF_F32) {
         float v[8];
         raw8_values(r[0], DBF_F32, true, v);
         return block_amax(amax_bits8(v));
@@ -332,10 +468,10 @@ __device__ __forceinline__ uint32_t block_amax_bits(const Raw8 (&r)[kCols / 8])
 
 // Eight values times 2^-s of a scale byte, exact (bf16 in pairs: results below
 // its normal range round to the code 0 in any case).
-template <dbf_dtype DT, bool kVec>
+template <dbf_dtype DT>
 __device__ __forceinline__ void scaled_values(const Raw8 &r, uint32_t byte, float (&v)[8])
 {
-    if (DT == DBF_BF16 && kVec) {
+    if (DT == DBF_BF16) {
         const uint32_t f = byte == 255u ? 0u : (254u - byte) << 7, f2 = f | f << 16;
         const uint32_t a[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
 #pragma unroll
@@ -348,32 +484,32 @@ __device__ __forceinline__ void scaled_values(const Raw8 &r, uint32_t byte, floa
         return;
     }
     const float inv = inv_scale(byte);
-    raw8_values(r, DT, kVec, v);
+    raw8_values(r, DT, true, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
 }
 
 // A lane's values to codes (eight to a word, or four); its neighbours hold the
 // rest of the block. Sets the block's scale byte.
-template <dbf_dtype DT, bool kVec, int kCols>
+template <dbf_dtype DT, int kCols>
 __device__ __forceinline__ void quantize_e2m1(const Raw8 (&r)[kCols / 8], uint32_t &byte, uint32_t (&w)[kCols / 8])
 {
-    byte = scale_byte4(block_amax_bits<DT, kVec, kCols>(r));
+    byte = scale_byte4(block_amax_bits<DT, kCols>(r));
 #pragma unroll
     for (int i = 0; i < kCols / 8; ++i) {
         float v[8];
-        scaled_values<DT, kVec>(r[i], byte, v);
+        scaled_values<DT>(r[i], byte, v);
         w[i] = byte == 255u ? 0u : e2m1x8(v);
     }
 }
-template <dbf_dtype DT, bool kVec, int kCols>
+template <dbf_dtype DT, int kCols>
 __device__ __forceinline__ void quantize_e4m3(const Raw8 (&r)[kCols / 8], uint32_t &byte, uint32_t (&w)[kCols / 4])
 {
-    byte = scale_byte8(block_amax_bits<DT, kVec, kCols>(r));
+    byte = scale_byte8(block_amax_bits<DT, kCols>(r));
 #pragma unroll
     for (int i = 0; i < kCols / 8; ++i) {
         float v[8];
-        scaled_values<DT, kVec>(r[i], byte, v);
+        scaled_values<DT>(r[i], byte, v);
         w[2 * i] = byte == 255u ? 0u : e4m3x4(v[0], v[1], v[2], v[3]);
         w[2 * i + 1] = byte == 255u ? 0u : e4m3x4(v[4], v[5], v[6], v[7]);
     }

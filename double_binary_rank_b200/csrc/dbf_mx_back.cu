@@ -464,7 +464,10 @@ __global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy
     if (c >= ld) return;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += static_cast<int64_t>(gridDim.x) * 8) {
         float v[8];
-        load8(dy, dt, t * N, c, N, vec, v);
+        const Raw8 in = vec             ? load_raw8(dy, dt, t * N, c, N, true)
+                        : dt == DBF_F32 ? load_shifted8<DBF_F32>(dy, t * N, c, N, T * N)
+                                        : load_shifted8<DBF_BF16>(dy, t * N, c, N, T * N);
+        raw8_values(in, dt, true, v);
         store_planes(op, ld, T * ld, t, c, planes, v);
     }
     griddep_launch();   // at the end: the product's CTAs would take this kernel's registers
@@ -503,16 +506,17 @@ __global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const
         const int64_t at = (row + 8 * i) * a.pitch8 + c;
         wg[i] = on ? *reinterpret_cast<const uint2 *>(a.g8 + at) : make_uint2(0u, 0u);
         wu[i] = on ? *reinterpret_cast<const uint2 *>(a.u8 + at) : make_uint2(0u, 0u);
-        in[i] = load_raw8(a.dh, DT, (row + 8 * i) * a.N, on ? c : a.N, a.N, kVec);
+        in[i] = kVec ? load_raw8(a.dh, DT, (row + 8 * i) * a.N, on ? c : a.N, a.N, true)
+                     : load_shifted8<DT>(a.dh, (row + 8 * i) * a.N, on ? c : a.N, a.N, a.T * a.N);
     }
     __syncthreads();
-    if (c < a.pitch8) {
+    if (!kVec || c < a.pitch8) {   // store_shifted8 is the whole warp's
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (8 * i >= left) break;
             const int64_t t = row + 8 * i;
             float dh[8], g[8], u[8];
-            raw8_values(in[i], DT, kVec, dh);
+            raw8_values(in[i], DT, true, dh);
             const float sg = scale_value(sc[0][lane >> 2][8 * i + warp]), su = scale_value(sc[1][lane >> 2][8 * i + warp]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -527,8 +531,13 @@ __global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const
                     u[4 * h + j] = dh[4 * h + j] * value;
                 }
             }
-            store8(a.dg, DT, t * a.N, c, a.N, kVec, g);
-            store8(a.du, DT, t * a.N, c, a.N, kVec, u);
+            if (kVec) {
+                store8(a.dg, DT, t * a.N, c, a.N, true, g);
+                store8(a.du, DT, t * a.N, c, a.N, true, u);
+            } else {
+                store_shifted8<DT>(a.dg, t * a.N, c, a.N, g);
+                store_shifted8<DT>(a.du, t * a.N, c, a.N, u);
+            }
             if (kOperands && c < a.ld) {
                 // columns past the last are not read: the maps end at column N
 #pragma unroll
@@ -561,6 +570,17 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + (threadIdx.x & 31)) * 8;
     const bool vec = epilogue_vec(e);
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < e.T; t += static_cast<int64_t>(gridDim.x) * 8) {
+        if (!vec) {   // single values: neighbouring lanes take neighbouring ones
+            for (int i = 0; i < 8; ++i) {
+                const int64_t at = static_cast<int64_t>(blockIdx.y) * 256 + i * 32 + (threadIdx.x & 31);
+                if (at >= N) break;
+                const float v = e.accumulate ? load_act(e.y, e.yd, t * N + at) : 0.0f;
+                float sum = 0.0f;
+                for (int s = 0; s < splits; ++s) sum += partial[s * plane + t * N + at];
+                store_act(e.y, e.yd, t * N + at, sum + v);
+            }
+            continue;
+        }
         Raw8 x[1];
         epilogue_reads<false>(e, t, static_cast<int>(c), c < N, x);
         float v[1][8] = {};

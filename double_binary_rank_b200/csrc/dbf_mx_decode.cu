@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(kThreads) mx_decode_kernel(
                 uint32_t byte, q[1];
                 const Raw8 r[1] = {in[i]};
                 if (g.xd == DBF_BF16 && g.vec)
-                    quantize_e2m1<DBF_BF16, true, 8>(r, byte, q);
+                    quantize_e2m1<DBF_BF16, 8>(r, byte, q);
                 else   // fp32 values, loaded as they are or one by one
-                    quantize_e2m1<DBF_F32, true, 8>(r, byte, q);
+                    quantize_e2m1<DBF_F32, 8>(r, byte, q);
                 const uint32_t word = tile_scales<8>(byte, lane);
                 uint8_t *xs = xq + ks * x_stage;
                 *reinterpret_cast<uint32_t *>(xs + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = q[0];

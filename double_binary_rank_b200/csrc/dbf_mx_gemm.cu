@@ -137,14 +137,17 @@ __device__ __forceinline__ bool gated_tile(const Args &g, float *own, uint32_t l
                        : gated_tile<true, false, kAct>(g, own, lanes, t, n, j0, ready))
                : gated_tile<false, true, kAct>(g, own, lanes, t, n, j0, ready);
 }
-// The same where the finish is simple.
+// The same where the finish is simple, or rows are no whole vectors.
 template <int kMats, int kAct>
-__device__ __forceinline__ void simple_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, int step)
+__device__ __forceinline__ void column_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, int step, bool simple)
 {
     for (int j = j0; j < g.w; j += step) {
         float v[kMats][16];
         load_chunk(lanes + j, g.w, v);
-        simple_finish<kMats, kAct>(g.ep, reinterpret_cast<uint32_t *>(own), t + j, n, v, threadIdx.x & 31);
+        if (simple)
+            simple_finish<kMats, kAct>(g.ep, reinterpret_cast<uint32_t *>(own), t + j, n, v, threadIdx.x & 31);
+        else
+            column_finish<kMats, kAct>(g.ep, own, t + j, n, v);
     }
 }
 
@@ -327,13 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
             const int n = p * g.row_step + (two ? half * g.row_off : 0) + static_cast<int>(rank) * 128 + quarter * 32 +
                           (lane & 3) * 8;
             const int64_t t = static_cast<int64_t>(c) * g.w + (lane >> 2);
-            if (simple) {
+            if (simple || !epilogue_vec(g.ep)) {
+                if (g.ep.g_add && g.ep.u_add && g.ep.add_dt == DBF_BF16)
+                    prefetch_addends(g.ep, t - (lane >> 2), g.w, n - (lane & 3) * 8 - quarter * 32, warp - 2 - kScaleWarps);
                 if (!bar_wait(full, acc.phase, abort)) break;
                 tc_fence_after();
+                const int64_t t0 = t - (lane >> 2);
+                const int n0 = n - (lane & 3) * 8;
                 if (!kGated || silu)
-                    simple_tile<kMats, DBF_GATE_SILU>(g, own, lanes, t - (lane >> 2), n - (lane & 3) * 8, 2 * j_first, 2 * j_step);
+                    column_tile<kMats, DBF_GATE_SILU>(g, own, lanes, t0, n0, 2 * j_first, 2 * j_step, simple);
                 else
-                    simple_tile<kMats, DBF_GATE_GELU>(g, own, lanes, t - (lane >> 2), n - (lane & 3) * 8, 2 * j_first, 2 * j_step);
+                    column_tile<kMats, DBF_GATE_GELU>(g, own, lanes, t0, n0, 2 * j_first, 2 * j_step, simple);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive_leader(empty);
@@ -405,20 +412,20 @@ __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict_
 {
     griddep_wait();   // the workspace may still be read by the call before
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kCols = lane_cols<DT, kVec>();
+    constexpr int kCols = lane_cols<DT>();
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kCols;
     const int64_t nb = blocks(M), pitch = nb * 16, tiles = scale_tiles(M);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + warp;
     const int left = static_cast<int>(T - row < 32 ? T - row : 32);   // row + 8 i exists where 8 i < left
     Raw8 in[4][kCols / 8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_cols<DT, kVec, kCols>(x, (row + 8 * i) * M, 8 * i < left ? c : M, M, in[i]);
+    for (int i = 0; i < 4; ++i) load_cols<DT, kVec, kCols>(x, (row + 8 * i) * M, 8 * i < left ? c : M, M, T * M, in[i]);
     uint8_t *out = codes + row * pitch + c / 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i, out += 8 * pitch) {
         const int r = static_cast<int>(row) + 8 * i;
         uint32_t byte, q[kCols / 8];
-        quantize_e2m1<DT, kVec, kCols>(in[i], byte, q);
+        quantize_e2m1<DT, kCols>(in[i], byte, q);
         const uint32_t word = tile_scales<kCols>(byte, lane);
         if (8 * i >= left) continue;
         if (c < nb * kBlock) store_words(out, q);
@@ -547,7 +554,7 @@ cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const bool vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
-    const int cols = 32 * (vec && c.xd == DBF_BF16 ? lane_cols<DBF_BF16, true>() : lane_cols<DBF_F32, true>());
+    const int cols = 32 * (c.xd == DBF_BF16 ? lane_cols<DBF_BF16>() : lane_cols<DBF_F32>());
     cfg.gridDim = dim3(static_cast<unsigned>((c.T + 31) / 32), static_cast<unsigned>((c.M + cols - 1) / cols));
     cfg.blockDim = dim3(256);
     cfg.stream = s;

@@ -145,15 +145,52 @@ __device__ __forceinline__ void turn8(float *own, const float (&col)[kMats][8], 
     }
 }
 
-// The epilogue where nothing but the products is read and the output is fp32, or
-// bf16 with rows of whole 16-byte vectors: 16 tokens at once are finished as they
-// come, a column of 16 tokens per lane. fp32 is stored so (a warp's lanes are 128
-// bytes of a row); bf16 is turned as pairs of tokens in one word: a third of the
+// The epilogue where nothing but the products is read: 16 tokens at once are
+// finished as they come, a column of 16 tokens per lane. fp32, and rows that are no
+// whole 16-byte vectors, are stored so (a warp's lanes are 128 or 64 bytes of a
+// row); other bf16 is turned as pairs of tokens in one word: a third of the
 // instructions of the general one, whose issue bounds the prefill kernel's
 // epilogue.
 __device__ __forceinline__ bool epilogue_is_simple(const Epilogue &e)
 {
-    return (e.yd == DBF_F32 || epilogue_vec(e)) && !e.accumulate && !e.g_add && !e.u_add && !e.g8;
+    return !e.accumulate && !e.g_add && !e.u_add && !e.g8;
+}
+// A lane's column of 16 tokens of a T x N matrix as loaded (all loads before the
+// first use), added to v, and stored from it. n: the column.
+__device__ __forceinline__ void read_column(const void *src, dbf_dtype dt, const Epilogue &e, int64_t t0, int n, uint32_t (&a)[16])
+{
+    const int left = n < e.N && src ? static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16) : 0;
+    const int64_t at = t0 * e.N + n, step = e.N;
+    if (dt == DBF_F32) {
+        const uint32_t *p = static_cast<const uint32_t *>(src) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = j < left ? p[j * step] : 0u;
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = j < left ? p[j * step] : 0u;
+    }
+}
+__device__ __forceinline__ void add_column(const uint32_t (&a)[16], dbf_dtype dt, float (&v)[16])
+{
+    const int shift = dt == DBF_F32 ? 0 : 16;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(a[j] << shift);
+}
+template <int kMats, int kAct>
+__device__ __forceinline__ void store_column(const Epilogue &e, int64_t t0, int n, const float (&v)[kMats][16])
+{
+    const int left = n < e.N ? static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16) : 0;
+    const int64_t at = t0 * e.N + n;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float y = kMats == 2 ? gate_value(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
+        if (j >= left) continue;
+        if (e.yd == DBF_F32)
+            static_cast<float *>(e.y)[at + j * static_cast<int64_t>(e.N)] = y;
+        else
+            static_cast<__nv_bfloat16 *>(e.y)[at + j * static_cast<int64_t>(e.N)] = __float2bfloat16_rn(y);
+    }
 }
 // n0: the warp's first column; own: kTurnFloats words; slot: which column the
 // lane holds
@@ -162,13 +199,8 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
                                               int slot)
 {
     const int lane = threadIdx.x & 31;
-    if (e.yd == DBF_F32) {
-        const int n = n0 + slot;
-        const int left = static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16);
-        float *y = static_cast<float *>(e.y) + t0 * e.N + n;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < left && n < e.N) y[j * static_cast<int64_t>(e.N)] = kMats == 2 ? gate_value(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
+    if (e.yd == DBF_F32 || !epilogue_vec(e)) {
+        store_column<kMats, kAct>(e, t0, n0 + slot, v);
         return;
     }
     __syncwarp();
@@ -301,6 +333,43 @@ __device__ __forceinline__ void gated_finish(const Epilogue &e, int64_t t, int c
         for (int j = 0; j < 8; ++j) h[j] = gate_value(kAct, r[0][8 * i + j]) * r[1][8 * i + j];
         store8(e.y, DBF_BF16, t * e.N, c + 16 * i, e.N, true, h);
     }
+}
+
+// Rows that are no whole 16-byte vectors, where more is read or kept: everything
+// but the 8-bit copies, whose rows are, stays a column to a lane. Eight values to a
+// lane would be as many accesses of single values, each over eight rows instead of
+// one (2 x (209 -> 10325) at 3484 tokens with addends: 521 us).
+template <int kMats, int kAct>
+__device__ __forceinline__ void column_finish(const Epilogue &e, float *own, int64_t t0, int n0, float (&v)[kMats][16])
+{
+    const int lane = threadIdx.x & 31, n = n0 + lane;
+    if (kMats == 2) {
+        if (e.g_add || e.u_add) {
+            uint32_t a[2][16];
+            read_column(e.g_add, e.add_dt, e, t0, n, a[0]);
+            read_column(e.u_add, e.add_dt, e, t0, n, a[1]);
+            add_column(a[0], e.add_dt, v[0]);
+            add_column(a[1], e.add_dt, v[kMats - 1]);
+        }
+        if (e.g8) {
+#pragma unroll
+            for (int m = 0; m < kMats; ++m) {
+                float r[16];
+                if (n >= e.N) {   // rows past the last may have given anything, a NaN too
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[m][j] = 0.0f;
+                }
+                turn16(own, v[m], r);
+                const int64_t t = t0 + (lane >> 1);
+                keep8(m ? e.u8 : e.g8, m ? e.us : e.gs, e.pitch8, e.T, t, n0 + (lane & 1) * 8, t < e.T, r);
+            }
+        }
+    } else if (e.accumulate) {
+        uint32_t a[16];
+        read_column(e.y, e.yd, e, t0, n, a);
+        add_column(a, e.yd, v[0]);
+    }
+    store_column<kMats, kAct>(e, t0, n, v);
 }
 
 // The workspace of a product: x's codes, and its scales in whole tiles of 128

@@ -38,14 +38,14 @@ __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__re
     // four groups of 32
     const int64_t tile = blockIdx.x / (32 / kWarps);
     const int r32 = static_cast<int>(blockIdx.x % (32 / kWarps)) * kWarps + warp;
-    constexpr int kCols = lane_cols<DT, kVec>();
+    constexpr int kCols = lane_cols<DT>();
     const int64_t row = tile * 128 + r32, c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kCols;
     const int64_t nb = blocks(k), pitch = nb * 16, tiles = scale_tiles(k);
     const int left = static_cast<int>(rows - row < 128 ? rows - row : 128);   // row + 32 g exists where 32 g < left
     Raw8 x[kRowsPerWarp][kCols / 8];
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g)
-        load_cols<DT, kVec, kCols>(src, (row + 32 * g) * k, 32 * g < left ? c : k, k, x[g]);
+        load_cols<DT, kVec, kCols>(src, (row + 32 * g) * k, 32 * g < left ? c : k, k, rows * k, x[g]);
     uint32_t words[kRowsPerWarp];
     bool bad = false;
     uint8_t *out = codes + row * pitch + c / 2;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(32 * kWarps) quantize4_kernel(const void *__re
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g, out += 32 * pitch) {
         uint32_t byte, w[kCols / 8];
-        quantize_e2m1<DT, kVec, kCols>(x[g], byte, w);
+        quantize_e2m1<DT, kCols>(x[g], byte, w);
         bad |= byte == 255u;
         if (in && 32 * g < left) store_words(out, w);
         words[g] = tile_scales<kCols>(byte, lane);
@@ -74,16 +74,17 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize4_kernel(const uint8_t 
     const int64_t tile = blockIdx.x / (32 / kWarps);
     const int r32 = static_cast<int>(blockIdx.x % (32 / kWarps)) * kWarps + warp;
     const int64_t row = tile * 128 + r32, c = static_cast<int64_t>(blockIdx.y) * kSegment + lane * 8;
-    if (c >= k) return;
+    if (kVec && c >= k) return;
     const int64_t pitch = code_pitch(k), tiles = scale_tiles(k);
     const int left = static_cast<int>(rows - row < 128 ? rows - row : 128);
     // the scales of the four rows and four blocks of this half-warp: 16 bytes
-    const uint4 s4 = *reinterpret_cast<const uint4 *>(scales + (tile * tiles + (c >> 7)) * 512 + r32 * 16);
+    const bool in_row = kVec || c < k;
+    const uint4 s4 = in_row ? *reinterpret_cast<const uint4 *>(scales + (tile * tiles + (c >> 7)) * 512 + r32 * 16) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
     const uint8_t *in = codes + row * pitch + c / 2;
     uint32_t w[kRowsPerWarp];
 #pragma unroll
-    for (int g = 0; g < kRowsPerWarp; ++g, in += 32 * pitch) w[g] = 32 * g < left ? *reinterpret_cast<const uint32_t *>(in) : 0u;
+    for (int g = 0; g < kRowsPerWarp; ++g, in += 32 * pitch) w[g] = in_row && 32 * g < left ? *reinterpret_cast<const uint32_t *>(in) : 0u;
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g) {
         if (32 * g >= left) break;
@@ -92,7 +93,10 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize4_kernel(const uint8_t 
         from_e2m1x8(w[g], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= s;
-        store8(dst, DT, (row + 32 * g) * k, c, k, kVec, v);
+        if (kVec)
+            store8(dst, DT, (row + 32 * g) * k, c, k, true, v);
+        else
+            store_shifted8<DT>(dst, (row + 32 * g) * k, c, k, v);
     }
 }
 
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps) act8_save_kernel(const void *__re
                                                                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                                 int32_t *status)
 {
-    constexpr int kCols = lane_cols<DT, kVec>();
+    constexpr int kCols = lane_cols<DT>();
     __shared__ uint8_t gather[kCols][32];   // kCols blocks: a warp's columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32, row = r0 + warp;
@@ -111,13 +115,13 @@ __global__ void __launch_bounds__(32 * kWarps) act8_save_kernel(const void *__re
     Raw8 x[kRowsPerWarp][kCols / 8];
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g)
-        load_cols<DT, kVec, kCols>(src, (row + kWarps * g) * k, kWarps * g < left ? c : k, k, x[g]);
+        load_cols<DT, kVec, kCols>(src, (row + kWarps * g) * k, kWarps * g < left ? c : k, k, rows * k, x[g]);
     bool bad = false;
     uint8_t *out = codes + row * pitch + c;
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g, out += kWarps * pitch) {
         uint32_t byte, w[kCols / 4];
-        quantize_e4m3<DT, kVec, kCols>(x[g], byte, w);
+        quantize_e4m3<DT, kCols>(x[g], byte, w);
         bad |= byte == 255u;
         if (kWarps * g < left && c < pitch) store_words(out, w);
         if (lane % (32 / kCols) == 0) gather[lane * kCols / 32][g * kWarps + warp] = static_cast<uint8_t>(byte);
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps) act8_load_kernel(const uint8_t *_
     const int64_t b = static_cast<int64_t>(blockIdx.y) * (kSegment / kBlock) + warp;
     gather[warp][lane] = b < nb && r0 + lane < rows ? scales[b * rows + r0 + lane] : 0;
     __syncthreads();
-    if (c >= k) return;
+    if (kVec && c >= k) return;
 #pragma unroll
     for (int g = 0; g < kRowsPerWarp; ++g) {
         if (kWarps * g >= left) break;
@@ -160,7 +164,10 @@ __global__ void __launch_bounds__(32 * kWarps) act8_load_kernel(const uint8_t *_
         from_e4m3x4(w[g].x, lo);
         from_e4m3x4(w[g].y, hi);
         const float v[8] = {lo[0] * s, lo[1] * s, lo[2] * s, lo[3] * s, hi[0] * s, hi[1] * s, hi[2] * s, hi[3] * s};
-        store8(dst, DT, (row + kWarps * g) * k, c, k, kVec, v);
+        if (kVec)
+            store8(dst, DT, (row + kWarps * g) * k, c, k, true, v);
+        else
+            store_shifted8<DT>(dst, (row + kWarps * g) * k, c, k, v);
     }
 }
 
@@ -203,7 +210,7 @@ cudaError_t launch_quantize4(const void *src, dbf_dtype dt, int64_t rows, int64_
 {
     by_type(dt, vectors(src, k), [&](auto type, auto vec) {
         quantize4_kernel<decltype(type)::value, decltype(vec)::value>
-            <<<grid4(rows, k, 32 * lane_cols<decltype(type)::value, decltype(vec)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
+            <<<grid4(rows, k, 32 * lane_cols<decltype(type)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
     });
     return cudaGetLastError();
 }
@@ -223,7 +230,7 @@ cudaError_t launch_act8_save(const void *src, dbf_dtype dt, int64_t rows, int64_
 {
     by_type(dt, vectors(src, k), [&](auto type, auto vec) {
         act8_save_kernel<decltype(type)::value, decltype(vec)::value>
-            <<<grid8(rows, k, 32 * lane_cols<decltype(type)::value, decltype(vec)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
+            <<<grid8(rows, k, 32 * lane_cols<decltype(type)::value>()), 32 * kWarps, 0, s>>>(src, rows, k, codes, scales, status);
     });
     return cudaGetLastError();
 }

@@ -70,6 +70,39 @@ def test_act8_is_exact(dbf, rows, k, kind):
     assert np.array_equal(host(dbf.act8_load(a, dtype=torch.float16)), val.astype(np.float16).astype(np.float64))
 
 
+@pytest.mark.parametrize("rows,k", [(3, 33), (5, 31), (7, 250), (9, 255), (66, 257), (130, 511), (37, 1371), (65, 2050)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_rows_that_start_anywhere(dbf, rows, k, kind, first):
+    """Rows that are no whole vectors, in tensors that start anywhere: the shifted loads and stores of all formats, and
+    nothing in front of or behind the tensor is touched."""
+    rng = np.random.default_rng(rows * 77 + k)
+    x = rng.standard_normal((rows, k)) * np.exp2(rng.integers(-8, 6, (rows, 1)))
+
+    def place(fill=None):
+        buf = torch.full((first + rows * k + 16,), -7.0, device="cuda", dtype=DT[kind])
+        view = buf[first:first + rows * k].view(rows, k)
+        if fill is not None:
+            view.copy_(torch.tensor(fill).to(DT[kind]))
+        return buf, view
+
+    buf, t = place(x)
+    val4, codes, byte = R.mx4(host(t))
+    packed, scales = R.pack4(codes, byte)
+    gc, gs = dbf.mx4_quantize(t)
+    assert torch.equal(gc.cpu(), torch.from_numpy(packed)) and torch.equal(gs.cpu(), torch.from_numpy(scales))
+    val8, codes8, byte8 = R.act8(host(t))
+    a = dbf.act8_save(t)
+    assert np.array_equal(a.codes.cpu().numpy(), codes8.reshape(rows, -1).astype(np.uint8))
+    assert np.array_equal(a.scales.cpu().numpy(), byte8.T.astype(np.uint8))
+    for load, val in ((lambda o: dbf.mx4_dequantize(gc, gs, rows, k, out=o), val4), (lambda o: dbf.act8_load(a, out=o), val8)):
+        buf, o = place()
+        load(o)
+        want = val.astype(np.float16).astype(np.float64) if kind == "f16" else val
+        assert np.array_equal(host(o), want)
+        assert (buf[:first] == -7.0).all().item() and (buf[first + rows * k:] == -7.0).all().item()
+
+
 @pytest.mark.parametrize("f", ["mx4", "act8"])
 def test_extreme_blocks(dbf, f):
     """Subnormals, the largest values, zeros, negative zeros, NaN and infinities."""
