@@ -299,8 +299,8 @@ __device__ __forceinline__ void pick_words(uint32_t (&w)[kIn], uint32_t first, u
 // load_raw8 in the form of 'vec' where rows start anywhere: the aligned vectors
 // around the eight values, shifted. Single values (each instruction over all
 // lanes' vectors again) only where a vector would leave the tensor, which ends
-// at element 'total'. A 5003 x 6895 bf16 matrix to 4 bits took 65 us in single
-// values, 16 us with rows of whole vectors.
+// at element 'total'. A 5003 x 6895 bf16 matrix to 4 bits and back took 130 us in
+// single values, 68 us so (31 us with rows of whole vectors).
 template <dbf_dtype DT>
 __device__ __forceinline__ Raw8 load_shifted8(const void *src, int64_t row_start, int64_t c, int64_t k, int64_t total)
 {

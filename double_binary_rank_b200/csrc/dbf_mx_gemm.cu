@@ -141,13 +141,18 @@ __device__ __forceinline__ bool gated_tile(const Args &g, float *own, uint32_t l
 template <int kMats, int kAct>
 __device__ __forceinline__ void column_tile(const Args &g, float *own, uint32_t lanes, int64_t t, int n, int j0, int step, bool simple)
 {
+    if (simple) {
+        for (int j = j0; j < g.w; j += step) {
+            float v[kMats][16];
+            load_chunk(lanes + j, g.w, v);
+            simple_finish<kMats, kAct>(g.ep, reinterpret_cast<uint32_t *>(own), t + j, n, v, threadIdx.x & 31);
+        }
+        return;
+    }
     for (int j = j0; j < g.w; j += step) {
         float v[kMats][16];
         load_chunk(lanes + j, g.w, v);
-        if (simple)
-            simple_finish<kMats, kAct>(g.ep, reinterpret_cast<uint32_t *>(own), t + j, n, v, threadIdx.x & 31);
-        else
-            column_finish<kMats, kAct>(g.ep, own, t + j, n, v);
+        column_finish<kMats, kAct>(g.ep, own, t + j, n, v);
     }
 }
 
