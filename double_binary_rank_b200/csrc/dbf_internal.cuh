@@ -161,8 +161,12 @@ cudaError_t launch_act8_load(const uint8_t *codes, const uint8_t *scales, int64_
                              dbf_dtype dt, cudaStream_t s);
 // products: mats 1 (y = W q(x)) or 2 (the gated block)
 bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats);   // else mx_gemm takes the call
-// x to codes and scales (dbf_mx_gemm.cu); token t has scale row t / w * pad + t % w
+// x to codes and scales (dbf_mx_gemm.cu); token t has scale row x_scale_row(t, w, pad)
 cudaError_t mx_quantize_x(const mx::Product &c, int w, int pad, uint8_t *codes, uint8_t *scales, cudaStream_t s);
+// how a call is cut, as dbf_debug_mx4_cut reports it; false: not for few tokens
+bool mx_decode_cut(const mx::Product &c, int sms, int64_t (&cut)[8]);
+void mx_gemm_cut(const mx::Product &c, int sms, int64_t (&cut)[8]);
+void mx_back_cut(const mx::Gradient &c, int mats, int sms, int64_t (&cut)[8]);
 cudaError_t mx_decode(const mx::Product &c, cudaStream_t s);
 cudaError_t mx_gemm(const mx::Product &c, cudaStream_t s);
 size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int mats);

@@ -621,9 +621,9 @@ constexpr int64_t kMaxSplits = 16;
 struct Plan {
     int w, splits;
 };
-Plan plan(int64_t M, int64_t T, int64_t nk)
+Plan plan(int64_t M, int64_t T, int64_t nk, int sms)
 {
-    const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    const int64_t n_p = (M + 255) / 256, pairs = std::max(1, sms / 2);
     Plan best = {16, 1};
     double least = -1;
     for (int w = 16; w <= 512; w += w < 256 ? 16 : 32) {
@@ -641,6 +641,12 @@ Plan plan(int64_t M, int64_t T, int64_t nk)
     return best;
 }
 int64_t stages(int64_t N, int mats, int planes) { return (N + kRowsK - 1) / kRowsK * mats * planes; }
+
+int ring_of(int w)
+{
+    const int fixed = 1024 + kEpiWarps * kTurnFloats * 4 + static_cast<int>(sizeof(Smem));
+    return std::min<int>(kMaxStages, (kMaxSmem - fixed) / stage_bytes(w));
+}
 
 int64_t operand_ld(int64_t N) { return (N + 7) / 8 * 8; }
 bool direct_operand(int64_t N, dbf_dtype d) { return d == DBF_BF16 && N % 8 == 0; }
@@ -673,7 +679,7 @@ dim3 row_grid(int64_t T, int64_t cols)
 cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, int planes, bool pre, size_t partial_at, cudaStream_t s)
 {
     const int mats = c.codes[1] ? 2 : 1;
-    const Plan pl = plan(c.M, c.T, stages(c.N, mats, planes));
+    const Plan pl = plan(c.M, c.T, stages(c.N, mats, planes), device_sms());
     const int w = pl.w, halves = w > 256 ? 2 : 1;
     CUtensorMap map[2];
     for (int m = 0; m < 2; ++m) {
@@ -705,8 +711,7 @@ cudaError_t product(const Gradient &c, const void *const *operand, int64_t ld, i
     g.ep.N = static_cast<int32_t>(c.M), g.ep.T = c.T;
     g.status = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c.ws) + kWsStatusOffset);
 
-    const int fixed = 1024 + kEpiWarps * kTurnFloats * 4 + sizeof(Smem);
-    g.ring = std::min<int>(kMaxStages, (kMaxSmem - fixed) / stage_bytes(w));
+    g.ring = ring_of(w);
     // the largest a launch may ask for, so that no second CTA shares the SM: each allocates all of its tensor memory
     const int smem = kMaxSmem;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(mx_back_kernel), smem);
@@ -741,6 +746,15 @@ size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int
     const int64_t n_p = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
     const size_t partial = static_cast<size_t>(std::min(kMaxSplits * T, pairs * 512 / n_p)) * static_cast<size_t>(M) * 4;
     return kWsHeaderBytes + (direct_operand(N, d) ? 0 : mats * plane_bytes(N, T, d)) + partial;
+}
+
+void mx_back_cut(const Gradient &c, int mats, int sms, int64_t (&cut)[8])
+{
+    const int64_t nk = stages(c.N, mats, pieces(c));
+    const Plan pl = plan(c.M, c.T, nk, sms);
+    const int64_t of[8] = {DBF_MX4_GRADIENT, pl.w, pl.w > 256 ? 2 : 1, pl.splits, ring_of(pl.w), nk,
+                           (c.M + 255) / 256 * ((c.T + pl.w - 1) / pl.w) * pl.splits, 0};
+    std::copy(of, of + 8, cut);
 }
 
 cudaError_t mx_backward(const Gradient &c, cudaStream_t s)

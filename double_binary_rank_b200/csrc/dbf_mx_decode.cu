@@ -250,10 +250,10 @@ struct Shape {
 
 // Split of the columns, ring depth and CTAs to an SM; false when the CTA's
 // columns of x do not fit in shared memory.
-bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
+bool shape(int64_t M, int64_t N, int64_t T, int mats, int64_t sms, Shape &p)
 {
     if (T > kMaxColumns / mats) return false;
-    const int64_t nk = (M + 255) / 256, row_blocks = (N + 127) / 128, sms = device_sms();
+    const int64_t nk = (M + 255) / 256, row_blocks = (N + 127) / 128;
     if (row_blocks > 65535) return false;
     p.w = static_cast<int>((T + 15) / 16 * 16);
     const int64_t stage = mats * int64_t{kABytes + kSfBytes}, x_stage = p.w * 128 + 1024, partials = int64_t{mats} * p.w * 512;
@@ -297,13 +297,22 @@ bool shape(int64_t M, int64_t N, int64_t T, int mats, Shape &p)
 bool mx_decode_fits(int64_t M, int64_t N, int64_t T, int mats)
 {
     Shape p;
-    return shape(M, N, T, mats, p);
+    return shape(M, N, T, mats, device_sms(), p);
+}
+
+bool mx_decode_cut(const Product &c, int sms, int64_t (&cut)[8])
+{
+    Shape p;
+    if (!shape(c.M, c.N, c.T, c.mats, sms, p)) return false;
+    const int64_t of[8] = {DBF_MX4_FEW_TOKENS, p.w, p.split, p.pre, p.ring, p.nks, (c.N + 127) / 128, c.T - 1};
+    std::copy(of, of + 8, cut);
+    return true;
 }
 
 cudaError_t mx_decode(const Product &c, cudaStream_t s)
 {
     Shape p;
-    if (!shape(c.M, c.N, c.T, c.mats, p)) return cudaErrorInvalidValue;
+    if (!shape(c.M, c.N, c.T, c.mats, device_sms(), p)) return cudaErrorInvalidValue;
     const bool gated = c.mats == 2;
     CUtensorMap a[2], sa[2];
     for (int m = 0; m < 2; ++m) {

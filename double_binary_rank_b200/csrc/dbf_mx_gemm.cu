@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(
 
 // Pre-pass: x to codes and scales in the workspace. The scales of the tokens
 // of one tile start a new 128-row scale tile, since a tile of w tokens is no
-// multiple of 128: token t has scale row (t / w) * pad + t % w.
+// multiple of 128 (x_scale_row).
 template <dbf_dtype DT, bool kVec>
 __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict__ x, int64_t T, int64_t M, int w, int pad,
                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(256) quantize_x_kernel(const void *__restrict_
         if (8 * i >= left) continue;
         if (c < nb * kBlock) store_words(out, q);
         if (lane % (128 / kCols) == 0 && (c >> 7) < tiles)
-            *reinterpret_cast<uint32_t *>(scales + scale_at(r / w * pad + r % w, c >> 5, tiles)) = word;
+            *reinterpret_cast<uint32_t *>(scales + scale_at(x_scale_row(r, w, pad), c >> 5, tiles)) = word;
     }
     // Only now: the product's CTAs would take the registers of this kernel's
     // (one of its CTAs beside a product's on an SM against four alone). They
@@ -489,9 +489,9 @@ int fixed_smem(int mats) { return 1024 + kEpiWarps * mats * kTurnFloats * 4 + st
 // epilogue is long against K (2048 x 8192 at 4096 tokens with addends: 112 us on
 // one set, 102 us on two; 4096 x 11008 at 2048 tokens: 109 us and 121 us), one
 // accumulator only where tiles are fewer than pairs.
-Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind)
+Plan plan(int64_t M, int64_t N, int64_t T, int mats, Kind kind, int sms)
 {
-    const int64_t nk = (M + 255) / 256, pairs = std::max(1, device_sms() / 2);
+    const int64_t nk = (M + 255) / 256, pairs = std::max(1, sms / 2);
     Plan p = {};
     double least = -1;
     for (int accs = mats; accs <= 2; ++accs)
@@ -552,6 +552,15 @@ bool tc_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ba
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+void mx_gemm_cut(const Product &c, int sms, int64_t (&cut)[8])
+{
+    const Plan pl = plan(c.M, c.N, c.T, c.mats, kind_of(c), sms);
+    const int64_t rows = c.mats == 2 ? 256 : 256 * pl.accs;
+    const int64_t of[8] = {DBF_MX4_MANY_TOKENS, pl.w, pl.accs, pl.bufs, pl.ring, (c.M + 255) / 256,
+                           (c.N + rows - 1) / rows * ((c.T + pl.w - 1) / pl.w), x_scale_row(static_cast<int>(c.T - 1), pl.w, pl.pad)};
+    std::copy(of, of + 8, cut);
+}
+
 cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint8_t *scales, cudaStream_t s)
 {
     cudaLaunchAttribute attr;
@@ -572,7 +581,7 @@ cudaError_t mx_quantize_x(const Product &c, int w, int pad, uint8_t *codes, uint
 
 cudaError_t mx_gemm(const Product &c, cudaStream_t s)
 {
-    const Plan pl = plan(c.M, c.N, c.T, c.mats, kind_of(c));
+    const Plan pl = plan(c.M, c.N, c.T, c.mats, kind_of(c), device_sms());
     uint8_t *codes = static_cast<uint8_t *>(c.ws) + x_codes_at(), *scales = static_cast<uint8_t *>(c.ws) + x_scales_at(c.M, c.T);
 
     CUtensorMap a[2], sa[2], b, sb;

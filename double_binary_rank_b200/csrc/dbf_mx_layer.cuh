@@ -387,6 +387,10 @@ inline size_t product_workspace_bytes(int64_t M, int64_t T)
     return x_scales_at(M, T) + static_cast<size_t>((T + 15) / 16 * scale_tiles(M) * 512);
 }
 
+// The scale row of token t: each tile of w tokens starts a new one of 128 (pad:
+// the scale rows of a tile). The row passes 2^31 where t does not (w < pad).
+__host__ __device__ inline int64_t x_scale_row(int t, int w, int pad) { return static_cast<int64_t>(t / w) * pad + t % w; }
+
 // One call: a weight (plain) or two of one shape (gated), and its tokens.
 struct Product {
     int64_t M, N, T;

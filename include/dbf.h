@@ -601,6 +601,34 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
                                   const dbf_act8 *saved_u, const void *dh, dbf_dtype dh_dtype, void *dg, void *du, void *dx,
                                   dbf_dtype dx_dtype, int64_t T, int flags, void *ws, size_t ws_bytes, void *stream);
 
+/* How one of the calls above is cut on a GPU of 'sms' SMs, for a layer of shape
+ * M, N (or two of it) and T tokens. Host only, for tests: no pointer is read.
+ * call: which one; DBF_MX4_GATED_ADD is the gated forward with addends,
+ *    DBF_MX4_GATED_SAVE the one that keeps g and u.
+ * dy_dtype, dx_dtype: of the gradients (DBF_F32 or DBF_BF16), else not used.
+ * cut[0] the kernel: DBF_MX4_FEW_TOKENS, DBF_MX4_MANY_TOKENS, DBF_MX4_GRADIENT
+ * cut[1] tokens of a tile
+ * cut[2] few: CTAs of a cluster; many and gradient: accumulators of a set
+ * cut[3] few: 1 if x is quantised by a launch of its own; many: sets of
+ *        accumulators; gradient: parts of the contraction
+ * cut[4] stages in shared memory, cut[5] stages of a CTA (few) or a tile
+ *        (gradient: of all its parts)
+ * cut[6] clusters (few) or tiles
+ * cut[7] the row of x's scales that the last token has (gradient: 0); the
+ *        workspace holds (T + 15) / 16 * 128 of them
+ * Errors: DBF_ERR_INVALID_ARG, DBF_ERR_UNSUPPORTED as the calls'. */
+typedef enum {
+    DBF_MX4_FORWARD = 0,
+    DBF_MX4_GATED = 1,
+    DBF_MX4_GATED_ADD = 2,
+    DBF_MX4_GATED_SAVE = 3,
+    DBF_MX4_BACKWARD = 4,
+    DBF_MX4_GATED_BACKWARD = 5
+} dbf_mx4_call;
+enum { DBF_MX4_FEW_TOKENS = 0, DBF_MX4_MANY_TOKENS = 1, DBF_MX4_GRADIENT = 2 };
+dbf_status dbf_debug_mx4_cut(dbf_mx4_call call, int32_t M, int32_t N, int64_t T, dbf_dtype dy_dtype, dbf_dtype dx_dtype,
+                             int32_t sms, int64_t *cut);
+
 /* Static description of a status code. */
 const char *dbf_status_string(dbf_status s);
 
