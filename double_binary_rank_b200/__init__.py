@@ -115,8 +115,7 @@ _SIGS = {
     "dbf_mx4_gated_backward_workspace_bytes": (_sz, [_MP, _MP, _i64, ctypes.c_int]),
     "dbf_mx4_gated_backward": (ctypes.c_int, [_MP, _MP, ctypes.c_int, _AP, _AP, _vp, ctypes.c_int, _vp, _vp, _vp,
                                               ctypes.c_int, _i64, ctypes.c_int, _vp, _sz, _vp]),
-    "dbf_debug_mx4_cut": (ctypes.c_int, [ctypes.c_int, _i32, _i32, _i64, ctypes.c_int, ctypes.c_int, _i32,
-                                         ctypes.POINTER(ctypes.c_int64)]),
+    "dbf_debug_mx4_cut": (ctypes.c_int, [ctypes.c_int, _i32, _i32, _i64, ctypes.c_int, _i32, ctypes.POINTER(ctypes.c_int64)]),
     "dbf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dbf_version": (ctypes.c_char_p, []),
 }

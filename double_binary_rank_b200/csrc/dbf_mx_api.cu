@@ -257,20 +257,19 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
     return from_cuda(mx_gated_backward(c, act, *saved_g, *saved_u, dg, du, static_cast<cudaStream_t>(stream)));
 }
 
-dbf_status dbf_debug_mx4_cut(dbf_mx4_call call, int32_t M, int32_t N, int64_t T, dbf_dtype dy_dtype, dbf_dtype dx_dtype,
-                             int32_t sms, int64_t *cut)
+dbf_status dbf_debug_mx4_cut(dbf_mx4_call call, int32_t M, int32_t N, int64_t T, dbf_dtype dy_dtype, int32_t sms, int64_t *cut)
 {
     dbf_mx4_layer L = {};
     L.M = M, L.N = N;
     const bool back = call == DBF_MX4_BACKWARD || call == DBF_MX4_GATED_BACKWARD;
     if (call < DBF_MX4_FORWARD || call > DBF_MX4_GATED_BACKWARD || !layer_shape_ok(&L) || T < 1 || sms < 1 || !cut ||
-        (back && (!act_dtype_ok(dy_dtype) || !act_dtype_ok(dx_dtype))))
+        (back && !act_dtype_ok(dy_dtype)))
         return DBF_ERR_INVALID_ARG;
     if (back ? !gradient_ok(&L, T) : !tokens_ok(&L, T)) return DBF_ERR_UNSUPPORTED;
     int64_t of[8];
     if (back) {
         mx::Gradient c = {};
-        c.M = M, c.N = N, c.T = T, c.dyd = dy_dtype, c.dxd = dx_dtype;
+        c.M = M, c.N = N, c.T = T, c.dyd = dy_dtype;
         mx_back_cut(c, call == DBF_MX4_GATED_BACKWARD ? 2 : 1, sms, of);
     } else {
         // only whether there are addends and copies is looked at

@@ -9,9 +9,10 @@
 // so the block-scaled MMA cannot take them: the codes are expanded on chip to
 // bf16, exactly (E2M1 times a power of two has two significant bits), and the
 // product runs at the bf16 rate with fp32 accumulators. bf16 gradients are
-// operands as they are; fp32 ones are cut into bf16 pieces, each a product more:
-// three of eight bits for an fp32 dx (v = p0 + p1 + p2 exactly), two for a bf16
-// one (off by at most 2^-16 of v, against the 2^-8 of rounding dx).
+// operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
+// (v = p0 + p1 + p2 exactly), three times the products, whatever dx's type: what
+// two pieces leave of a value, 2^-16 of it, is not small beside a dx whose terms
+// cancel.
 //
 // A CTA pair owns 256 columns of W x w <= 512 tokens of dx, over 256 tokens as
 // two accumulators (an expanded stage feeds two MMAs a step), contraction over
@@ -410,10 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
 
 // fp32 to three bf16 pieces by truncation: p0 the upper half of the word, then
 // the same of what is left (each difference is exact); the last has at most
-// eight bits left. Of two pieces the second is rounded instead: what is left of
-// v after p0 is below 2^-7 |v|, its eight bits leave at most 2^-9 of that. A NaN
-// or an infinity stays whole in p0.
-__device__ __forceinline__ void split(float v, int planes, uint16_t (&p)[3])
+// eight bits left. A NaN or an infinity stays whole in p0.
+__device__ __forceinline__ void split3(float v, uint16_t (&p)[3])
 {
     const uint32_t b = __float_as_uint(v);
     if ((b & 0x7F800000u) == 0x7F800000u) {
@@ -423,10 +422,6 @@ __device__ __forceinline__ void split(float v, int planes, uint16_t (&p)[3])
     }
     p[0] = static_cast<uint16_t>(b >> 16);
     const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
-    if (planes == 2) {
-        p[1] = __bfloat16_as_ushort(__float2bfloat16_rn(r1));
-        return;
-    }
     p[1] = static_cast<uint16_t>(__float_as_uint(r1) >> 16);
     const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
     p[2] = static_cast<uint16_t>(__float_as_uint(r2) >> 16);
@@ -439,8 +434,8 @@ __device__ __forceinline__ void store_planes(uint16_t *op, int64_t ld, int64_t p
     uint16_t p[8][3];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (planes > 1)
-            split(v[i], planes, p[i]);
+        if (planes == 3)
+            split3(v[i], p[i]);
         else
             p[i][0] = static_cast<uint16_t>(__float_as_uint(v[i]) >> 16);   // a bf16 value already
     }
@@ -640,6 +635,8 @@ Plan plan(int64_t M, int64_t T, int64_t nk, int sms)
     }
     return best;
 }
+// pieces of a gradient's values
+int pieces(dbf_dtype d) { return d == DBF_F32 ? 3 : 1; }
 int64_t stages(int64_t N, int mats, int planes) { return (N + kRowsK - 1) / kRowsK * mats * planes; }
 
 int ring_of(int w)
@@ -652,10 +649,8 @@ int64_t operand_ld(int64_t N) { return (N + 7) / 8 * 8; }
 bool direct_operand(int64_t N, dbf_dtype d) { return d == DBF_BF16 && N % 8 == 0; }
 size_t plane_bytes(int64_t N, int64_t T, dbf_dtype d)
 {
-    return align_up(static_cast<size_t>(T * operand_ld(N)) * 2 * (d == DBF_F32 ? 3 : 1), 256);
+    return align_up(static_cast<size_t>(T * operand_ld(N)) * 2 * pieces(d), 256);
 }
-
-int pieces(const Gradient &c) { return c.dyd != DBF_F32 ? 1 : c.dxd == DBF_F32 ? 3 : 2; }
 
 struct PdlAttr {
     cudaLaunchAttribute attr[2];
@@ -750,7 +745,7 @@ size_t mx_back_workspace_bytes(int64_t M, int64_t N, int64_t T, dbf_dtype d, int
 
 void mx_back_cut(const Gradient &c, int mats, int sms, int64_t (&cut)[8])
 {
-    const int64_t nk = stages(c.N, mats, pieces(c));
+    const int64_t nk = stages(c.N, mats, pieces(c.dyd));
     const Plan pl = plan(c.M, c.T, nk, sms);
     const int64_t of[8] = {DBF_MX4_GRADIENT, pl.w, pl.w > 256 ? 2 : 1, pl.splits, ring_of(pl.w), nk,
                            (c.M + 255) / 256 * ((c.T + pl.w - 1) / pl.w) * pl.splits, 0};
@@ -760,7 +755,7 @@ void mx_back_cut(const Gradient &c, int mats, int sms, int64_t (&cut)[8])
 cudaError_t mx_backward(const Gradient &c, cudaStream_t s)
 {
     const void *operand[2] = {c.dy, nullptr};
-    const int planes = pieces(c);
+    const int planes = pieces(c.dyd);
     if (direct_operand(c.N, c.dyd)) return product(c, operand, c.N, 1, false, kWsHeaderBytes, s);
     uint16_t *op = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);
     const int64_t ld = operand_ld(c.N);
@@ -784,7 +779,7 @@ cudaError_t mx_gated_backward(const Gradient &c, int act, const dbf_act8 &sg, co
     a.g8 = sg.codes, a.gs = sg.scales, a.u8 = su.codes, a.us = su.scales;
     a.dh = c.dy, a.dg = dg, a.du = du;
     a.T = c.T, a.N = c.N, a.pitch8 = blocks(c.N) * kBlock, a.ld = operand_ld(c.N);
-    a.planes = pieces(c);
+    a.planes = pieces(c.dyd);
     const void *operand[2] = {dg, du};
     if (want && !direct) {
         a.op_g = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(c.ws) + kWsHeaderBytes);

@@ -522,10 +522,9 @@ dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dt
 
 /* Gradient of dbf_mx4_forward for the values it multiplies: dx = [acc] dx +
  * dy W. The rounding of x to q(x) is passed straight through. W is expanded
- * exactly and bf16 gradients are used as they are. fp32 ones are cut into bf16
- * pieces: three that add up to them (parts below 2^-133 are lost) for an fp32
- * dx, two (off by at most 2^-16 of a value) for a bf16 dx. Products are exact
- * and sums fp32.
+ * exactly and bf16 gradients are used as they are; fp32 ones are cut into three
+ * bf16 pieces that add up to them (parts below 2^-133 are lost), so products
+ * are exact and sums fp32.
  * dy: T x N and dx: T x M, DBF_F32 or DBF_BF16, 16-byte aligned, not
  *    overlapping. flags: DBF_ACCUMULATE | DBF_WEIGHTS_STATIC.
  * ws: dbf_mx4_backward_workspace_bytes(L, T, dy_dtype) bytes, 256-byte
@@ -605,7 +604,7 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
  * M, N (or two of it) and T tokens. Host only, for tests: no pointer is read.
  * call: which one; DBF_MX4_GATED_ADD is the gated forward with addends,
  *    DBF_MX4_GATED_SAVE the one that keeps g and u.
- * dy_dtype, dx_dtype: of the gradients (DBF_F32 or DBF_BF16), else not used.
+ * dy_dtype: of the gradient (DBF_F32 or DBF_BF16), else not used.
  * cut[0] the kernel: DBF_MX4_FEW_TOKENS, DBF_MX4_MANY_TOKENS, DBF_MX4_GRADIENT
  * cut[1] tokens of a tile
  * cut[2] few: CTAs of a cluster; many and gradient: accumulators of a set
@@ -626,8 +625,7 @@ typedef enum {
     DBF_MX4_GATED_BACKWARD = 5
 } dbf_mx4_call;
 enum { DBF_MX4_FEW_TOKENS = 0, DBF_MX4_MANY_TOKENS = 1, DBF_MX4_GRADIENT = 2 };
-dbf_status dbf_debug_mx4_cut(dbf_mx4_call call, int32_t M, int32_t N, int64_t T, dbf_dtype dy_dtype, dbf_dtype dx_dtype,
-                             int32_t sms, int64_t *cut);
+dbf_status dbf_debug_mx4_cut(dbf_mx4_call call, int32_t M, int32_t N, int64_t T, dbf_dtype dy_dtype, int32_t sms, int64_t *cut);
 
 /* Static description of a status code. */
 const char *dbf_status_string(dbf_status s);

@@ -16,10 +16,10 @@ def dbf():
     return m
 
 
-def cut(dbf, call, M, N, T, dy=None, dx=None, sms=SMS):
+def cut(dbf, call, M, N, T, dy=None, sms=SMS):
     """The cut as a list, or the status that refused it."""
     out = (ctypes.c_int64 * 8)()
-    st = dbf._lib.dbf_debug_mx4_cut(call, M, N, T, dbf.F32 if dy is None else dy, dbf.F32 if dx is None else dx, sms, out)
+    st = dbf._lib.dbf_debug_mx4_cut(call, M, N, T, dbf.F32 if dy is None else dy, sms, out)
     return list(out) if st == dbf.OK else st
 
 
@@ -27,7 +27,7 @@ def test_refusals(dbf):
     assert cut(dbf, 6, 64, 64, 4) == cut(dbf, -1, 64, 64, 4) == cut(dbf, FORWARD, 0, 64, 4) == cut(dbf, FORWARD, 64, 64, 0) == dbf.ERR_INVALID_ARG
     assert cut(dbf, FORWARD, 64, 64, 4, sms=0) == cut(dbf, BACKWARD, 64, 64, 4, dy=dbf.F16) == dbf.ERR_INVALID_ARG
     assert cut(dbf, FORWARD, 64, 64, 1 << 40) == cut(dbf, BACKWARD, 64, 64, 1 << 30) == dbf.ERR_UNSUPPORTED
-    assert dbf._lib.dbf_debug_mx4_cut(FORWARD, 64, 64, 4, 0, 0, SMS, None) == dbf.ERR_INVALID_ARG
+    assert dbf._lib.dbf_debug_mx4_cut(FORWARD, 64, 64, 4, 0, SMS, None) == dbf.ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("call", [FORWARD, GATED, GATED_ADD, GATED_SAVE])
