@@ -12,7 +12,11 @@
 // operands as they are; fp32 ones are cut into three bf16 pieces of eight bits
 // (v = p0 + p1 + p2 exactly), three times the products, whatever dx's type: what
 // two pieces leave of a value, 2^-16 of it, is not small beside a dx whose terms
-// cancel.
+// cancel. The smallest pieces of all weights are summed first: the tensor cores
+// truncate their fp32 sums, and a small piece's terms added to the large ones' sum
+// are cut off at its last place, each time towards zero (4096 -> 11008 at 2048
+// tokens, normal data: dx off by 4.7e-5 with the smallest last, 6.3e-7 so; a
+// plain fp32 product by 1.8e-6).
 //
 // A CTA pair owns 256 columns of W x w <= 512 tokens of dx, over 256 tokens as
 // two accumulators (an expanded stage feeds two MMAs a step), contraction over
@@ -115,6 +119,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// The products that are summed, small pieces first, the weights in turn.
+__device__ __forceinline__ int weight_of(const Args &g, int seg) { return g.mats == 2 ? seg & 1 : 0; }
+__device__ __forceinline__ int piece_of(const Args &g, int seg) { return g.planes - 1 - (g.mats == 2 ? seg >> 1 : seg); }
+
 // Tiles (256 columns of W x w tokens, a part of the contraction) in column
 // order, so that pairs that run together share the gradient's rows.
 struct Tile {
@@ -180,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
             for (int k = c.k0; k < c.k1; ++k) {
                 ok = warp_wait(&sh->empty[s], ph ^ 1u, abort);
                 if (!ok) break;
-                const CUtensorMap *map = seg < g.planes ? &mB0 : &mB1;
-                const int row = tok + static_cast<int>(seg % g.planes * g.plane_rows);
+                const CUtensorMap *map = weight_of(g, seg) ? &mB1 : &mB0;
+                const int row = tok + static_cast<int>(piece_of(g, seg) * g.plane_rows);
                 uint8_t *st = stage0 + s * stage_size + kABytes;
                 if (elect_one()) {
                     if (rank == 0) bar_expect_tx(&sh->full[s], g.w * kRowsK * 2);
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_back_kernel(const __grid_const
                 c = tile_of(g, tile < g.tiles ? tile : unit, nk);
                 k += c.k0;
             }
-            const int at = min(k, nk - 1), seg = at / g.nn, m = seg < g.planes ? 0 : 1, i = at - seg * g.nn, n = i * kRowsK + r;
+            const int at = min(k, nk - 1), seg = at / g.nn, m = weight_of(g, seg), i = at - seg * g.nn, n = i * kRowsK + r;
             const int block = c.p * 8 + static_cast<int>(rank) * 4 + q;
             steps = (min(g.nn - i, c.k1 - at) + kGroups - 1) / kGroups;
             k += steps * kGroups;
