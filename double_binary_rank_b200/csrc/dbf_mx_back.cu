@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float value;
-                    const float slope = gate_slope(kAct, p[j] * sg, value);
+                    const float slope = gate_slope<DT == DBF_F32>(kAct, p[j] * sg, value);
                     g[4 * h + j] = dh[4 * h + j] * (q[j] * su) * slope;
                     u[4 * h + j] = dh[4 * h + j] * value;
                 }

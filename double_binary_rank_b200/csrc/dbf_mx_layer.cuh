@@ -29,27 +29,35 @@ struct Epilogue {
 // s (1 + g (1 - s)). GELU in its tanh form: with z = c (g + 0.044715 g^3) and
 // c = sqrt(2 / pi), g / 2 (1 + tanh z) = g s with s = 1 / (1 + e^-2z),
 // derivative s + g s (1 - s) 2 c (1 + 3 * 0.044715 g^2). e^-g overflows to
-// infinity and its reciprocal is 0, as the limit is; both approximations are
-// off by an ulp or two of fp32.
+// infinity and its reciprocal is 0, as the limit is.
+// The reciprocal is off by a unit of fp32 (2^-23 of it) at most; below 2^-126 it
+// is 0. kExact, for results that stay fp32: expf, off by two units. Results that
+// are rounded to bf16 (2^-8 of a value) take __expf, off by 2 + 1.173 |z| units of
+// e^-z, at most 2^-16 where s is not 0: with expf for them too the plain gate took
+// 85.6 us, 80.3 us so (2 x (4096 -> 11008) at 2048 tokens); fp32 results 89 us
+// either way. A division instead of the reciprocal took fp32 results to 130 us.
 constexpr float kGelu2c = 1.5957691216057308f, kGeluCube = 0.044715f;
+template <bool kExact>
 __device__ __forceinline__ float sigmoid(float g)
 {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + (kExact ? expf(-g) : __expf(-g))));
     return r;
 }
+template <bool kExact>
 __device__ __forceinline__ float gate_value(int act, float g)
 {
-    return g * sigmoid(act == DBF_GATE_SILU ? g : kGelu2c * (g + kGeluCube * g * g * g));
+    return g * sigmoid<kExact>(act == DBF_GATE_SILU ? g : kGelu2c * (g + kGeluCube * g * g * g));
 }
+template <bool kExact>
 __device__ __forceinline__ float gate_slope(int act, float g, float &value)
 {
     if (act == DBF_GATE_SILU) {
-        const float s = sigmoid(g);
+        const float s = sigmoid<kExact>(g);
         value = g * s;
         return s * (1.0f + g * (1.0f - s));
     }
-    const float s = sigmoid(kGelu2c * (g + kGeluCube * g * g * g));
+    const float s = sigmoid<kExact>(kGelu2c * (g + kGeluCube * g * g * g));
     const float d = s * (1.0f - s);
     value = g * s;
     return d == 0.0f ? s : s + g * d * kGelu2c * (1.0f + 3.0f * kGeluCube * g * g);   // d == 0: g * g may be infinite
@@ -112,8 +120,13 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue &e, int64_t t, in
             keep8(e.g8, e.gs, e.pitch8, e.T, t, c, on, g);
             keep8(e.u8, e.us, e.pitch8, e.T, t, c, on, u);
         }
+        if (e.yd == DBF_F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = gate_value(e.act, g[i]) * u[i];
+            for (int i = 0; i < 8; ++i) g[i] = gate_value<true>(e.act, g[i]) * u[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = gate_value<false>(e.act, g[i]) * u[i];
+        }
     }
     if (on) store8(e.y, e.yd, t * N, c, N, vec, v[0]);
 }
@@ -182,19 +195,20 @@ __device__ __forceinline__ void store_column(const Epilogue &e, int64_t t0, int 
 {
     const int left = n < e.N ? static_cast<int>(e.T - t0 < 16 ? e.T - t0 : 16) : 0;
     const int64_t at = t0 * e.N + n, step = e.N;
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = kMats == 2 ? gate_value(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
     if (e.yd == DBF_F32) {
         float *p = static_cast<float *>(e.y) + at;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < left) p[j * step] = y[j];
+        for (int j = 0; j < 16; ++j) {
+            const float y = kMats == 2 ? gate_value<true>(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
+            if (j < left) p[j * step] = y;
+        }
     } else {
         __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(e.y) + at;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < left) p[j * step] = __float2bfloat16_rn(y[j]);
+        for (int j = 0; j < 16; ++j) {
+            const float y = kMats == 2 ? gate_value<false>(kAct, v[0][j]) * v[kMats - 1][j] : v[0][j];
+            if (j < left) p[j * step] = __float2bfloat16_rn(y);
+        }
     }
 }
 // n0: the warp's first column; own: kTurnFloats words; slot: which column the
@@ -213,8 +227,8 @@ __device__ __forceinline__ void simple_finish(const Epilogue &e, uint32_t *own, 
     for (int p = 0; p < 8; ++p) {
         float a = v[0][2 * p], b = v[0][2 * p + 1];
         if (kMats == 2) {
-            a = gate_value(kAct, a) * v[kMats - 1][2 * p];
-            b = gate_value(kAct, b) * v[kMats - 1][2 * p + 1];
+            a = gate_value<false>(kAct, a) * v[kMats - 1][2 * p];
+            b = gate_value<false>(kAct, b) * v[kMats - 1][2 * p + 1];
         }
         const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
         own[p * 36 + slot] = *reinterpret_cast<const uint32_t *>(&w);
@@ -335,7 +349,7 @@ __device__ __forceinline__ void gated_finish(const Epilogue &e, int64_t t, int c
     for (int i = 0; i < 2; ++i) {
         float h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = gate_value(kAct, r[0][8 * i + j]) * r[1][8 * i + j];
+        for (int j = 0; j < 8; ++j) h[j] = gate_value<false>(kAct, r[0][8 * i + j]) * r[1][8 * i + j];
         store8(e.y, DBF_BF16, t * e.N, c + 16 * i, e.N, true, h);
     }
 }
