@@ -109,53 +109,9 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t w, float (&v)[4])
     }
 }
 
-// Eight consecutive values of row p[0 .. k) from column c (a multiple of 8);
-// columns at or past k read as zero. vec: every row starts 16-byte aligned
-// and k is a multiple of 8, so the eight are one or two aligned vectors.
-__device__ __forceinline__ void load8(const void *src, dbf_dtype dt, int64_t row_start, int64_t c, int64_t k, bool vec,
-                                      float (&v)[8])
-{
-    if (c >= k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        return;
-    }
-    const int64_t at = row_start + c;
-    if (vec) {
-        if (dt == DBF_F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
-            const float4 a = p[0], b = p[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at);
-            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (dt == DBF_BF16) {
-                    v[2 * i] = __uint_as_float(q[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-                } else {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&q[i]));
-                    v[2 * i] = f.x;
-                    v[2 * i + 1] = f.y;
-                }
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (c + i >= k)
-            v[i] = 0.0f;
-        else if (dt == DBF_F16)
-            v[i] = h2f(static_cast<const uint16_t *>(src)[at + i]);
-        else
-            v[i] = load_act(src, dt, at + i);
-    }
-}
-
-// The reverse: eight values to columns c .. c + 7 of a row, those at or past k
-// left out.
+// Eight values to columns c .. c + 7 of a row, those at or past k left out; c is
+// a multiple of 8. vec: every row starts 16-byte aligned and k is a multiple of
+// 8, so the eight are one or two aligned vectors; else fp32 or bf16.
 __device__ __forceinline__ void store8(void *dst, dbf_dtype dt, int64_t row_start, int64_t c, int64_t k, bool vec,
                                        const float (&v)[8])
 {
@@ -185,15 +141,13 @@ __device__ __forceinline__ void store8(void *dst, dbf_dtype dt, int64_t row_star
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (c + i >= k) break;
-        if (dt == DBF_F16)
-            static_cast<__half *>(dst)[at + i] = __float2half_rn(v[i]);
-        else
-            store_act(dst, dt, at + i, v[i]);
+        store_act(dst, dt, at + i, v[i]);
     }
 }
 
 // Eight values as loaded, so that the load can be issued long before its
-// conversion: 16-bit types in 'lo', fp32 (and all types without 'vec') in both.
+// conversion: 16-bit types in 'lo', fp32 (and what is loaded without 'vec') in
+// both. vec and columns past k as in store8; those read as zero.
 struct Raw8 {
     uint4 lo, hi;
 };
@@ -213,15 +167,17 @@ __device__ __forceinline__ Raw8 load_raw8(const void *src, dbf_dtype dt, int64_t
         return r;
     }
     float v[8];
-    load8(src, dt, row_start, c, k, false, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < k ? load_act(src, dt, at + i) : 0.0f;
     r.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     r.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     return r;
 }
-__device__ __forceinline__ void raw8_values(const Raw8 &r, dbf_dtype dt, bool vec, float (&v)[8])
+// The values of what was loaded as vectors
+__device__ __forceinline__ void raw8_values(const Raw8 &r, dbf_dtype dt, float (&v)[8])
 {
     const uint32_t a[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
-    if (dt == DBF_F32 || !vec) {
+    if (dt == DBF_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]);
         return;
@@ -449,7 +405,7 @@ __device__ __forceinline__ uint32_t block_amax_bits(const Raw8 (&r)[kCols / 8])
 {
     if (DT == DBF_F32) {
         float v[8];
-        raw8_values(r[0], DBF_F32, true, v);
+        raw8_values(r[0], DBF_F32, v);
         return block_amax(amax_bits8(v));
     }
     uint32_t m = 0;
@@ -484,7 +440,7 @@ __device__ __forceinline__ void scaled_values(const Raw8 &r, uint32_t byte, floa
         return;
     }
     const float inv = inv_scale(byte);
-    raw8_values(r, DT, true, v);
+    raw8_values(r, DT, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
 }

@@ -467,10 +467,10 @@ __global__ void __launch_bounds__(256) planes_kernel(const void *__restrict__ dy
     if (c >= ld) return;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += static_cast<int64_t>(gridDim.x) * 8) {
         float v[8];
-        const Raw8 in = vec             ? load_raw8(dy, dt, t * N, c, N, true)
+        const Raw8 in = vec             ? load_raw8(dy, DBF_F32, t * N, c, N, true)   // bf16 rows of whole vectors are operands
                         : dt == DBF_F32 ? load_shifted8<DBF_F32>(dy, t * N, c, N, T * N)
                                         : load_shifted8<DBF_BF16>(dy, t * N, c, N, T * N);
-        raw8_values(in, dt, true, v);
+        raw8_values(in, dt, v);
         store_planes(op, ld, T * ld, t, c, planes, v);
     }
     griddep_launch();   // at the end: the product's CTAs would take this kernel's registers
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const
             if (8 * i >= left) break;
             const int64_t t = row + 8 * i;
             float dh[8], g[8], u[8];
-            raw8_values(in[i], DT, true, dh);
+            raw8_values(in[i], DT, dh);
             const float sg = scale_value(sc[0][lane >> 2][8 * i + warp]), su = scale_value(sc[1][lane >> 2][8 * i + warp]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -559,9 +559,10 @@ __global__ void __launch_bounds__(256, kOperands ? 2 : 3) gate_back_kernel(const
 template <dbf_dtype DT, bool kVec>
 auto gate_back(bool operands, int act)
 {
+    constexpr bool kCan = DT == DBF_F32 || !kVec;   // bf16 rows of whole vectors are operands themselves
     if (act == DBF_GATE_SILU)
-        return operands ? gate_back_kernel<DT, kVec, true, DBF_GATE_SILU> : gate_back_kernel<DT, kVec, false, DBF_GATE_SILU>;
-    return operands ? gate_back_kernel<DT, kVec, true, DBF_GATE_GELU> : gate_back_kernel<DT, kVec, false, DBF_GATE_GELU>;
+        return operands ? gate_back_kernel<DT, kVec, kCan, DBF_GATE_SILU> : gate_back_kernel<DT, kVec, false, DBF_GATE_SILU>;
+    return operands ? gate_back_kernel<DT, kVec, kCan, DBF_GATE_GELU> : gate_back_kernel<DT, kVec, false, DBF_GATE_GELU>;
 }
 
 // dx = [acc] dx + the parts' sums, in order.
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
         epilogue_reads<false>(e, t, static_cast<int>(c), c < N, x);
         float v[1][8] = {};
         for (int s = 0; s < splits; ++s) {
-            const Raw8 r = load_raw8(partial + s * plane, DBF_F32, t * N, c, N, vec);
-            add_raw8(r, DBF_F32, vec, v[0]);
+            const Raw8 r = load_raw8(partial + s * plane, DBF_F32, t * N, c, N, true);
+            add_raw8(r, DBF_F32, true, v[0]);
         }
         epilogue_finish<false>(e, t, static_cast<int>(c), c < N, x, v);
     }

@@ -356,7 +356,7 @@ cudaError_t mx_decode(const Product &c, cudaStream_t s)
     g.M = c.M;
     g.x = c.x;
     g.xd = c.xd;
-    g.vec = c.M % 8 == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+    g.vec = c.M % 8 == 0;   // x is 16-byte aligned
     g.early = p.pre || (c.flags & DBF_WEIGHTS_STATIC) ? 1 : 0;
     g.tmem_cols = static_cast<uint32_t>(p.tmem_cols);
     g.ep = c.ep;
