@@ -53,10 +53,36 @@ size_t product_workspace(const dbf_mx4_layer *L, int64_t T)
     return layer_shape_ok(L) && tokens_ok(L, T) ? mx::product_workspace_bytes(L->M, T) : 0;
 }
 
+// Whether two T x cols matrices share memory: tiles of an output are written while
+// other tiles' inputs are still read.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+Span span(const void *p, dbf_dtype d, int64_t T, int64_t cols) { return {p, T * cols * static_cast<int64_t>(size_of(d))}; }
+bool meet(const Span &a, const Span &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+// Whether one of the first 'outs' of them shares memory with any other
+template <size_t n>
+bool any_meet(const Span (&s)[n], size_t outs)
+{
+    for (size_t i = 0; i < outs; ++i)
+        for (size_t j = i + 1; j < n; ++j)
+            if (meet(s[i], s[j])) return true;
+    return false;
+}
+
 dbf_status run(const mx::Product &c, size_t need, size_t ws_bytes, cudaStream_t s)
 {
     if (!c.ws || ws_bytes < need) return DBF_ERR_WORKSPACE;
     if (!aligned(c.ws, 256)) return DBF_ERR_ALIGNMENT;
+    const Span x = span(c.x, c.xd, c.T, c.M), y = span(c.ep.y, c.ep.yd, c.T, c.N);
+    const int64_t codes = c.T * c.ep.pitch8, scales = c.T * mx::blocks(c.N);
+    const Span all[] = {y, {c.ep.g8, codes}, {c.ep.gs, scales}, {c.ep.u8, codes}, {c.ep.us, scales}, x};
+    if (any_meet(all, 5)) return DBF_ERR_INVALID_ARG;
     return from_cuda(mx_decode_fits(c.M, c.N, c.T, c.mats) ? mx_decode(c, s) : mx_gemm(c, s));
 }
 
@@ -212,6 +238,7 @@ dbf_status dbf_mx4_backward(const dbf_mx4_layer *L, const void *dy, dbf_dtype dy
     if (!aligned(dy, 16) || !aligned(dx, 16)) return DBF_ERR_ALIGNMENT;
     if (!ws || ws_bytes < mx_back_workspace_bytes(L->M, L->N, T, dy_dtype, 1)) return DBF_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return DBF_ERR_ALIGNMENT;
+    if (meet(span(dy, dy_dtype, T, L->N), span(dx, dx_dtype, T, L->M))) return DBF_ERR_INVALID_ARG;
     mx::Gradient c = {};
     c.M = L->M, c.N = L->N, c.T = T;
     c.codes[0] = L->codes, c.scales[0] = L->scales;
@@ -254,6 +281,9 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
         c.codes[1] = up->codes, c.scales[1] = up->scales;
         c.ws = ws;
     }
+    const Span all[] = {span(dg, dh_dtype, T, gate->N), span(du, dh_dtype, T, gate->N), span(dx, dx_dtype, T, gate->M),
+                        span(dh, dh_dtype, T, gate->N)};
+    if (any_meet(all, 3)) return DBF_ERR_INVALID_ARG;
     return from_cuda(mx_gated_backward(c, act, *saved_g, *saved_u, dg, du, static_cast<cudaStream_t>(stream)));
 }
 

@@ -516,7 +516,8 @@ size_t dbf_mx4_workspace_bytes(const dbf_mx4_layer *L, int64_t T);
  * ws: dbf_mx4_workspace_bytes(L, T) bytes, 256-byte aligned, header as in
  *    dbf_forward. T == 0 is a no-op. Errors: DBF_ERR_INVALID_ARG,
  *    DBF_ERR_ALIGNMENT, DBF_ERR_WORKSPACE, DBF_ERR_UNSUPPORTED (sizes whose
- *    tiles 32 bits cannot count), DBF_ERR_CUDA. */
+ *    tiles 32 bits cannot count), DBF_ERR_CUDA. DBF_ERR_INVALID_ARG also for an
+ *    x and a y that share memory. */
 dbf_status dbf_mx4_forward(const dbf_mx4_layer *L, const void *x, dbf_dtype x_dtype, void *y, dbf_dtype y_dtype, int64_t T,
                            int flags, void *ws, size_t ws_bytes, void *stream);
 
@@ -576,9 +577,13 @@ size_t dbf_mx4_gated_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_la
  * h: T x N, DBF_F32 or DBF_BF16. save_g, save_u: both or neither; g and u
  *    (addends included, from their fp32 values) are kept there in 8 bits
  *    (T x N) for dbf_mx4_gated_backward.
+ *    What is written overlaps nothing else, except that h may be an addend of
+ *    its own type.
  * flags: DBF_WEIGHTS_STATIC or 0. All pointers 16-byte aligned.
  * ws: dbf_mx4_gated_workspace_bytes(gate, up, T) bytes, 256-byte aligned,
- *    header as in dbf_forward. Errors as dbf_mx4_forward. */
+ *    header as in dbf_forward. T == 0 is a no-op. Errors as dbf_mx4_forward;
+ *    DBF_ERR_INVALID_ARG also for outputs that share memory with x or one
+ *    another. */
 dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const void *x,
                                  dbf_dtype x_dtype, const void *g_add, const void *u_add, dbf_dtype add_dtype, void *h,
                                  dbf_dtype h_dtype, const dbf_act8 *save_g, const dbf_act8 *save_u, int64_t T, int flags,
@@ -592,11 +597,12 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
  * dy (dbf_backward). dx NULL: only dg and du; the layers' codes and scales are
  * not read then and ws may be NULL.
  * saved_g, saved_u: T x N. dh, dg, du: T x N, DBF_F32 or DBF_BF16; all
- *    16-byte aligned; dg and du overlap neither each other nor dh.
+ *    16-byte aligned; dg, du and dx overlap neither one another nor the inputs.
  * flags: DBF_ACCUMULATE (dx) | DBF_WEIGHTS_STATIC.
  * ws: dbf_mx4_gated_backward_workspace_bytes(gate, up, T, dh_dtype) bytes,
  *    256-byte aligned, header as in dbf_forward. T == 0 is a no-op. Errors as
- *    dbf_mx4_backward. */
+ *    dbf_mx4_backward; DBF_ERR_INVALID_ARG also for gradients that share memory
+ *    with dh or one another. */
 size_t dbf_mx4_gated_backward_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T, dbf_dtype dh_dtype);
 dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const dbf_act8 *saved_g,
                                   const dbf_act8 *saved_u, const void *dh, dbf_dtype dh_dtype, void *dg, void *du, void *dx,

@@ -279,3 +279,23 @@ def test_few_tokens_quantised_ahead_follow_what_was_enqueued(dbf, T, M, N, gated
     for i, y in enumerate(outs):
         assert torch.equal(y, want[i % 2][i // 2 % 2])
     assert dbf.workspace_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("T,M,N", [(3, 64, 96), (16, 520, 73), (70, 300, 264), (70, 300, 261), (2100, 264, 3000), (4100, 64, 1000)])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kept", [False, True])
+def test_h_in_the_place_of_an_addend(dbf, T, M, N, kind, kept):
+    rng = np.random.default_rng(T)
+    gl, ul = (quantized(dbf, codes(rng, N, M) / 64) for _ in range(2))
+    x = codes(rng, T, M).to(torch.bfloat16)
+    add = [torch.randn(T, N, device="cuda", generator=torch.Generator("cuda").manual_seed(i)).to(kind) for i in (1, 2)]
+    save = (lambda: (dbf.Act8.empty(T, N, "cuda"), dbf.Act8.empty(T, N, "cuda"))) if kept else (lambda: None)
+    first = save()
+    want = dbf.mx4_gated_forward(gl, ul, x, g_add=add[0], u_add=add[1], h_dtype=kind, save=first)
+    for i in range(2):
+        a = [t.clone() for t in add]
+        again = save()
+        h = dbf.mx4_gated_forward(gl, ul, x, g_add=a[0], u_add=a[1], h=a[i], save=again)
+        assert h is a[i] and torch.equal(h, want) and torch.equal(a[1 - i], add[1 - i])
+        assert not kept or all(torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) for p, q in zip(first, again))
