@@ -25,8 +25,9 @@
 // The token width w is chosen per call (a multiple of 16 up to 224, what 512
 // tensor-memory columns hold beside two buffers of 32 of scales) so that the
 // tiles fill whole waves of pairs; narrower tiles, whose stages take less time
-// than scales need to get there, have up to four buffers. 8192^3 takes 216 us: 31
-// of the pre-pass, 156 of the products and 26 of epilogues. Every wait is bounded;
+// than scales need to get there, have up to four buffers. 8192^3 takes 219 us
+// in short graphs: 31 of the pre-pass, 156 of the products and 26 of epilogues
+// (255 us call after call, at the clocks of the power cap). Every wait is bounded;
 // on expiry the status word is set.
 #include <algorithm>
 #include <atomic>
