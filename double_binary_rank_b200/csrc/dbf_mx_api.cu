@@ -281,9 +281,10 @@ dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer
         c.codes[1] = up->codes, c.scales[1] = up->scales;
         c.ws = ws;
     }
-    const Span all[] = {span(dg, dh_dtype, T, gate->N), span(du, dh_dtype, T, gate->N), span(dx, dx_dtype, T, gate->M),
-                        span(dh, dh_dtype, T, gate->N)};
-    if (any_meet(all, 3)) return DBF_ERR_INVALID_ARG;
+    // dx may lie over dh: the launch that reads dh ends before one writes dx
+    const Span g = span(dg, dh_dtype, T, gate->N), u = span(du, dh_dtype, T, gate->N);
+    const Span by_gate[] = {g, u, span(dh, dh_dtype, T, gate->N)}, by_product[] = {g, u, span(dx, dx_dtype, T, gate->M)};
+    if (any_meet(by_gate, 2) || any_meet(by_product, 2)) return DBF_ERR_INVALID_ARG;
     return from_cuda(mx_gated_backward(c, act, *saved_g, *saved_u, dg, du, static_cast<cudaStream_t>(stream)));
 }
 

@@ -597,12 +597,13 @@ dbf_status dbf_mx4_gated_forward(const dbf_mx4_layer *gate, const dbf_mx4_layer 
  * dy (dbf_backward). dx NULL: only dg and du; the layers' codes and scales are
  * not read then and ws may be NULL.
  * saved_g, saved_u: T x N. dh, dg, du: T x N, DBF_F32 or DBF_BF16; all
- *    16-byte aligned; dg, du and dx overlap neither one another nor the inputs.
+ *    16-byte aligned; dg, du and dx overlap neither one another nor the inputs,
+ *    except that dx may lie over dh.
  * flags: DBF_ACCUMULATE (dx) | DBF_WEIGHTS_STATIC.
  * ws: dbf_mx4_gated_backward_workspace_bytes(gate, up, T, dh_dtype) bytes,
  *    256-byte aligned, header as in dbf_forward. T == 0 is a no-op. Errors as
- *    dbf_mx4_backward; DBF_ERR_INVALID_ARG also for gradients that share memory
- *    with dh or one another. */
+ *    dbf_mx4_backward; DBF_ERR_INVALID_ARG also for dg, du and dx that share
+ *    memory with one another, and dg and du with dh. */
 size_t dbf_mx4_gated_backward_workspace_bytes(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, int64_t T, dbf_dtype dh_dtype);
 dbf_status dbf_mx4_gated_backward(const dbf_mx4_layer *gate, const dbf_mx4_layer *up, dbf_gate act, const dbf_act8 *saved_g,
                                   const dbf_act8 *saved_u, const void *dh, dbf_dtype dh_dtype, void *dg, void *du, void *dx,

@@ -53,5 +53,5 @@ def test_gated_backward(dbf):
         a = by(dbf.DbfAct8C(c, s))   # one of both is read twice, which is fine
         return dbf._lib.dbf_mx4_gated_backward(by(L), by(L), 0, a, a, dh, dbf.F32, dg, du, dx, dbf.F32, T, 0, ws, need, None)
 
-    assert call(dg=du) == call(dg=dh) == call(du=dh) == call(dx=dg) == call(dx=du) == call(dx=dh) == dbf.ERR_INVALID_ARG
+    assert call(dg=du) == call(dg=dh) == call(du=dh) == call(dx=dg) == call(dx=du) == dbf.ERR_INVALID_ARG
     assert call(dg=dh + 16) == call(dg=dh, dx=None) == dbf.ERR_INVALID_ARG

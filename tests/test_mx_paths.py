@@ -299,3 +299,20 @@ def test_h_in_the_place_of_an_addend(dbf, T, M, N, kind, kept):
         h = dbf.mx4_gated_forward(gl, ul, x, g_add=a[0], u_add=a[1], h=a[i], save=again)
         assert h is a[i] and torch.equal(h, want) and torch.equal(a[1 - i], add[1 - i])
         assert not kept or all(torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) for p, q in zip(first, again))
+
+
+@gpu
+@pytest.mark.parametrize("T,N", [(1, 64), (33, 95), (600, 520), (2050, 1032)])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_dx_in_the_place_of_dh(dbf, T, N, kind):
+    """dh is read before dx is written, also where the contraction is in parts and where dx is added to what dh was."""
+    rng = np.random.default_rng(T)
+    gl, ul = (quantized(dbf, codes(rng, N, N)) for _ in range(2))
+    r = torch.Generator("cuda").manual_seed(T)
+    saved = tuple(dbf.act8_save(torch.randn(T, N, device="cuda", generator=r)) for _ in range(2))
+    dh = torch.randn(T, N, device="cuda", generator=r).to(kind)
+    for accumulate in (False, True):
+        want = dbf.mx4_gated_backward(gl, ul, dh, saved, dx=dh.clone(), accumulate=accumulate)
+        here = dh.clone()
+        got = dbf.mx4_gated_backward(gl, ul, here, saved, dx=here, accumulate=accumulate)
+        assert got[0] is here and all(torch.equal(a, b) for a, b in zip(got, want))
